@@ -529,6 +529,156 @@ int32_t kvarn_affine_decode(const void* q, int32_t num_q_heads, float sm_scale, 
                             kvarn_stream_t stream);
 
 /*
+ * kvarn_decode_mass - kvarn_decode that also says how much attention every
+ * committed tile drew, for evicting the tiles that draw least. (The pages
+ * describing the method have no counterpart of this call.)
+ *
+ * mass_out[b][t] = decay * mass_in[b][t] + the softmax weights of the tokens
+ * of tile t, summed over the tokens and over the query heads, for the
+ * committed tiles t < seq_lens[b] / N, and 0 for the other t < max_seq_len /
+ * N. With decay = 1 the masses accumulate over the steps; the weights of one
+ * step add up to at most num_q_heads (the raw tail has the rest). A tile is
+ * the unit because its column scales are spread over its pages: only whole
+ * tiles can leave a cache.
+ *
+ *   mass_in, mass_out  device fp32, row b at b * mass_stride; may be the same
+ *   mass_stride        >= max_seq_len / N
+ *   decay              in [0, 1]
+ *   workspace          >= kvarn_decode_mass_workspace_bytes(...)
+ * Other arguments and results as kvarn_decode; out and lse are bit for bit
+ * those of kvarn_decode. The sums are taken in a fixed order: the same call
+ * gives the same masses. num_seqs is at most 65535.
+ */
+int64_t kvarn_decode_mass_workspace_bytes(const kvarn_layout* layout, int32_t num_seqs, int32_t num_q_heads,
+                                          int32_t max_seq_len);
+
+int32_t kvarn_decode_mass(const void* q, int32_t num_q_heads, float sm_scale, const void* cache,
+                          const kvarn_layout* layout, const int32_t* block_table, int32_t bt_stride,
+                          const int32_t* seq_lens, int32_t max_seq_len, const void* tail_k, const void* tail_v,
+                          int32_t num_seqs, float* out, float* lse, const float* mass_in, float* mass_out,
+                          int32_t mass_stride, float decay, void* workspace, int64_t workspace_bytes,
+                          uint32_t* error_flags, kvarn_stream_t stream);
+
+/*
+ * kvarn_evict_tiles - shorten sequences to a budget of tiles by dropping the
+ * tiles of least mass (kvarn_decode_mass). (The pages describing the method
+ * have no counterpart of this call.)
+ *
+ * A sequence with C = seq_lens[b] / N committed tiles, C > keep_tiles, keeps
+ * its first sink_tiles tiles, its newest recent_tiles tiles, and of the tiles
+ * between them those of the largest mass up to keep_tiles in all; of equal
+ * masses the earlier tile stays (-0 equals 0; a NaN is below every number).
+ * The kept tiles move to logical tiles 0.. in their order, in the block table
+ * and in the masses, and the sequence is C - kept tiles of N tokens shorter;
+ * its raw tail is untouched and follows the last kept tile. Positions are
+ * not renumbered: keys carry theirs from before they were encoded. A sequence
+ * within the budget is copied as it is.
+ *
+ *   mass_in, mass_out  device fp32, rows mass_stride apart (>= T =
+ *                      max_seq_len / N); mass_out past the kept tiles is 0 up
+ *                      to tile T
+ *   block_table, block_table_out, freed
+ *                      device int32, rows bt_stride apart (>= T * N/P);
+ *                      block_table_out past the kept tiles' pages is -1 up to
+ *                      entry T * N/P
+ *   freed              the dropped tiles' page ids in their order, then -1 up
+ *                      to entry T * N/P; freed_count[b] of them
+ *   seq_lens, seq_lens_out  device int32 [num_seqs]
+ *   keep_tiles         >= sink_tiles + recent_tiles
+ * The outputs may be the inputs (mass_out = mass_in and so on); freed is a
+ * buffer of its own. A length outside [0, max_seq_len] sets
+ * KVARN_DEVERR_SEQ_LEN and is clamped.
+ */
+int32_t kvarn_evict_tiles(const float* mass_in, float* mass_out, int32_t mass_stride, const int32_t* block_table,
+                          int32_t* block_table_out, int32_t* freed, int32_t bt_stride, const int32_t* seq_lens,
+                          int32_t* seq_lens_out, int32_t* freed_count, int32_t max_seq_len, int32_t num_seqs,
+                          const kvarn_layout* layout, int32_t keep_tiles, int32_t sink_tiles, int32_t recent_tiles,
+                          uint32_t* error_flags, kvarn_stream_t stream);
+
+/*
+ * kvarn_decode_shared - kvarn_decode_verify of a batch whose sequences all
+ * begin with the same prefix_tokens tokens, stored once: the prefix's pages
+ * are read once for the whole batch. (The pages describing the method have no
+ * counterpart of this call.)
+ *
+ * Sequence b holds L = seq_lens[b] tokens: the prefix [0, S), S =
+ * prefix_tokens, then its own; the last Q = num_queries are under
+ * verification as in kvarn_decode_verify (Q = 1: plain decode). Logical page
+ * l of the prefix is prefix_table[l]; the sequence's own whole tiles [S, C),
+ * C = floor((L - Q + 1)/N)*N, are read from the pages block_table names, at
+ * the same logical indices as ever (its first S/P entries are not read), and
+ * tokens [C, L) are rows 0.. of the raw tail.
+ *
+ *   prefix_table   device int32 [prefix_tokens / P]
+ *   prefix_tokens  a positive multiple of N
+ *   seq_lens       each 0 (a padding row: out = 0, lse = -inf) or at least
+ *                  S + Q - 1, so that every query sees the whole prefix; any
+ *                  other length sets KVARN_DEVERR_SEQ_LEN
+ *   workspace      >= kvarn_decode_shared_workspace_bytes(...)
+ * Other arguments and results as kvarn_decode_verify. num_seqs * Q *
+ * num_q_heads is at most 2^30.
+ */
+int64_t kvarn_decode_shared_workspace_bytes(const kvarn_layout* layout, int32_t num_seqs, int32_t num_q_heads,
+                                            int32_t num_queries, int32_t max_seq_len, int32_t prefix_tokens);
+
+int32_t kvarn_decode_shared(const void* q, int32_t num_q_heads, int32_t num_queries, float sm_scale,
+                            const void* cache, const kvarn_layout* layout, const int32_t* prefix_table,
+                            int32_t prefix_tokens, const int32_t* block_table, int32_t bt_stride,
+                            const int32_t* seq_lens, int32_t max_seq_len, const void* tail_k, const void* tail_v,
+                            int32_t tail_capacity, int32_t num_seqs, float* out, float* lse, void* workspace,
+                            int64_t workspace_bytes, uint32_t* error_flags, kvarn_stream_t stream);
+
+/*
+ * kvarn_rope - rotary positions of queries and keys, before keys are encoded
+ * or appended and queries decode. (The pages describing the method leave the
+ * positions to the engine.)
+ *
+ * Channels rope_offset + [0, R), R = rope_dim, of every head are turned by
+ * the angles t_i = positions[b][n] * inv_freq[i], i < R/2:
+ *   y_a = scale (x_a cos t_i - x_b sin t_i)
+ *   y_b = scale (x_a sin t_i + x_b cos t_i)
+ * with (a, b) = rope_offset + (i, i + R/2) (interleaved = 0, the half layout)
+ * or rope_offset + (2i, 2i + 1) (interleaved = 1). Other channels are copied
+ * unscaled. inverse = 1 turns by -t_i: the gradient with respect to x given
+ * that with respect to y (and, for scale = 1, the inverse). Frequencies
+ * scaled for long contexts are the caller's table; scale is the factor that
+ * such scalings put on queries and keys. The angle is reduced modulo a turn
+ * in 64-bit fixed point, exact for any position; the arithmetic is fp32, the
+ * result rounded once to the tensors' type.
+ *
+ *   tensors      host array of 1 .. KVARN_ROPE_MAX_TENSORS tensors that share
+ *                positions (queries and keys, in one launch). Element (b, n,
+ *                h, d) is at b*seq_stride + n*token_stride + h*head_stride +
+ *                d (elements). in = out (with equal strides) turns in place;
+ *                otherwise the two must not overlap
+ *   dtype        of every tensor: 0 fp16, 1 bf16, 2 fp32
+ *   positions    device int32, token n of sequence b at b*pos_stride + n (a
+ *                pos_stride of 0: shared by the batch); any value
+ *   inv_freq     device fp64 [R/2], finite
+ *   rope_dim     even, rope_offset + rope_dim <= head_dim
+ * head_dim is at most KVARN_ROPE_MAX_DIM. Tensors whose addresses and strides
+ * are all multiples of 16 bytes, with R/2 and rope_offset multiples of 16
+ * bytes' worth of elements, take the vector path; others one element at a
+ * time.
+ */
+#define KVARN_ROPE_MAX_TENSORS 4
+#define KVARN_ROPE_MAX_DIM 1024
+
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t in_seq_stride, in_token_stride, in_head_stride;
+  int64_t out_seq_stride, out_token_stride, out_head_stride;
+  int32_t num_heads;
+  int32_t head_dim;
+} kvarn_rope_tensor;
+
+int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_t dtype, int32_t num_seqs,
+                   int32_t num_tokens, const int32_t* positions, int64_t pos_stride, const double* inv_freq,
+                   int32_t rope_dim, int32_t rope_offset, int32_t interleaved, float scale, int32_t inverse,
+                   kvarn_stream_t stream);
+
+/*
  * kvarn_set_copy_wait_test - diagnostic of the dense decode kernels'
  * (kvarn_decode, _verify, _window, _fp16, _noalloc, kvarn_affine_decode)
  * bounded waits for their page copies, so that a test can drive the time-out

@@ -272,6 +272,14 @@ static int32_t check_decode_common(const kvarn_layout* L, int32_t num_q_heads,
   return KVARN_OK;
 }
 
+// The tile masses of kvarn_decode_mass.
+struct MassArgs {
+  const float* in;
+  float* out;
+  int32_t stride;
+  float decay;
+};
+
 static int32_t decode_dense_common(const void* q, int32_t num_q_heads, int32_t num_queries, float sm_scale,
                                    const void* cache, const kvarn_layout* L, const int32_t* block_table,
                                    int32_t bt_stride, const int32_t* seq_lens, int32_t max_seq_len,
@@ -279,7 +287,7 @@ static int32_t decode_dense_common(const void* q, int32_t num_q_heads, int32_t n
                                    int32_t sink_tokens, const void* sink_k, const void* sink_v,
                                    int32_t recent_tokens, int32_t num_seqs, float* out, float* lse,
                                    void* workspace, int64_t workspace_bytes, uint32_t* error_flags,
-                                   kvarn_stream_t stream, bool affine = false) {
+                                   kvarn_stream_t stream, bool affine = false, const MassArgs* mass = nullptr) {
   int32_t s = affine ? check_affine(L) : check_dense(L);
   if (s != KVARN_OK) return s;
   s = check_decode_common(L, num_q_heads, block_table, bt_stride, seq_lens, max_seq_len, num_seqs,
@@ -299,7 +307,9 @@ static int32_t decode_dense_common(const void* q, int32_t num_q_heads, int32_t n
   if ((sink_k && !aligned(sink_k, 16)) || (sink_v && !aligned(sink_v, 16))) return KVARN_EALIGN;
   const DensePlan plan = dense_plan(L, num_seqs, num_q_heads, num_queries, accepted,
                                     raw_bound(L, max_seq_len, num_queries, sink_tokens, recent_tokens), affine);
-  if (workspace_bytes < dense_ws(L, num_seqs, num_q_heads, num_queries, plan)) return KVARN_EWORKSPACE;
+  int64_t need = dense_ws(L, num_seqs, num_q_heads, num_queries, plan);
+  if (mass) need += mass_workspace_bytes(static_cast<int64_t>(num_seqs) * num_q_heads, max_seq_len / L->tile_tokens);
+  if (workspace_bytes < need) return KVARN_EWORKSPACE;
   DecodeParams p{};
   p.q = q;
   p.num_q_heads = num_q_heads;
@@ -331,6 +341,12 @@ static int32_t decode_dense_common(const void* q, int32_t num_q_heads, int32_t n
   p.v_bits = L->v_bits;
   p.scale_bytes = affine ? 2 : (L->scale_dtype == 1 ? 2 : 4);
   p.codec = affine ? 1 : 0;
+  if (mass) {
+    p.mass_in = mass->in;
+    p.mass_out = mass->out;
+    p.mass_stride = mass->stride;
+    p.mass_decay = mass->decay;
+  }
   return from_cuda(launch_decode_dense(p, plan, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -566,6 +582,213 @@ int32_t kvarn_affine_decode(const void* q, int32_t num_q_heads, float sm_scale, 
   return decode_dense_common(q, num_q_heads, 1, sm_scale, cache, L, block_table, bt_stride, seq_lens,
                              max_seq_len, tail_k, tail_v, L->tile_tokens, 0, nullptr, nullptr, 0, num_seqs,
                              out, lse, workspace, workspace_bytes, error_flags, stream, true);
+}
+
+int64_t kvarn_decode_mass_workspace_bytes(const kvarn_layout* L, int32_t num_seqs, int32_t num_q_heads,
+                                          int32_t max_seq_len) {
+  if (check_dense(L) != KVARN_OK || num_seqs < 0 || num_q_heads < 1 || max_seq_len < 0 ||
+      num_q_heads % L->num_kv_heads)
+    return -1;
+  const DensePlan plan = dense_plan(L, num_seqs, num_q_heads, 1, max_seq_len, raw_bound(L, max_seq_len, 1, 0, 0));
+  return dense_ws(L, num_seqs, num_q_heads, 1, plan) +
+         mass_workspace_bytes(static_cast<int64_t>(num_seqs) * num_q_heads, max_seq_len / L->tile_tokens);
+}
+
+int32_t kvarn_decode_mass(const void* q, int32_t num_q_heads, float sm_scale, const void* cache,
+                          const kvarn_layout* L, const int32_t* block_table, int32_t bt_stride,
+                          const int32_t* seq_lens, int32_t max_seq_len, const void* tail_k, const void* tail_v,
+                          int32_t num_seqs, float* out, float* lse, const float* mass_in, float* mass_out,
+                          int32_t mass_stride, float decay, void* workspace, int64_t workspace_bytes,
+                          uint32_t* error_flags, kvarn_stream_t stream) {
+  if (!L) return KVARN_EINVAL;
+  const int32_t s = check_dense(L);
+  if (s != KVARN_OK) return s;
+  if (num_seqs > 0) {
+    const int32_t tiles = std::max(0, max_seq_len) / L->tile_tokens;
+    if (tiles > 0 && (!mass_in || !mass_out || mass_stride < tiles)) return KVARN_EINVAL;
+    if (!(decay >= 0.f && decay <= 1.f)) return KVARN_EINVAL;
+    if (!aligned(mass_in, 4) || !aligned(mass_out, 4)) return KVARN_EALIGN;
+    if (num_seqs > 65535) return KVARN_EUNSUPPORTED;
+  }
+  // without a committed tile there is no mass to write
+  const MassArgs m{mass_in, mass_out, mass_stride, decay};
+  return decode_dense_common(q, num_q_heads, 1, sm_scale, cache, L, block_table, bt_stride, seq_lens, max_seq_len,
+                             tail_k, tail_v, L->tile_tokens, 0, nullptr, nullptr, 0, num_seqs, out, lse, workspace,
+                             workspace_bytes, error_flags, stream, false, &m);
+}
+
+// Plan of a decode over a shared prefix (whole tiles) and the tokens past it.
+static SharedPlan shared_plan(const kvarn_layout* L, int32_t num_seqs, int32_t num_q_heads, int32_t num_queries,
+                              int32_t max_seq_len, int32_t prefix_tokens) {
+  const int32_t own = std::max(0, max_seq_len - num_queries + 1 - prefix_tokens);
+  return plan_shared(num_seqs, L->num_kv_heads, num_q_heads / L->num_kv_heads, num_queries,
+                     prefix_tokens / L->tile_tokens, own / L->tile_tokens, L->head_dim, L->tile_tokens,
+                     raw_bound(L, std::max(0, max_seq_len - prefix_tokens), num_queries, 0, 0), L->k_bits, L->v_bits,
+                     L->scale_dtype == 1 ? 2 : 4);
+}
+
+static bool shared_sizes_ok(const kvarn_layout* L, int32_t num_seqs, int32_t num_q_heads, int32_t num_queries,
+                            int32_t max_seq_len, int32_t prefix_tokens) {
+  return num_seqs >= 0 && num_q_heads >= 1 && max_seq_len >= 0 && num_queries >= 1 &&
+         num_queries <= KVARN_MAX_VERIFY_QUERIES && num_q_heads % L->num_kv_heads == 0 && prefix_tokens > 0 &&
+         prefix_tokens % L->tile_tokens == 0 &&
+         static_cast<int64_t>(num_seqs) * num_queries * num_q_heads <= (1 << 30);
+}
+
+int64_t kvarn_decode_shared_workspace_bytes(const kvarn_layout* L, int32_t num_seqs, int32_t num_q_heads,
+                                            int32_t num_queries, int32_t max_seq_len, int32_t prefix_tokens) {
+  if (check_dense(L) != KVARN_OK ||
+      !shared_sizes_ok(L, num_seqs, num_q_heads, num_queries, max_seq_len, prefix_tokens))
+    return -1;
+  return shared_workspace_bytes(static_cast<int64_t>(num_seqs) * num_queries * num_q_heads, L->head_dim,
+                                shared_plan(L, num_seqs, num_q_heads, num_queries, max_seq_len, prefix_tokens));
+}
+
+int32_t kvarn_decode_shared(const void* q, int32_t num_q_heads, int32_t num_queries, float sm_scale,
+                            const void* cache, const kvarn_layout* L, const int32_t* prefix_table,
+                            int32_t prefix_tokens, const int32_t* block_table, int32_t bt_stride,
+                            const int32_t* seq_lens, int32_t max_seq_len, const void* tail_k, const void* tail_v,
+                            int32_t tail_capacity, int32_t num_seqs, float* out, float* lse, void* workspace,
+                            int64_t workspace_bytes, uint32_t* error_flags, kvarn_stream_t stream) {
+  int32_t s = check_dense(L);
+  if (s != KVARN_OK) return s;
+  if (num_queries < 1 || num_queries > KVARN_MAX_VERIFY_QUERIES) return KVARN_EUNSUPPORTED;
+  s = check_decode_common(L, num_q_heads, block_table, bt_stride, seq_lens, max_seq_len, num_seqs, out, workspace,
+                          error_flags);
+  if (s != KVARN_OK || num_seqs == 0) return s;
+  if (!shared_sizes_ok(L, num_seqs, num_q_heads, num_queries, max_seq_len, prefix_tokens)) return KVARN_EINVAL;
+  if (tail_capacity < L->tile_tokens + num_queries - 2 || tail_capacity < 1) return KVARN_EINVAL;
+  if (!q || !cache || !prefix_table) return KVARN_EINVAL;
+  if (num_q_heads / L->num_kv_heads > 8) return KVARN_EUNSUPPORTED;
+  const int32_t committed = std::max(0, max_seq_len - num_queries + 1) / L->tile_tokens * L->tile_tokens;
+  if (committed > prefix_tokens && bt_stride < committed / kPageTokens) return KVARN_EINVAL;
+  if (!aligned(q, 16) || !aligned(cache, 128)) return KVARN_EALIGN;
+  if ((tail_k && !aligned(tail_k, 16)) || (tail_v && !aligned(tail_v, 16))) return KVARN_EALIGN;
+  const SharedPlan plan = shared_plan(L, num_seqs, num_q_heads, num_queries, max_seq_len, prefix_tokens);
+  if (workspace_bytes <
+      shared_workspace_bytes(static_cast<int64_t>(num_seqs) * num_queries * num_q_heads, L->head_dim, plan))
+    return KVARN_EWORKSPACE;
+  DecodeParams p{};
+  p.q = q;
+  p.num_q_heads = num_q_heads;
+  p.sm_scale = sm_scale;
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.D = L->head_dim;
+  p.N = L->tile_tokens;
+  p.num_kv_heads = L->num_kv_heads;
+  p.num_pages = L->num_pages;
+  p.block_table = block_table;
+  p.bt_stride = bt_stride;
+  p.seq_lens = seq_lens;
+  p.max_seq_len = max_seq_len;
+  p.tail_k = tail_k;
+  p.tail_v = tail_v;
+  p.num_seqs = num_seqs;
+  p.out = out;
+  p.lse = lse;
+  p.workspace = workspace;
+  p.err = error_flags;
+  p.bf16 = L->kv_dtype == 1;
+  p.num_queries = num_queries;
+  p.tail_cap = tail_capacity;
+  p.k_bits = L->k_bits;
+  p.v_bits = L->v_bits;
+  p.scale_bytes = L->scale_dtype == 1 ? 2 : 4;
+  p.skip_tokens = prefix_tokens;
+  return from_cuda(launch_decode_shared(p, plan, prefix_table, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int32_t kvarn_evict_tiles(const float* mass_in, float* mass_out, int32_t mass_stride, const int32_t* block_table,
+                          int32_t* block_table_out, int32_t* freed, int32_t bt_stride, const int32_t* seq_lens,
+                          int32_t* seq_lens_out, int32_t* freed_count, int32_t max_seq_len, int32_t num_seqs,
+                          const kvarn_layout* L, int32_t keep_tiles, int32_t sink_tiles, int32_t recent_tiles,
+                          uint32_t* error_flags, kvarn_stream_t stream) {
+  const int32_t s = check_dense(L);
+  if (s != KVARN_OK) return s;
+  if (num_seqs < 0 || max_seq_len < 0 || sink_tiles < 0 || recent_tiles < 0 || keep_tiles < sink_tiles ||
+      keep_tiles - sink_tiles < recent_tiles)
+    return KVARN_EINVAL;
+  if (num_seqs == 0) return KVARN_OK;
+  const int32_t tiles = max_seq_len / L->tile_tokens;
+  if (!seq_lens || !seq_lens_out || !freed_count || !error_flags) return KVARN_EINVAL;
+  if (tiles > 0 && (!mass_in || !mass_out || !block_table || !block_table_out || !freed || mass_stride < tiles ||
+                    bt_stride < tiles * (L->tile_tokens / kPageTokens) || freed == block_table ||
+                    freed == block_table_out))
+    return KVARN_EINVAL;
+  if (!aligned(mass_in, 4) || !aligned(mass_out, 4) || !aligned(block_table, 4) || !aligned(block_table_out, 4) ||
+      !aligned(freed, 4) || !aligned(seq_lens, 4) || !aligned(seq_lens_out, 4) || !aligned(freed_count, 4) ||
+      !aligned(error_flags, 4))
+    return KVARN_EALIGN;
+  EvictParams p{};
+  p.mass = mass_in;
+  p.mass_out = mass_out;
+  p.mass_stride = mass_stride;
+  p.table = block_table;
+  p.table_out = block_table_out;
+  p.freed = freed;
+  p.freed_count = freed_count;
+  p.bt_stride = bt_stride;
+  p.seq_lens = seq_lens;
+  p.lens_out = seq_lens_out;
+  p.max_seq_len = max_seq_len;
+  p.num_seqs = num_seqs;
+  p.N = L->tile_tokens;
+  p.keep = keep_tiles;
+  p.sink = sink_tiles;
+  p.recent = recent_tiles;
+  p.err = error_flags;
+  return from_cuda(launch_evict(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_t dtype, int32_t num_seqs,
+                   int32_t num_tokens, const int32_t* positions, int64_t pos_stride, const double* inv_freq,
+                   int32_t rope_dim, int32_t rope_offset, int32_t interleaved, float scale, int32_t inverse,
+                   kvarn_stream_t stream) {
+  if (!tensors || num_tensors < 1 || num_tensors > KVARN_ROPE_MAX_TENSORS) return KVARN_EINVAL;
+  if (dtype < 0 || dtype > 2) return KVARN_EUNSUPPORTED;
+  if (num_seqs < 0 || num_tokens < 0 || rope_dim < 2 || rope_dim % 2 || rope_offset < 0 || pos_stride < 0 ||
+      (interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
+    return KVARN_EINVAL;
+  const uintptr_t size = dtype == 2 ? 4 : 2;
+  RopeParams p{};
+  int64_t heads = 0;
+  for (int32_t k = 0; k < num_tensors; ++k) {
+    const kvarn_rope_tensor& t = tensors[k];
+    if (t.num_heads < 0 || t.head_dim < 1) return KVARN_EINVAL;
+    if (static_cast<int64_t>(rope_offset) + rope_dim > t.head_dim) return KVARN_EINVAL;
+    if (t.head_dim > KVARN_ROPE_MAX_DIM) return KVARN_EUNSUPPORTED;
+    heads += t.num_heads;
+  }
+  if (heads > (1 << 20) || static_cast<int64_t>(num_seqs) * num_tokens > INT32_MAX) return KVARN_EUNSUPPORTED;
+  if (num_seqs == 0 || num_tokens == 0 || heads == 0) return KVARN_OK;
+  if (!positions || !inv_freq) return KVARN_EINVAL;
+  if (!aligned(positions, 4) || !aligned(inv_freq, 8)) return KVARN_EALIGN;
+  for (int32_t k = 0; k < num_tensors; ++k) {
+    const kvarn_rope_tensor& t = tensors[k];
+    if (t.num_heads == 0) continue;
+    if (!t.in || !t.out) return KVARN_EINVAL;
+    if (!aligned(t.in, size) || !aligned(t.out, size)) return KVARN_EALIGN;
+    // in place: every element is written where it was read
+    if (t.in == t.out && (t.in_seq_stride != t.out_seq_stride || t.in_token_stride != t.out_token_stride ||
+                          t.in_head_stride != t.out_head_stride))
+      return KVARN_EINVAL;
+    p.t[p.num_tensors++] = {t.in,            t.out,            t.in_seq_stride,   t.in_token_stride, t.in_head_stride,
+                            t.out_seq_stride, t.out_token_stride, t.out_head_stride, t.num_heads,      t.head_dim};
+    if (t.in != t.out && t.head_dim > rope_dim) p.copy_rest = 1;
+  }
+  p.total_heads = static_cast<int32_t>(heads);
+  p.dtype = dtype;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.positions = positions;
+  p.pos_stride = pos_stride;
+  p.inv_freq = inv_freq;
+  p.rope_dim = rope_dim;
+  p.offset = rope_offset;
+  p.interleaved = interleaved;
+  p.scale = scale;
+  p.inverse = inverse;
+  return from_cuda(launch_rope(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int32_t kvarn_set_copy_wait_test(int64_t cycles, int32_t withhold) {

@@ -159,9 +159,8 @@ static cudaError_t cache_tensor_map(CUtensorMap* map, const void* cache, int64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cudaStream_t st) {
-  if (p.num_seqs == 0) return cudaSuccess;
-  DecArgs A{};
+cudaError_t dense_args(const DecodeParams& p, const DensePlan& plan, DecArgs& A) {
+  A = DecArgs{};
   {
     const int kb = p.k_bits ? p.k_bits : 4, vb = p.v_bits ? p.v_bits : 2, sb = p.scale_bytes ? p.scale_bytes : 4;
     const bool aff = p.codec == 1;
@@ -188,7 +187,8 @@ cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cu
   A.G = p.num_q_heads / p.num_kv_heads;
   A.Q = p.num_queries > 0 ? p.num_queries : 1;
   A.tail_cap = p.tail_cap > 0 ? p.tail_cap : p.N;
-  A.sink_tiles = p.sink_tokens / p.N;
+  A.sink_tiles = (p.skip_tokens + p.sink_tokens) / p.N;
+  A.sink_raw = p.sink_tokens;
   A.recent = p.recent_tokens;
   A.sink_k = p.sink_k;
   A.sink_v = p.sink_v;
@@ -217,31 +217,32 @@ cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cu
     A.wait_limit = w > 0 ? w : kDefaultCopyWait;
     A.withhold = g_copy_withhold.load(std::memory_order_relaxed);
   }
+  return cudaSuccess;
+}
+
+cudaError_t run_decode_kernel(const DecodeParams& p, const DecArgs& A, int ctas, cudaStream_t st) {
   cudaError_t e = cudaErrorInvalidValue;
   const int kb = p.k_bits ? p.k_bits : 4, vb = p.v_bits ? p.v_bits : 2, sb = p.scale_bytes ? p.scale_bytes : 4;
   if (p.codec == 2) {  // the uncompressed fp16 pages (tiles of 32 tokens)
-    e = p.D == 128 ? run_raw<128>(A, plan.ctas, st) : p.D == 256 ? run_raw<256>(A, plan.ctas, st)
-                                                                  : cudaErrorInvalidValue;
-    if (e != cudaSuccess) return e;
-    return p.D == 128 ? launch_merge<128, false>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st)
-                      : launch_merge<256, false>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st);
+    return p.D == 128   ? run_raw<128>(A, ctas, st)
+           : p.D == 256 ? run_raw<256>(A, ctas, st)
+                        : cudaErrorInvalidValue;
   }
   if (p.codec == 1) {
     if (p.D != 128 || p.N != 128 || kb != vb) return cudaErrorInvalidValue;
     switch (kb) {
 #define KVARN_AFF_CASE(K) \
-  case K: e = run_affine_widths<K>(A, p.bf16, plan.ctas, st); break;
+  case K: e = run_affine_widths<K>(A, p.bf16, ctas, st); break;
       KVARN_AFFINE_WIDTHS(KVARN_AFF_CASE)
 #undef KVARN_AFF_CASE
       default: break;
     }
-    if (e != cudaSuccess) return e;
-    return launch_merge<128, false>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st);
+    return e;
   }
   if (kb == 4 && vb == 2 && sb == 4) {
 #define KV_DISPATCH(DD, NN, WW)                                                              \
   if (p.D == DD && p.N == NN)                                                                \
-    e = run_dense<DD, NN, WW, 4, 2, 4>(A, plan.ctas, st);
+    e = run_dense<DD, NN, WW, 4, 2, 4>(A, ctas, st);
     KV_DISPATCH(128, 128, 4)
     KV_DISPATCH(128, 64, 4)
     KV_DISPATCH(256, 128, 2)
@@ -250,7 +251,7 @@ cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cu
   } else if (sb == 2 && p.D == 256) {
     switch (16 * kb + vb) {
 #define KVARN_RUN_CASE(K, V) \
-  case 16 * K + V: e = run_dense_widths256<K, V, 2>(A, p.N, p.bf16, plan.ctas, st); break;
+  case 16 * K + V: e = run_dense_widths256<K, V, 2>(A, p.N, p.bf16, ctas, st); break;
       KVARN_WIDTH_PAIRS_256(KVARN_RUN_CASE)
 #undef KVARN_RUN_CASE
       default: break;
@@ -258,7 +259,7 @@ cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cu
   } else if (sb == 2) {
     switch (16 * kb + vb) {
 #define KVARN_RUN_CASE(K, V) \
-  case 16 * K + V: e = run_dense_widths<K, V, 2>(A, p.D, p.N, p.bf16, plan.ctas, st); break;
+  case 16 * K + V: e = run_dense_widths<K, V, 2>(A, p.D, p.N, p.bf16, ctas, st); break;
       KVARN_WIDTH_PAIRS(KVARN_RUN_CASE)
 #undef KVARN_RUN_CASE
       default: break;
@@ -266,15 +267,82 @@ cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cu
   } else if (sb == 4 && p.D == 128) {
     switch (16 * kb + vb) {
 #define KVARN_RUN_CASE(K, V) \
-  case 16 * K + V: e = run_dense_widths<K, V, 4>(A, p.D, p.N, p.bf16, plan.ctas, st); break;
+  case 16 * K + V: e = run_dense_widths<K, V, 4>(A, p.D, p.N, p.bf16, ctas, st); break;
       KVARN_WIDTH_PAIRS_S32(KVARN_RUN_CASE)
 #undef KVARN_RUN_CASE
       default: break;
     }
   }
+  return e;
+}
+
+// Attention mass of a tile: its weights summed over the query heads, from
+// each head's (maximum, sum) of the tile and lse: sum l 2^(m - lse log2 e).
+// A CTA takes 32 tiles of a sequence, a warp every 8th head, lanes the tiles
+// (the pairs of a row are contiguous); the warps' sums are added in a fixed
+// order. Reads 8 bytes per head and tile.
+constexpr int kMassWarps = 8;
+__global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(const DecArgs A, int N, const float* lse,
+                                                               const float* mass_in, float* mass_out, int mass_stride,
+                                                               float decay) {
+  __shared__ float part[kMassWarps][32];
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
+  const int t = blockIdx.x * 32 + lane, C = seq_tiles(A, N, b);
+  float sum = 0.f;
+  if (t < C) {
+    const float2* st = A.stats + static_cast<int64_t>(b) * A.Hq * A.stat_tiles + t;
+#pragma unroll 8
+    for (int h = warp; h < A.Hq; h += kMassWarps) {
+      const float2 v = st[static_cast<int64_t>(h) * A.stat_tiles];
+      sum = fmaf(v.y, exp2f(v.x - lse[b * A.Hq + h] * kLog2e), sum);
+    }
+  }
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && t < A.stat_tiles) {
+#pragma unroll
+    for (int w = 1; w < kMassWarps; ++w) sum += part[w][lane];
+    const int64_t at = static_cast<int64_t>(b) * mass_stride + t;
+    mass_out[at] = t < C ? fmaf(decay, mass_in[at], sum) : 0.f;
+  }
+}
+
+int64_t mass_workspace_bytes(int64_t rows, int32_t max_tiles) {
+  return rows * max_tiles * 8 + (rows * 4 + 15) / 16 * 16;
+}
+
+cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cudaStream_t st) {
+  if (p.num_seqs == 0) return cudaSuccess;
+  DecArgs A;
+  cudaError_t e = dense_args(p, plan, A);
   if (e != cudaSuccess) return e;
-  return p.D == 128 ? launch_merge<128>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st)
-                    : launch_merge<256>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st);
+  const int64_t rows = static_cast<int64_t>(p.num_seqs) * A.Q * p.num_q_heads;
+  float* lse = p.lse;
+  if (p.mass_out) {
+    A.stat_tiles = p.max_seq_len / p.N;
+    A.stats = reinterpret_cast<float2*>(static_cast<char*>(p.workspace) + dense_stream_workspace_bytes(rows, p.D, plan));
+    if (!lse) lse = reinterpret_cast<float*>(A.stats + rows * A.stat_tiles);
+  }
+  e = run_decode_kernel(p, A, plan.ctas, st);
+  if (e != cudaSuccess) return e;
+  if (p.codec != 0)  // the affine and fp16 pages are in the original basis
+    return p.D == 128 ? launch_merge<128, false>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st)
+                      : launch_merge<256, false>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st);
+  e = p.D == 128 ? launch_merge<128>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, lse, st)
+                 : launch_merge<256>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, lse, st);
+  if (e != cudaSuccess || !p.mass_out || A.stat_tiles == 0) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((A.stat_tiles + 31) / 32, p.num_seqs);
+  cfg.blockDim = dim3(32 * kMassWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mass_kernel, A, p.N, static_cast<const float*>(lse), p.mass_in, p.mass_out,
+                            p.mass_stride, p.mass_decay);
 }
 
 }  // namespace kvarn

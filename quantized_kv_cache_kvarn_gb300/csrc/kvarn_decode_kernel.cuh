@@ -159,7 +159,8 @@ struct DecArgs {
   int32_t Hq, Hkv, G;
   int32_t Q;           // query tokens per sequence (speculative verify: the last Q tokens)
   int32_t tail_cap;    // tail rows per (sequence, KV head)
-  int32_t sink_tiles;  // raw sink records: tokens [0, sink_tiles N) are rows of sink_k / sink_v
+  int32_t sink_tiles;  // the pages' first tile: tokens before it are raw sink records or a shared prefix
+  int32_t sink_raw;    // raw sink records: tokens [0, sink_raw) are rows of sink_k / sink_v
   int32_t recent;      // raw recent records: the newest `recent` accepted tokens stay in the tail
   const void* sink_k;
   const void* sink_v;
@@ -184,6 +185,9 @@ struct DecArgs {
   long long wait_limit;   // clock cycles a page copy is waited for before the kernel gives up
   int32_t bf16;           // storage dtype of q and of the raw records: 0 fp16, 1 bf16
   int32_t withhold;       // diagnostic: every copy is announced this many bytes larger (its phase never completes)
+  int32_t fixed_tiles;    // > 0: every sequence has this many committed tiles and seq_lens is not read
+  float2* stats;          // per output row and tile (base-2 maximum, sum) of its scores, or null
+  int32_t stat_tiles;     // row length of stats
 };
 
 template <typename T, int E>
@@ -345,7 +349,7 @@ struct RawSplit {
     miss = (c1 > max(c0, n_sink) && (A.tail_k == nullptr || A.tail_v == nullptr)) ||
            (min(c1, n_sink) > c0 && (A.sink_k == nullptr || A.sink_v == nullptr));
     slot = A.tile_slots + chunk;
-    sink0 = (static_cast<int64_t>(b) * A.Hkv + kvh) * (A.sink_tiles * N);
+    sink0 = (static_cast<int64_t>(b) * A.Hkv + kvh) * A.sink_raw;
     tail0 = (static_cast<int64_t>(b) * A.Hkv + kvh) * A.tail_cap;
   }
   __device__ int qj(int r) const { return __shfl_sync(0xffffffffu, qj_l, r); }
@@ -724,6 +728,7 @@ template <int D, int W, int CD = 0> constexpr int decode_min_ctas() {
 
 // Length of sequence b, checked against max_seq_len (flagged and clamped).
 __device__ __forceinline__ int checked_len(const DecArgs& A, int b) {
+  if (A.fixed_tiles > 0) return 0;  // no lengths: see committed_end
   int len = A.seq_lens[b];
   if (len < 0 || len > A.max_seq_len) {
     set_error(A.err, KVARN_DEVERR_SEQ_LEN);
@@ -738,6 +743,7 @@ __device__ __forceinline__ int checked_len(const DecArgs& A, int b) {
 // stay raw. Compressed tiles are [sink_tiles, committed / N).
 __device__ __forceinline__ int committed_end(const DecArgs& A, int N, int len) {
   if (A.partial_tiles) return (len + N - 1) / N * N;  // every token is in the pages
+  if (A.fixed_tiles > 0) return A.fixed_tiles * N;    // a shared prefix: seen whole by every row
   return max(A.sink_tiles * N, (max(0, visible_len(len, A.Q, 0) - A.recent) / N) * N);
 }
 
@@ -940,6 +946,13 @@ __device__ __forceinline__ bool dense_segment(const DecArgs& A, unsigned char* s
     issue_k(phys);
     issue_v(phys);
   }
+
+  // where the unit's first tile of this segment goes in the tile masses'
+  // pairs; in shared memory, so that no register holds it over the tiles
+  __shared__ int64_t stat_base[UNITS];
+  volatile int64_t* stat_at = stat_base + unit;
+  if (!PLAIN_Q && A.stats && leader && lane == 0)
+    *stat_at = static_cast<int64_t>(b * A.Hq + kvh * A.G) * A.stat_tiles + first;
 
   // ---- rotated, scaled query rows of the row group (unused rows are zero)
   for (int h = warp; h < 8; h += W) {
@@ -1175,6 +1188,11 @@ __device__ __forceinline__ bool dense_segment(const DecArgs& A, unsigned char* s
     const float2 pt = tree_reduce(ps2, [](float2 a, float2 b) { return f2add(a, b); });
     lsum = fmaf(lsum, alpha, pt.x + pt.y);
     m = m_new;
+    if (!PLAIN_Q && A.stats) {  // the tile's share of each row, for the tile masses (one query: row g is head g)
+      const float lt = warp_sum_xor(pt.x + pt.y, 1, 4);
+      if (t == 0 && leader && g < A.G)
+        A.stats[*stat_at + static_cast<int64_t>(g) * A.stat_tiles + i * UNITS] = make_float2(m_new, lt);
+    }
 
     // the K slot is free: start the next tile's K part
     if (i + 1 < n_my) {
@@ -1397,7 +1415,7 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
     } else {
       tail_partials<D, N, W, (S::RAW_KST > 0)>(A, smem + S::OFF_RAW_MRG, reinterpret_cast<float*>(smem + S::OFF_QROT),
                                                reinterpret_cast<float*>(smem + S::OFF_RAW_PB), smem + S::OFF_RAW_KST, b,
-                                               x % A.Hkv, RowMap(A, x / A.Hkv), len, A.sink_tiles * N,
+                                               x % A.Hkv, RowMap(A, x / A.Hkv), len, A.sink_raw,
                                                committed_end(A, N, len), chunk);
     }
   }
@@ -1449,6 +1467,11 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
     dead = !dense_segment<D, N, W, KB, VB, SB, CD>(A, smem, P.b, P.x, t0, t1, slot, ph, dead) || dead;
   }
 }
+
+// The arguments of the decode kernels for a call's parameters, and the kernel
+// of its layout without the merge (kvarn_decode.cu).
+cudaError_t dense_args(const DecodeParams& p, const DensePlan& plan, DecArgs& A);
+cudaError_t run_decode_kernel(const DecodeParams& p, const DecArgs& A, int ctas, cudaStream_t st);
 
 template <int D, int N, int W, int KB, int VB, int SB, int CD = kCodecKvarn>
 cudaError_t run_dense(const DecArgs& A, int ctas, cudaStream_t st) {

@@ -112,6 +112,11 @@ struct DecodeParams {
   const void* sink_v;
   int32_t k_bits, v_bits, scale_bytes;  // dense code widths and scale size (0: the k4v2 preset, fp32)
   int32_t codec;        // dense: 0 the KVarN pages, 1 the affine comparison pages
+  int32_t skip_tokens;  // dense: tokens before the first tile taken from block_table (a shared prefix; 0: none)
+  const float* mass_in;  // dense: tile masses to add to (null: none are gathered)
+  float* mass_out;
+  int32_t mass_stride;
+  float mass_decay;
 };
 
 // (query head, query token) row groups of eight per KV head.
@@ -178,6 +183,66 @@ cudaError_t launch_store_fp16(const StoreFp16Params& p, cudaStream_t st);
 // Resident CTAs per SM of the decode over uncompressed fp16 pages (the dense
 // decode kernel with no codec: DecodeParams::codec = 2, N = 32).
 int raw_decode_ctas_per_sm(int32_t D);
+
+// Tile masses of the dense decode: one (base-2 maximum, sum) pair per output
+// row and committed tile in the workspace, and one lse per row where the
+// caller takes none.
+int64_t mass_workspace_bytes(int64_t rows, int32_t max_tiles);
+
+// Rotary positions (kvarn_rope.cu).
+constexpr int kRopeMaxTensors = 4;
+struct RopeTensor {
+  const void* in;
+  void* out;
+  int64_t in_seq, in_tok, in_head, out_seq, out_tok, out_head;  // elements
+  int32_t heads, dim;
+};
+struct RopeParams {
+  RopeTensor t[kRopeMaxTensors];
+  int32_t num_tensors, total_heads;
+  int32_t dtype;  // 0 fp16, 1 bf16, 2 fp32
+  int32_t num_seqs, num_tokens;
+  const int32_t* positions;
+  int64_t pos_stride;
+  const double* inv_freq;
+  int32_t rope_dim, offset;
+  int32_t interleaved;
+  float scale;
+  int32_t inverse;
+  int32_t copy_rest;  // some tensor has channels outside the rotated ones to copy
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t st);
+
+// Eviction of tiles (kvarn_evict.cu).
+struct EvictParams {
+  const float* mass;
+  float* mass_out;
+  int32_t mass_stride;
+  const int32_t* table;
+  int32_t* table_out;
+  int32_t* freed;
+  int32_t* freed_count;
+  int32_t bt_stride;
+  const int32_t* seq_lens;
+  int32_t* lens_out;
+  int32_t max_seq_len, num_seqs, N;
+  int32_t keep, sink, recent;
+  int32_t key_cap;
+  uint32_t* err;
+};
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
+
+// Decode over a prefix that the whole batch shares (kvarn_shared.cu): the
+// prefix's partials, the own tokens' decode, one merge.
+struct SharedPlan {
+  DensePlan own;     // each sequence's tokens past the prefix
+  DensePlan prefix;  // the prefix as one sequence whose query rows are the batch's
+};
+SharedPlan plan_shared(int32_t num_seqs, int32_t num_kv_heads, int32_t G, int32_t num_queries, int32_t prefix_tiles,
+                       int32_t own_tiles, int32_t D, int32_t N, int32_t raw_max, int32_t kb, int32_t vb, int32_t sb);
+int64_t shared_workspace_bytes(int64_t rows, int32_t D, const SharedPlan& plan);
+cudaError_t launch_decode_shared(const DecodeParams& p, const SharedPlan& plan, const int32_t* prefix_table,
+                                 cudaStream_t st);
 
 SplitPlan plan_mla(int32_t num_seqs, int32_t max_seq_len);
 int64_t mla_workspace_bytes(int32_t num_seqs, int32_t num_heads, const SplitPlan& plan);

@@ -390,57 +390,90 @@ def affine_decode(q, layout: Layout, cache, block_table, seq_lens, max_seq_len, 
 # --------------------------------------------- serving around the cache
 # Rotary positions, attention over a shared prefix, tile masses and the
 # eviction of tiles by them. These calls also check what the C ABI can not
-# see: types, shapes, contiguity and the device of every tensor.
+# see: types, shapes, contiguity and the device of every tensor. A decode step
+# makes several of them, so the checks are plain comparisons and messages are
+# only built for a refusal.
 
 ROPE_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise KvarnError(what)
+def _refuse(what: str, why: str):
+    raise KvarnError(f"{what}: {why}")
 
 
-def _on_current_device(what: str, *tensors):
-    """Every tensor on the GPU that is current: the launches go there."""
+def _device_of(what: str, *tensors) -> int:
+    """The current device, on which every tensor must live: the launches go there."""
+    dev = -1
     for t in tensors:
         if t is not None:
-            _need(t.is_cuda, f"{what}: tensor must live on the GPU")
-            _need(t.device.index == torch.cuda.current_device(), f"{what}: tensor is not on the current device")
+            d = t.get_device()
+            if d < 0:
+                _refuse(what, "tensor must live on the GPU")
+            if dev < 0:
+                dev = torch._C._cuda_getDevice()
+            if d != dev:
+                _refuse(what, "tensor is not on the current device")
+    return dev
 
 
-def _tensor(what: str, name: str, t, dtype, shape, optional=False):
-    """t is None (where allowed) or contiguous, of this type and shape (-1: any size)."""
-    if t is None:
-        _need(optional, f"{what}: {name} is missing")
-        return
-    _need(t.dtype == dtype, f"{what}: {name} must be {dtype}, not {t.dtype}")
-    _need(t.dim() == len(shape) and all(n in (-1, m) for n, m in zip(shape, t.shape)),
-          f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    _need(t.is_contiguous(), f"{what}: {name} must be contiguous")
+def _raw_stream(what: str, stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        _refuse(what, "stream is not on the current device")
+    return stream.cuda_stream
 
 
-def _table(what: str, name: str, t, dtype, rows: int):
-    _need(t is not None and t.dtype == dtype and t.dim() == 2 and t.shape[0] == rows and
-          (t.shape[1] == 0 or t.stride(1) == 1) and t.stride(0) >= t.shape[1],
-          f"{what}: {name} must be a row-contiguous {dtype} matrix of {rows} rows")
+def _tensor(what: str, name: str, t, dtype, shape):
+    """t is contiguous, of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(what, f"{name} must be contiguous {dtype} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)} "
+                      f"with strides {t.stride()}")
+
+
+def _row_stride(what: str, name: str, t, dtype, rows: int) -> int:
+    """Row stride of a matrix of `rows` rows, contiguous within a row."""
+    if t.dtype is dtype and t.dim() == 2:
+        (n, m), (s, e) = t.shape, t.stride()
+        if n == rows and (e == 1 or m <= 1) and (s >= m or n <= 1):
+            return m if n <= 1 else s
+    _refuse(what, f"{name} must be a row-contiguous {dtype} matrix of {rows} rows, not {t.dtype} {tuple(t.shape)} "
+                  f"with strides {t.stride()}")
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap):
-    """The checks of the decode calls' common tensors. q: [B, ..., Hq, D]."""
+    """The checks of the decode calls' common tensors (q: [B, ..., Hq, D]);
+    returns the block table's row stride."""
     kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
-    B, Hkv, D = q.shape[0], layout.num_kv_heads, layout.head_dim
-    _on_current_device(what, q, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse)
-    _tensor(what, "q", q, kv_dtype, (*q.shape[:-1], D))
-    _need(cache.dtype == torch.uint8 and cache.is_contiguous() and
-          cache.numel() >= layout.num_pages * Hkv * page_bytes(layout), f"{what}: cache is smaller than the layout")
-    _table(what, "block_table", block_table, torch.int32, B)
+    shape = q.shape
+    B, Hkv, D = shape[0], layout.num_kv_heads, layout.head_dim
+    _tensor(what, "q", q, kv_dtype, (*shape[:-1], D))
+    if (cache.dtype is not torch.uint8 or not cache.is_contiguous()
+            or cache.numel() < layout.num_pages * Hkv * page_bytes(layout)):
+        _refuse(what, "cache is not contiguous bytes of the layout's pages")
+    bt_stride = _row_stride(what, "block_table", block_table, torch.int32, B)
     _tensor(what, "seq_lens", seq_lens, torch.int32, (B,))
-    _tensor(what, "out", out, torch.float32, q.shape)
-    _tensor(what, "lse", lse, torch.float32, q.shape[:-1], optional=True)
-    for name, t in (("tail_k", tail_k), ("tail_v", tail_v)):
-        _tensor(what, name, t, kv_dtype, (B, Hkv, cap, D), optional=True)
-    _need(workspace.is_contiguous(), f"{what}: workspace must be contiguous")
+    _tensor(what, "out", out, torch.float32, shape)
+    if lse is not None:
+        _tensor(what, "lse", lse, torch.float32, shape[:-1])
+    if (tail_k is None) != (tail_v is None):
+        _refuse(what, "tail_k and tail_v come together")
+    if tail_k is not None:
+        _tensor(what, "tail_k", tail_k, kv_dtype, (B, Hkv, cap, D))
+        _tensor(what, "tail_v", tail_v, kv_dtype, (B, Hkv, cap, D))
+    if not workspace.is_contiguous():
+        _refuse(what, "workspace must be contiguous")
     _tensor(what, "err", err, torch.int32, (1,))
+    return bt_stride
+
+
+def _need(ok: bool, why: str):
+    if not ok:
+        raise KvarnError(why)
 
 
 def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.0, ntk: float = 1.0, yarn=None,
@@ -480,29 +513,40 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.
 
 
 def _rope(what, xs, outs, positions, inv_freq, rope_offset, interleaved, scale, inverse, stream):
-    single = isinstance(xs, torch.Tensor)
-    xs, outs = ([xs], [outs]) if single else (list(xs), list(outs))
-    _need(1 <= len(xs) <= 4 and len(xs) == len(outs), f"{what}: one to four tensors, each with an output")
-    _need(xs[0].dim() == 4, f"{what}: tensors must be [seqs, tokens, heads, head_dim]")
-    B, S = xs[0].shape[:2]
-    _need(xs[0].dtype in ROPE_DTYPES, f"{what}: type {xs[0].dtype} is not supported")
-    _on_current_device(what, *xs, *outs, positions, inv_freq)
-    arr = (RopeTensor * len(xs))()
-    for k, (x, y) in enumerate(zip(xs, outs)):
-        _need(x.dim() == 4 and x.shape[:2] == (B, S) and y.shape == x.shape and x.dtype == y.dtype == xs[0].dtype,
-              f"{what}: tensors must share sequences, tokens and type, and each output its tensor's shape")
-        _need(x.shape[3] == 1 or (x.stride(3) == 1 and y.stride(3) == 1), f"{what}: heads must be contiguous")
-        _need(all(n <= 1 or s != 0 for n, s in zip(y.shape, y.stride())), f"{what}: an output may not be broadcast")
-        arr[k] = RopeTensor(x.data_ptr(), y.data_ptr(), x.stride(0), x.stride(1), x.stride(2), y.stride(0), y.stride(1),
-                            y.stride(2), x.shape[2], x.shape[3])
-    _need(positions.dtype == torch.int32 and positions.dim() == 2 and tuple(positions.shape) in ((B, S), (1, S)) and
-          (S <= 1 or positions.stride(1) == 1), f"{what}: positions must be int32 [seqs or 1, tokens], rows contiguous")
-    _need(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous(),
-          f"{what}: inv_freq must be a float64 vector")
-    _check(lib().kvarn_rope(arr, len(xs), ROPE_DTYPES[xs[0].dtype], B, S, _ptr(positions),
-                            positions.stride(0) if positions.shape[0] > 1 else 0, _ptr(inv_freq),
-                            2 * inv_freq.numel(), rope_offset, int(interleaved), scale, int(inverse), _stream(stream)),
-           what)
+    if isinstance(xs, torch.Tensor):
+        xs, outs = (xs,), (outs,)
+    n = len(xs)
+    if not 1 <= n <= 4 or len(outs) != n:
+        _refuse(what, "one to four tensors, each with an output")
+    x0 = xs[0]
+    dtype = x0.dtype
+    if x0.dim() != 4 or dtype not in ROPE_DTYPES:
+        _refuse(what, f"tensors must be float16, bfloat16 or float32 [seqs, tokens, heads, head_dim], not {dtype} "
+                      f"{tuple(x0.shape)}")
+    B, S = x0.shape[0], x0.shape[1]
+    dev = _device_of(what, *xs, *outs, positions, inv_freq)
+    arr = (RopeTensor * n)()
+    for k in range(n):
+        x, y = xs[k], outs[k]
+        shape = x.shape
+        if len(shape) != 4 or shape[0] != B or shape[1] != S or y.shape != shape or x.dtype is not dtype or y.dtype is not dtype:
+            _refuse(what, "tensors must share sequences, tokens and type, and each output its tensor's shape")
+        xb, xt, xh, xe = x.stride()
+        yb, yt, yh, ye = y.stride()
+        if (xe != 1 or ye != 1) and shape[3] > 1:
+            _refuse(what, "the channels of a head must be contiguous")
+        if (yb == 0 and B > 1) or (yt == 0 and S > 1) or (yh == 0 and shape[2] > 1):
+            _refuse(what, "an output may not be broadcast")
+        arr[k] = (x.data_ptr(), y.data_ptr(), xb, xt, xh, yb, yt, yh, shape[2], shape[3])
+    rows = positions.shape[0] if positions.dim() == 2 else -1
+    if positions.dtype is not torch.int32 or (rows != B and rows != 1) or positions.shape[1] != S or (
+            S > 1 and positions.stride(1) != 1):
+        _refuse(what, "positions must be int32 [seqs or 1, tokens], rows contiguous")
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        _refuse(what, "inv_freq must be a contiguous float64 vector")
+    _check(lib().kvarn_rope(arr, n, ROPE_DTYPES[dtype], B, S, positions.data_ptr(), positions.stride(0) if rows > 1 else 0,
+                            inv_freq.data_ptr(), 2 * inv_freq.numel(), rope_offset, 1 if interleaved else 0, scale,
+                            1 if inverse else 0, _raw_stream(what, stream, dev)), what)
 
 
 def rope(xs, outs, positions, inv_freq, *, rope_offset=0, interleaved=False, scale=1.0, stream=None):
@@ -532,21 +576,23 @@ def decode_mass(q, layout: Layout, cache, block_table, seq_lens, max_seq_len, ou
     """decode that also gives every committed tile's attention mass: mass_out
     = decay * mass_in + the weights of the tile's tokens over all query heads
     (float32 [B, >= max_seq_len / N], may be the same tensor)."""
-    _need(q.dim() == 3, "decode_mass: q must be [seqs, heads, head_dim]")
+    what = "decode_mass"
+    if q.dim() != 3:
+        _refuse(what, "q must be [seqs, heads, head_dim]")
     B, Hq, _ = q.shape
-    _decode_tensors("decode_mass", q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse,
-                    layout.tile_tokens)
-    _on_current_device("decode_mass", mass_in, mass_out)
-    for name, t in (("mass_in", mass_in), ("mass_out", mass_out)):
-        _table("decode_mass", name, t, torch.float32, B)
-    _need(mass_in.shape[1] == mass_out.shape[1] and (B <= 1 or mass_in.stride(0) == mass_out.stride(0)),
-          "decode_mass: mass_in and mass_out differ in shape or stride")
-    _check(lib().kvarn_decode_mass(_ptr(q), Hq, sm_scale, _ptr(cache), ctypes.byref(layout), _ptr(block_table),
-                                   block_table.shape[1] if B <= 1 else block_table.stride(0), _ptr(seq_lens), max_seq_len,
-                                   _ptr(tail_k), _ptr(tail_v), B, _ptr(out), _ptr(lse), _ptr(mass_in), _ptr(mass_out),
-                                   mass_in.shape[1] if B <= 1 else mass_in.stride(0), decay, _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)),
-           "decode_mass")
+    dev = _device_of(what, q, cache, block_table, seq_lens, out, mass_in, mass_out, workspace, err, tail_k, tail_v, lse)
+    bt_stride = _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse,
+                                layout.tile_tokens)
+    stride = _row_stride(what, "mass_in", mass_in, torch.float32, B)
+    if _row_stride(what, "mass_out", mass_out, torch.float32, B) != stride or mass_out.shape != mass_in.shape:
+        _refuse(what, "mass_in and mass_out differ in shape or stride")
+    if mass_in.shape[1] < max_seq_len // layout.tile_tokens:
+        _refuse(what, "mass_in has fewer columns than max_seq_len has tiles")
+    _check(lib().kvarn_decode_mass(q.data_ptr(), Hq, sm_scale, cache.data_ptr(), ctypes.byref(layout),
+                                   block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), max_seq_len, _addr(tail_k),
+                                   _addr(tail_v), B, out.data_ptr(), _addr(lse), mass_in.data_ptr(), mass_out.data_ptr(),
+                                   stride, decay, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   err.data_ptr(), _raw_stream(what, stream, dev)), what)
 
 
 def evict_tiles(mass_in, block_table, seq_lens, layout: Layout, max_seq_len, keep_tiles, mass_out, block_table_out,
@@ -558,24 +604,27 @@ def evict_tiles(mass_in, block_table, seq_lens, layout: Layout, max_seq_len, kee
     freed_count of them per row) is a tensor of its own."""
     what = "evict_tiles"
     B = seq_lens.shape[0]
-    _on_current_device(what, mass_in, block_table, seq_lens, mass_out, block_table_out, seq_lens_out, freed, freed_count,
-                       err)
-    tables, masses = (block_table, block_table_out, freed), (mass_in, mass_out)
-    for t in tables:
-        _table(what, "a page table", t, torch.int32, B)
-    for t in masses:
-        _table(what, "a mass table", t, torch.float32, B)
-    for group in (tables, masses):
-        _need(all(t.shape == group[0].shape and (B <= 1 or t.stride(0) == group[0].stride(0)) for t in group),
-              f"{what}: tables of one kind differ in shape or stride")
-    for name, t in (("seq_lens", seq_lens), ("seq_lens_out", seq_lens_out), ("freed_count", freed_count)):
-        _tensor(what, name, t, torch.int32, (B,))
+    dev = _device_of(what, mass_in, block_table, seq_lens, mass_out, block_table_out, seq_lens_out, freed, freed_count, err)
+    rows = _row_stride(what, "block_table", block_table, torch.int32, B)
+    shape = block_table.shape
+    for name, t in (("block_table_out", block_table_out), ("freed", freed)):
+        if _row_stride(what, name, t, torch.int32, B) != rows or t.shape != shape:
+            _refuse(what, f"{name} differs from block_table in shape or stride")
+    masses = _row_stride(what, "mass_in", mass_in, torch.float32, B)
+    if _row_stride(what, "mass_out", mass_out, torch.float32, B) != masses or mass_out.shape != mass_in.shape:
+        _refuse(what, "mass_in and mass_out differ in shape or stride")
+    tiles = max_seq_len // layout.tile_tokens
+    if mass_in.shape[1] < tiles or shape[1] < tiles * (layout.tile_tokens // 16):
+        _refuse(what, "a table has fewer columns than max_seq_len has tiles")
+    _tensor(what, "seq_lens", seq_lens, torch.int32, (B,))
+    _tensor(what, "seq_lens_out", seq_lens_out, torch.int32, (B,))
+    _tensor(what, "freed_count", freed_count, torch.int32, (B,))
     _tensor(what, "err", err, torch.int32, (1,))
-    row = (lambda t: t.shape[1] if B <= 1 else t.stride(0))
-    _check(lib().kvarn_evict_tiles(_ptr(mass_in), _ptr(mass_out), row(mass_in), _ptr(block_table), _ptr(block_table_out),
-                                   _ptr(freed), row(freed), _ptr(seq_lens), _ptr(seq_lens_out), _ptr(freed_count),
-                                   max_seq_len, B, ctypes.byref(layout), keep_tiles, sink_tiles, recent_tiles, _ptr(err),
-                                   _stream(stream)), what)
+    _check(lib().kvarn_evict_tiles(mass_in.data_ptr(), mass_out.data_ptr(), masses, block_table.data_ptr(),
+                                   block_table_out.data_ptr(), freed.data_ptr(), rows, seq_lens.data_ptr(),
+                                   seq_lens_out.data_ptr(), freed_count.data_ptr(), max_seq_len, B, ctypes.byref(layout),
+                                   keep_tiles, sink_tiles, recent_tiles, err.data_ptr(), _raw_stream(what, stream, dev)),
+           what)
 
 
 def decode_shared_workspace_bytes(layout: Layout, num_seqs: int, num_q_heads: int, num_queries: int, max_seq_len: int,
@@ -593,19 +642,21 @@ def decode_shared(q, layout: Layout, cache, prefix_table, prefix_tokens, block_t
     prefix_tokens tokens (whole tiles), in the pages prefix_table names.
     q: [B, Q, Hq, D]; tail_k/v: [B, Hkv, capacity, D]; out: [B, Q, Hq, D]."""
     what = "decode_shared"
-    _need(q.dim() == 4, f"{what}: q must be [seqs, queries, heads, head_dim]")
+    if q.dim() != 4:
+        _refuse(what, "q must be [seqs, queries, heads, head_dim]")
     B, Q, Hq, _ = q.shape
-    cap = tail_k.shape[2] if tail_k is not None else layout.tile_tokens + Q - 2
-    _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap)
-    _on_current_device(what, prefix_table)
-    _tensor(what, "prefix_table", prefix_table, torch.int32, (-1,))
-    _need(prefix_table.numel() * layout.page_tokens >= prefix_tokens, f"{what}: prefix_table is shorter than the prefix")
-    _check(lib().kvarn_decode_shared(_ptr(q), Hq, Q, sm_scale, _ptr(cache), ctypes.byref(layout), _ptr(prefix_table),
-                                     prefix_tokens, _ptr(block_table),
-                                     block_table.shape[1] if B <= 1 else block_table.stride(0), _ptr(seq_lens),
-                                     max_seq_len, _ptr(tail_k), _ptr(tail_v), max(cap, 1), B, _ptr(out), _ptr(lse),
-                                     _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err),
-                                     _stream(stream)), what)
+    cap = tail_k.shape[2] if tail_k is not None and tail_k.dim() == 4 else max(1, layout.tile_tokens + Q - 2)
+    dev = _device_of(what, q, cache, prefix_table, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse)
+    bt_stride = _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap)
+    if (prefix_table.dtype is not torch.int32 or prefix_table.dim() != 1 or not prefix_table.is_contiguous()
+            or prefix_table.shape[0] * 16 < prefix_tokens):
+        _refuse(what, "prefix_table must be a contiguous int32 vector of the prefix's pages")
+    _check(lib().kvarn_decode_shared(q.data_ptr(), Hq, Q, sm_scale, cache.data_ptr(), ctypes.byref(layout),
+                                     prefix_table.data_ptr(), prefix_tokens, block_table.data_ptr(), bt_stride,
+                                     seq_lens.data_ptr(), max_seq_len, _addr(tail_k), _addr(tail_v), cap, B,
+                                     out.data_ptr(), _addr(lse), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), err.data_ptr(),
+                                     _raw_stream(what, stream, dev)), what)
 
 
 def set_copy_wait_test(cycles: int, withhold: bool = False) -> None:

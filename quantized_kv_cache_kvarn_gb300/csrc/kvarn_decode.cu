@@ -70,7 +70,28 @@ DensePlan plan_dense_stream(int32_t num_seqs, int32_t units_per_seq, int32_t max
   p.slots = p.tile_slots + p.raw_splits;
   const int64_t tile_ctas = (most + p.min_tiles - 1) / p.min_tiles;
   const int64_t raw_items = units * p.raw_splits;
-  p.ctas = static_cast<int32_t>(std::max<int64_t>(1, std::min(resident, std::max(tile_ctas, raw_items))));
+  p.ctas = static_cast<int32_t>(std::max<int64_t>(1, std::min(resident, tile_ctas + raw_items)));
+  return p;
+}
+
+DensePlan plan_dense_pieces(int32_t num_seqs, int32_t units_per_seq, int32_t max_tiles, int32_t D, int32_t N,
+                            int32_t raw_max, int32_t kb, int32_t vb, int32_t sb) {
+  DensePlan p{};
+  const int in_flight = D == 256 ? dense_decode_warps(D) / 2 : dense_decode_warps(D);
+  const int64_t resident = static_cast<int64_t>(device_sm_count()) * dense_decode_ctas_per_sm(D, N, kb, vb, sb);
+  const int64_t units = static_cast<int64_t>(num_seqs) * units_per_seq;
+  // a piece: as many rounds of the CTA's tiles in flight as the CTA slots
+  // need when the units are half of the longest on average
+  const int64_t rounds = std::max<int64_t>(1, units * max_tiles / (2 * in_flight * resident));
+  p.piece = p.min_tiles = static_cast<int32_t>(std::min<int64_t>(rounds * in_flight, std::max(1, max_tiles)));
+  p.tile_slots = (max_tiles + p.piece - 1) / p.piece;
+  // raw records: splits of 128 down to 32 while the CTA slots hold them all
+  // (a split of 32 takes about half the time of one of 128, most of it fixed)
+  p.raw_chunk = kRawChunk;
+  while (p.raw_chunk > 32 && units * ((raw_max + p.raw_chunk / 2 - 1) / (p.raw_chunk / 2)) <= resident) p.raw_chunk /= 2;
+  p.raw_splits = raw_max > p.raw_chunk ? (raw_max + p.raw_chunk - 1) / p.raw_chunk : 1;
+  p.slots = p.tile_slots + p.raw_splits;
+  p.ctas = static_cast<int32_t>(std::max<int64_t>(1, std::min(resident, units * (p.tile_slots + p.raw_splits))));
   return p;
 }
 
@@ -209,6 +230,7 @@ cudaError_t dense_args(const DecodeParams& p, const DensePlan& plan, DecArgs& A)
   A.raw_splits = plan.raw_splits;
   A.raw_chunk = plan.raw_chunk;
   A.slots = plan.slots;
+  A.piece = plan.piece;
   A.err = p.err;
   A.bf16 = p.bf16 ? 1 : 0;
   A.partial_tiles = p.codec == 2;

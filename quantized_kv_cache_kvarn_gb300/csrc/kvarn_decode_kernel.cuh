@@ -185,6 +185,10 @@ struct DecArgs {
   long long wait_limit;   // clock cycles a page copy is waited for before the kernel gives up
   int32_t bf16;           // storage dtype of q and of the raw records: 0 fp16, 1 bf16
   int32_t withhold;       // diagnostic: every copy is announced this many bytes larger (its phase never completes)
+  int32_t piece;          // > 0: tiles are cut into pieces of so many within each unit, a CTA per piece in turn, piece k
+                          // of a unit into slot k (0: stream-K over the flattened list)
+  int32_t late_wait;      // the kernel before on the stream started after this call's inputs were complete (it triggers
+                          // its dependents behind its own wait): run beside it and wait for its end before ending
   int32_t fixed_tiles;    // > 0: every sequence has this many committed tiles and seq_lens is not read
   float2* stats;          // per output row and tile (base-2 maximum, sum) of its scores, or null
   int32_t stat_tiles;     // row length of stats
@@ -1396,12 +1400,13 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
   // launched as a programmatic dependent of the kernel before it (a commit,
   // or whatever wrote the queries, lengths or tails): nothing in global
   // memory is read before that kernel has completed
-  pdl_wait_primary();
+  if (!A.late_wait) pdl_wait_primary();
 
-  // ---- raw records: items r = blockIdx.x, + gridDim.x, ... of (sequence,
-  //      unit, raw chunk)
+  // ---- raw records: items r = 0, 1, ... of (sequence, unit, raw chunk) go to
+  //      the CTAs from the last one down, so that while the grid has CTAs
+  //      to spare the raw items and the tiles run side by side
   const int64_t units = static_cast<int64_t>(A.num_seqs) * A.X;
-  for (int64_t r = blockIdx.x; r < units * A.raw_splits; r += gridDim.x) {
+  for (int64_t r = gridDim.x - 1 - blockIdx.x; r < units * A.raw_splits; r += gridDim.x) {
     const int chunk = static_cast<int>(r % A.raw_splits);
     const int64_t u = r / A.raw_splits;
     const int b = static_cast<int>(u / A.X), x = static_cast<int>(u % A.X);
@@ -1420,7 +1425,7 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
     }
   }
 
-  const int64_t total = tiles_before(A, N, A.num_seqs);
+  const int64_t total = A.piece > 0 ? 0 : tiles_before(A, N, A.num_seqs);
   const int64_t by_tiles = total / A.min_tiles > 1 ? total / A.min_tiles : 1;
   const int C = static_cast<int>(by_tiles < gridDim.x ? by_tiles : gridDim.x);
 
@@ -1430,7 +1435,9 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
       const int b = static_cast<int>(u / A.X), x = static_cast<int>(u % A.X);
       const int n = seq_tiles(A, N, b);
       int count = 0;
-      if (n > 0) {
+      if (A.piece > 0) {
+        count = (n + A.piece - 1) / A.piece;
+      } else if (n > 0) {
         const int64_t u0 = tiles_before(A, N, b) + static_cast<int64_t>(x) * n;
         count = cta_of_tile(u0 + n - 1, C, total, S::UNITS) - cta_of_tile(u0, C, total, S::UNITS) + 1;
       }
@@ -1440,16 +1447,24 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
     }
   }
   __syncthreads();  // mbarrier initialisation visible to every warp
-  if (total == 0 || static_cast<int>(blockIdx.x) >= C) return;
+  if (A.piece == 0 && (total == 0 || static_cast<int>(blockIdx.x) >= C)) {
+    if (A.late_wait) pdl_wait_primary();
+    return;
+  }
 
   // ---- this CTA's tiles, one segment per unit they touch. The position is
   //      kept in shared memory (no register holds it across a segment),
   //      double-buffered: the next position is written to the entry nobody
   //      reads in this pass, and read after the segment's closing barrier.
-  __shared__ int64_t pos[3];  // current tile (two entries), end of the range
+  //      In pieces: items = piece * units + unit, first pieces first, every
+  //      gridDim.x-th. Short units (each sequence's own tokens past a shared
+  //      prefix) keep a CTA each this way, where equal ranges of the
+  //      flattened list would put several units into one CTA, one after the
+  //      other.
+  __shared__ int64_t pos[3];  // current tile or item (two entries), end of the range
   if (threadIdx.x == 0) {
-    pos[0] = cta_range_start(blockIdx.x, C, total, S::UNITS);
-    pos[2] = cta_range_start(blockIdx.x + 1, C, total, S::UNITS);
+    pos[0] = A.piece > 0 ? blockIdx.x : cta_range_start(blockIdx.x, C, total, S::UNITS);
+    pos[2] = A.piece > 0 ? units * A.tile_slots : cta_range_start(blockIdx.x + 1, C, total, S::UNITS);
   }
   __syncthreads();
   uint32_t ph = 0;
@@ -1457,15 +1472,36 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
   for (int k = 0;; k ^= 1) {
     const int64_t cur = pos[k], stop = pos[2];
     if (cur >= stop) break;
-    const TilePos P = locate_tile(A, N, cur);
-    if (P.b < 0) break;  // unreachable: cur < total
-    const int64_t seg_end = min(stop, P.u0 + P.n);
-    const int slot = static_cast<int>(blockIdx.x) - cta_of_tile(P.u0, C, total, S::UNITS);
-    const int t0 = A.sink_tiles + P.tile;
-    const int t1 = t0 + static_cast<int>(seg_end - cur);
-    if (threadIdx.x == 0) pos[k ^ 1] = seg_end;
-    dead = !dense_segment<D, N, W, KB, VB, SB, CD>(A, smem, P.b, P.x, t0, t1, slot, ph, dead) || dead;
+    int b, x, slot, t0, t1;
+    int64_t next;
+    if (A.piece > 0) {
+      const int64_t nu = static_cast<int64_t>(A.num_seqs) * A.X, u = cur % nu;
+      slot = static_cast<int>(cur / nu);
+      b = static_cast<int>(u / A.X);
+      x = static_cast<int>(u % A.X);
+      t0 = slot * A.piece;
+      t1 = min(seq_tiles(A, N, b), t0 + A.piece);
+      next = cur + gridDim.x;
+    } else {
+      const TilePos P = locate_tile(A, N, cur);
+      if (P.b < 0) break;  // unreachable: cur < total
+      next = min(stop, P.u0 + P.n);
+      slot = static_cast<int>(blockIdx.x) - cta_of_tile(P.u0, C, total, S::UNITS);
+      b = P.b;
+      x = P.x;
+      t0 = P.tile;
+      t1 = t0 + static_cast<int>(next - cur);
+    }
+    if (threadIdx.x == 0) pos[k ^ 1] = next;
+    if (t0 >= t1) {  // past the unit's last piece
+      __syncthreads();
+      continue;
+    }
+    t0 += A.sink_tiles;
+    t1 += A.sink_tiles;
+    dead = !dense_segment<D, N, W, KB, VB, SB, CD>(A, smem, b, x, t0, t1, slot, ph, dead) || dead;
   }
+  if (A.late_wait) pdl_wait_primary();
 }
 
 // The arguments of the decode kernels for a call's parameters, and the kernel

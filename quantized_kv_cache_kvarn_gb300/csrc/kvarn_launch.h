@@ -143,6 +143,7 @@ struct DensePlan {
   int32_t raw_splits;
   int32_t raw_chunk;   // raw tokens per raw split (kRawChunk times a power of two)
   int32_t slots;       // tile_slots + raw_splits
+  int32_t piece;       // > 0: pieces of so many tiles within each unit instead of stream-K ranges
 };
 
 // units_per_seq: KV heads x row groups; max_tiles: compressed tiles a unit
@@ -150,6 +151,10 @@ struct DensePlan {
 DensePlan plan_dense_stream(int32_t num_seqs, int32_t units_per_seq, int32_t max_tiles, int32_t D, int32_t N,
                             int32_t raw_max, int32_t kb = 4, int32_t vb = 2, int32_t sb = 4,
                             int32_t ctas_per_sm = 0);
+// The same work in pieces: for many short units with a raw tail each, whose
+// longest (max_tiles, raw_max) sizes the grid.
+DensePlan plan_dense_pieces(int32_t num_seqs, int32_t units_per_seq, int32_t max_tiles, int32_t D, int32_t N,
+                            int32_t raw_max, int32_t kb, int32_t vb, int32_t sb);
 // Partials of `rows` output rows, then one int32 tile-partial count per row.
 int64_t dense_stream_workspace_bytes(int64_t rows, int32_t D, const DensePlan& plan);
 int dense_decode_warps(int32_t D);
@@ -237,7 +242,9 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
 struct SharedPlan {
   DensePlan own;     // each sequence's tokens past the prefix
   DensePlan prefix;  // the prefix as one sequence whose query rows are the batch's
-};
+  int32_t tc_units;  // > 0: the tensor-core kernel takes the prefix in so many (KV head, 128 rows) units,
+  int32_t tc_tps;    // tiles per split
+};                   // (and prefix.slots splits)
 SharedPlan plan_shared(int32_t num_seqs, int32_t num_kv_heads, int32_t G, int32_t num_queries, int32_t prefix_tiles,
                        int32_t own_tiles, int32_t D, int32_t N, int32_t raw_max, int32_t kb, int32_t vb, int32_t sb);
 int64_t shared_workspace_bytes(int64_t rows, int32_t D, const SharedPlan& plan);

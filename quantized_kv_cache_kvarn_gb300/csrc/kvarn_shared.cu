@@ -2,85 +2,107 @@
 // sm_103a.
 //
 // The shared prefix is one sequence whose query rows are the rows of the
-// whole batch: its pages are read and converted once per eight rows of a KV
-// head by the dense decode kernel, not once per sequence. Each sequence's own
-// tokens (tiles past the prefix, raw tail) go through the dense decode as
-// ever, starting at the prefix's end. Both leave (maximum, sum, output)
-// partials per row, which one merge joins by log-sum-exp.
+// whole batch. Its pages are read once per 128 rows of a KV head by the
+// tensor-core kernel (kvarn_shared_tc.cu), or, where there are few rows and
+// at head_dim 256, once per eight rows by the dense decode kernel. Each
+// sequence's own tokens (tiles past the prefix, raw tail) go through the
+// dense decode as ever, starting at the prefix's end. Both leave (maximum,
+// sum, output) partials per row, which one merge joins by log-sum-exp.
 #include <math.h>
 
 #include <algorithm>
 
 #include "kvarn_decode_kernel.cuh"
+#include "kvarn_shared.cuh"
 
 namespace kvarn {
 
 namespace {
 
-// One warp per output row: partials of the prefix (slots [0, pcounts[row])
+// Four warps per output row: partials of the prefix (slots [0, pcounts[row])
 // of `pre`), of the row's own tiles ([0, counts[row]) of `own`) and of its
 // raw tail ([raw_begin, slots)), the first two through the inverse Hadamard
-// transform. A sequence of length 0 has no prefix either: out = 0, lse =
+// transform. Each warp takes every fourth slot of each kind (a slot is one
+// dependent load, and a wide head's row may have thirty), the sums meet in
+// shared memory. A sequence of length 0 has no prefix either: out = 0, lse =
 // -inf; one shorter than the prefix and its queries is flagged.
 template <int D>
 __global__ void __launch_bounds__(128) shared_merge_kernel(const float* __restrict__ pre, int pslots,
                                                            const int32_t* __restrict__ pcounts,
                                                            const float* __restrict__ own, int slots,
-                                                           const int32_t* __restrict__ counts, int raw_begin, int rows,
+                                                           const int32_t* __restrict__ counts, int raw_begin,
                                                            int rows_per_seq, const int32_t* __restrict__ seq_lens,
                                                            int shortest, float* out, float* lse, uint32_t* err) {
   constexpr int E = D / 32, S = kPStride(D);
+  __shared__ float part[4][2 * D + 4];  // per warp: rotated part, raw part, sum
   pdl_wait_primary();
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x;
   const int len = seq_lens[row / rows_per_seq];
-  float* o = out + static_cast<int64_t>(row) * D + lane * E;
-  if (len < shortest) {
-    if (len != 0 && lane == 0) set_error(err, KVARN_DEVERR_SEQ_LEN);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    if (lse && lane == 0) lse[row] = -INFINITY;
-    return;
-  }
-  const int np = min(pcounts[row], pslots), nt = min(counts[row], raw_begin);
+  float* o = out + static_cast<int64_t>(row) * D;
+  const int np = pcounts ? min(pcounts[row], pslots) : pslots, nt = min(counts[row], raw_begin);
   const float* P = pre + static_cast<int64_t>(row) * pslots * S;
   const float* O = own + static_cast<int64_t>(row) * slots * S;
   auto used = [&](int s) { return s < nt || s >= raw_begin; };
-  float M = -INFINITY;
+  float M = -INFINITY;  // every warp takes the maximum over all slots
   for (int s = lane; s < np; s += 32) M = fmaxf(M, P[s * S]);
   for (int s = lane; s < slots; s += 32)
     if (used(s)) M = fmaxf(M, O[s * S]);
   M = warp_max_xor(M, 1, 32);
-  if (M == -INFINITY) {  // nothing to see, as in the plain decode's merge
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    if (lse && lane == 0) lse[row] = -INFINITY;
+  if (len < shortest || M == -INFINITY) {  // nothing to see, as in the plain decode's merge
+    if (len != 0 && len < shortest && threadIdx.x == 0) set_error(err, KVARN_DEVERR_SEQ_LEN);
+    for (int j = threadIdx.x; j < D; j += 128) o[j] = 0.f;
+    if (lse && threadIdx.x == 0) lse[row] = -INFINITY;
     return;
   }
-  float L = 0.f;
-  for (int s = lane; s < np; s += 32) L = fmaf(P[s * S + 1], exp2f(P[s * S] - M), L);
-  for (int s = lane; s < slots; s += 32)
-    if (used(s)) L = fmaf(O[s * S + 1], exp2f(O[s * S] - M), L);
-  L = warp_sum_xor(L, 1, 32);
-  float rot[E], more[E], raw[E];
-  accumulate_slots<E>(P, S, 0, np, M, rot);
-  accumulate_slots<E>(O, S, 0, nt, M, more);
-  accumulate_slots<E>(O, S, raw_begin, slots, M, raw);
+  float rot[E], raw[E], L = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) rot[e] += more[e];
+  for (int e = 0; e < E; ++e) rot[e] = raw[e] = 0.f;
+  auto take = [&](const float* p, float (&dst)[E]) {
+    const float w = exp2f(p[0] - M);
+    L = fmaf(p[1], w, L);
+    p += 4 + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + e);
+      dst[e] = fmaf(v.x, w, dst[e]);
+      dst[e + 1] = fmaf(v.y, w, dst[e + 1]);
+      dst[e + 2] = fmaf(v.z, w, dst[e + 2]);
+      dst[e + 3] = fmaf(v.w, w, dst[e + 3]);
+    }
+  };
+#pragma unroll 4
+  for (int s = warp; s < np; s += 4) take(P + static_cast<int64_t>(s) * S, rot);
+#pragma unroll 2
+  for (int s = warp; s < nt; s += 4) take(O + static_cast<int64_t>(s) * S, rot);
+  for (int s = raw_begin + warp; s < slots; s += 4) take(O + static_cast<int64_t>(s) * S, raw);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    part[warp][lane * E + e] = rot[e];
+    part[warp][D + lane * E + e] = raw[e];
+  }
+  if (lane == 0) part[warp][2 * D] = L;
+  __syncthreads();
+  if (warp != 0) return;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) L += part[w][2 * D];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    rot[e] = (part[0][lane * E + e] + part[1][lane * E + e]) + (part[2][lane * E + e] + part[3][lane * E + e]);
+    raw[e] = (part[0][D + lane * E + e] + part[1][D + lane * E + e]) + (part[2][D + lane * E + e] + part[3][D + lane * E + e]);
+  }
   warp_fwht<E>(rot);
   const float invL = 1.f / L, sc = invL / sqrtf(static_cast<float>(D));
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = fmaf(rot[e], sc, raw[e] * invL);
+  for (int e = 0; e < E; ++e) o[lane * E + e] = fmaf(rot[e], sc, raw[e] * invL);
   if (lse && lane == 0) lse[row] = (M + log2f(L)) * kLn2;
 }
 
 template <int D>
-cudaError_t launch_shared_merge(const DecArgs& P, const DecArgs& A, int rows, int shortest, float* out, float* lse,
-                                cudaStream_t st) {
+cudaError_t launch_shared_merge(const float* pre, int pslots, const int32_t* pcounts, const DecArgs& A, int rows,
+                                int shortest, float* out, float* lse, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((rows + 3) / 4);
+  cfg.gridDim = dim3(rows);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -88,18 +110,30 @@ cudaError_t launch_shared_merge(const DecArgs& P, const DecArgs& A, int rows, in
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D>, static_cast<const float*>(P.ws), P.slots,
-                            static_cast<const int32_t*>(P.counts), static_cast<const float*>(A.ws), A.slots,
-                            static_cast<const int32_t*>(A.counts), A.tile_slots, rows, rows / A.num_seqs, A.seq_lens,
+  return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D>, pre, pslots, pcounts, static_cast<const float*>(A.ws), A.slots,
+                            static_cast<const int32_t*>(A.counts), A.tile_slots, rows / A.num_seqs, A.seq_lens,
                             shortest, out, lse, A.err);
 }
+
+// Rows of a KV head from which the tensor-core kernel takes the prefix: it
+// spends the time of 128 rows on any number of them.
+#ifndef KVARN_SHARED_TC_ROWS
+#define KVARN_SHARED_TC_ROWS 16
+#endif
 
 }  // namespace
 
 SharedPlan plan_shared(int32_t num_seqs, int32_t num_kv_heads, int32_t G, int32_t num_queries, int32_t prefix_tiles,
                        int32_t own_tiles, int32_t D, int32_t N, int32_t raw_max, int32_t kb, int32_t vb, int32_t sb) {
   SharedPlan s{};
-  s.own = plan_dense_stream(num_seqs, num_kv_heads * row_groups(G, num_queries), own_tiles, D, N, raw_max, kb, vb, sb);
+  s.own = plan_dense_pieces(num_seqs, num_kv_heads * row_groups(G, num_queries), own_tiles, D, N, raw_max, kb, vb, sb);
+  const int64_t rows = static_cast<int64_t>(num_seqs) * num_queries * G;
+  const int64_t units = (rows + 127) / 128 * num_kv_heads;
+  if (D == 128 && rows >= KVARN_SHARED_TC_ROWS && units <= 65535 && prefix_tiles > 0) {
+    s.tc_units = static_cast<int32_t>(units);
+    s.prefix.slots = s.prefix.tile_slots = shared_tc_splits(s.tc_units, prefix_tiles, N / 64, &s.tc_tps);
+    return s;
+  }
   s.prefix = plan_dense_stream(1, num_kv_heads * row_groups(G, num_seqs * num_queries), prefix_tiles, D, N, 0, kb, vb, sb);
   s.prefix.raw_splits = 0;  // whole tiles only
   s.prefix.slots = s.prefix.tile_slots;
@@ -115,24 +149,58 @@ cudaError_t launch_decode_shared(const DecodeParams& p, const SharedPlan& plan, 
   if (p.num_seqs == 0) return cudaSuccess;
   const int Q = p.num_queries > 0 ? p.num_queries : 1;
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * Q * p.num_q_heads;
-  DecArgs A, P;
+  DecArgs A;
   cudaError_t e = dense_args(p, plan.own, A);
   if (e != cudaSuccess) return e;
-  DecodeParams pp = p;
-  pp.num_seqs = 1;
-  pp.num_queries = p.num_seqs * Q;
-  pp.block_table = prefix_table;
-  pp.skip_tokens = 0;
-  pp.workspace = static_cast<char*>(p.workspace) + dense_stream_workspace_bytes(rows, p.D, plan.own);
-  e = dense_args(pp, plan.prefix, P);
-  if (e != cudaSuccess) return e;
-  P.fixed_tiles = p.skip_tokens / p.N;
-  e = run_decode_kernel(pp, P, plan.prefix.ctas, st);
+  float* pre = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + dense_stream_workspace_bytes(rows, p.D, plan.own));
+  const int32_t* pcounts = nullptr;
+  const int kb = p.k_bits ? p.k_bits : 4, vb = p.v_bits ? p.v_bits : 2, sb = p.scale_bytes ? p.scale_bytes : 4;
+  if (plan.tc_units > 0) {
+    SharedTcArgs T{};
+    const DensePage pg(p.D, p.N, kb, vb, sb);
+    T.q = p.q;
+    T.qscale = p.sm_scale * kLog2e / sqrtf(static_cast<float>(p.D));
+    T.bf16 = p.bf16 ? 1 : 0;
+    T.cache = p.cache;
+    T.num_pages = p.num_pages;
+    T.table = prefix_table;
+    T.Hq = p.num_q_heads;
+    T.Hkv = p.num_kv_heads;
+    T.G = A.G;
+    T.rows_per_head = p.num_seqs * Q * A.G;
+    T.N = p.N;
+    T.tiles = p.skip_tokens / p.N;
+    T.tps = plan.tc_tps;
+    T.k_bits = kb;
+    T.v_bits = vb;
+    T.scale_bytes = sb;
+    T.page_bytes = pg.bytes();
+    T.k_part = pg.k_part();
+    T.tile_bytes = p.N / kPageTokens * pg.bytes();
+    T.ws = pre;
+    T.slots = plan.prefix.slots;
+    T.err = p.err;
+    e = launch_shared_tc(T, plan.tc_units, st);
+    A.late_wait = 1;
+  } else {
+    DecArgs P;
+    DecodeParams pp = p;
+    pp.num_seqs = 1;
+    pp.num_queries = p.num_seqs * Q;
+    pp.block_table = prefix_table;
+    pp.skip_tokens = 0;
+    pp.workspace = pre;
+    e = dense_args(pp, plan.prefix, P);
+    if (e != cudaSuccess) return e;
+    P.fixed_tiles = p.skip_tokens / p.N;
+    pcounts = P.counts;
+    e = run_decode_kernel(pp, P, plan.prefix.ctas, st);
+  }
   if (e == cudaSuccess) e = run_decode_kernel(p, A, plan.own.ctas, st);
   if (e != cudaSuccess) return e;
   const int shortest = p.skip_tokens + Q - 1 > 0 ? p.skip_tokens + Q - 1 : 1;
-  return p.D == 128 ? launch_shared_merge<128>(P, A, static_cast<int>(rows), shortest, p.out, p.lse, st)
-                    : launch_shared_merge<256>(P, A, static_cast<int>(rows), shortest, p.out, p.lse, st);
+  return p.D == 128 ? launch_shared_merge<128>(pre, plan.prefix.slots, pcounts, A, static_cast<int>(rows), shortest, p.out, p.lse, st)
+                    : launch_shared_merge<256>(pre, plan.prefix.slots, pcounts, A, static_cast<int>(rows), shortest, p.out, p.lse, st);
 }
 
 }  // namespace kvarn

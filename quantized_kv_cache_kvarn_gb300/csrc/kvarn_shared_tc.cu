@@ -1,0 +1,657 @@
+// Scores and values of a shared prefix on the fifth-generation tensor cores,
+// sm_103a, head_dim 128.
+//
+// The prefix's pages meet the query rows of the whole batch (R = sequences x
+// queries x G rows per KV head), so the products are matrix products: a CTA
+// takes 128 rows of one KV head and a run of the prefix's tiles, 64 tokens (a
+// stage) at a time, flash-attention style:
+//   S = q' K^T   (128 x 64, K = 128)     P = 2^(S - m)     O += P V
+// with q' = kappa q H / sqrt(D) (rotated basis, base-2 scores), K and V the
+// dequantised rotated rows c (a code + b).
+//
+// fp32 results need more than one fp16 product: every operand is x = hi + lo
+// in fp16 (off by 2^-22 of its tile's or row's magnitude, which a power of two
+// brings to about 1 first: 2^eK, 2^eV per tile, 2^eq per row, put back with
+// the softmax's own scale, so that neither large nor small caches leave
+// fp16's range), and each product is hi hi + lo hi + hi lo, three MMAs with
+// fp32 accumulators in tensor memory. Codes as exact operands with the scales
+// folded around them (as in the dense decode) would need two, but their
+// column scales change q' with every tile and their row scales the output:
+// 576 + 320 more issue slots per SM and tile than this form spends.
+//
+// Roles (448 threads, one CTA per SM):
+//   warps 0-3    softmax: thread = row = tensor-memory lane. Reads the 64
+//                scores, keeps the running maximum (raised only when a score
+//                passes it by 2^8, so that O is rescaled a few times at most)
+//                and sum, writes P hi / lo over the scores as the A operand
+//   warps 4-11   dequantisation, warp = (page of the stage, 64-channel group):
+//                code planes -> exact fp16 (the decode's conversions) -> fp32
+//                c (a code + b) -> hi and lo, stored in the B operands'
+//                128-byte-swizzled rows: K as token rows of channels, V as
+//                channel rows of tokens, which is how the pages' fragments
+//                pair their codes, so every store is one conflict-free word
+//   warp 12      MMA issue: QK of stage s + 2 behind PV of stage s, so that the
+//                tensor pipe has work while the softmax runs
+//   warp 13      page copies (bulk copies, two tiles in flight) and, per tile,
+//                the scales unpacked to fp32 and the two exponents
+// Tensor memory: q' hi, lo 128 columns; S (then P) 2 x 64; O 128, and 128 for
+// the sum of its small products (lo hi + hi lo): the tensor cores truncate the
+// accumulator at every step, so the long sum takes four steps a stage instead
+// of twelve (error against 64 bits at 16384 tokens with one accumulator:
+// 5.4e-6, the fp32 form's is 2.5e-6).
+// A stage costs the tensor pipe 24 MMAs of N = 64 and 12 of N = 128: 1536
+// cycles per 64 tokens and 128 rows.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kvarn_common.cuh"
+#include "kvarn_launch.h"
+#include "kvarn_merge.cuh"
+#include "kvarn_shared.cuh"
+#include "kvarn_tcgen05.cuh"
+
+namespace kvarn {
+
+namespace {
+
+constexpr int kD = 128, kM = 128, kStage = 64;  // channels, rows of a CTA, tokens of a stage
+constexpr int kSoftmax = 128, kDequant = 256, kThreads = kSoftmax + kDequant + 64;
+constexpr int kMmaWarp = (kSoftmax + kDequant) / 32;  // the page copies' warp follows it
+constexpr int kPlane = kStage * kD * 2;   // hi or lo operand plane: 16 KB
+constexpr int kRing = 2;                  // stages of K and of V in flight
+constexpr int kPages = 4;                 // most tiles whose pages are in shared memory or on their way
+constexpr int kMetaSlots = 8;             // tiles whose scales are kept: past kPages, the softmax may be three behind
+constexpr int kMeta = 6 * 128 * 4 + 16;   // cK, cV, aK, bK, aV, bV, 2^eK, eV
+constexpr int kOffK = 0, kOffV = kRing * 2 * kPlane, kOffMeta = 2 * kOffV, kOffScale = kOffMeta + kMetaSlots * kMeta;
+constexpr int kBarBytes = 320, kOffBar = kOffScale + kM * 4, kOffRaw = kOffBar + kBarBytes;
+constexpr int kQRow = 2 * kD * 2 + 16;    // staged query row: hi, lo, padding
+static_assert(kM * kQRow <= kOffMeta, "query rows are staged in the operand rings");
+static_assert(kOffRaw % 16 == 0 && kOffMeta % 1024 == 0, "layout");
+enum { B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SF = 8, B_PF = 10, B_OF = 12, B_FIN = 14, B_RF = 15, B_RE = B_RF + kPages,
+       B_META = B_RE + kPages, kBars = B_META + kMetaSlots };
+static_assert(kBars * 8 + 8 <= kBarBytes, "barriers");
+constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256, kColL = 384;  // tensor-memory columns
+constexpr uint32_t kIdQK = tc_idesc_f16(kM, kStage, false, false), kIdPV = tc_idesc_f16(kM, kD, false, false);
+constexpr int kSmemMax = 232448;
+static_assert(kOffRaw + 2 * 8 * DensePage(kD, 128, 8, 8, 4).bytes() + 1024 <= kSmemMax, "two tiles of the widest pages");
+constexpr long long kWait = 2000000000LL;
+constexpr float kRaise = 8.f;  // log2 of how far a score may pass the running maximum
+
+__device__ __forceinline__ bool probe(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// D (tensor memory) = A (tensor memory) * B^T (+ D if `accumulate`).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// Exponent of a positive normal float, 0 for others (zero, inf, nan, subnormal).
+__device__ __forceinline__ int exponent_of(float x) {
+  const int e = (__float_as_int(x) >> 23) & 255;
+  return e == 0 || e == 255 ? 0 : e - 127;
+}
+
+// hi and lo words of a pair at `off` of the two planes of an operand stage.
+__device__ __forceinline__ void put_pair(unsigned char* plane, uint32_t off, float2 x) {
+  uint32_t hi, lo;
+  split_hi_lo2(x, hi, lo);
+  *reinterpret_cast<uint32_t*>(plane + off) = hi;
+  *reinterpret_cast<uint32_t*>(plane + kPlane + off) = lo;
+}
+
+// K of one page and one group of 64 channels (ch): 16 pairs a lane. page: the
+// raw K part; a, b: the page's 16 row scales (a / kappa, b + a centre); c: the
+// tile's column scales; tok0: the page's first token in the stage.
+template <int KB>
+__device__ __forceinline__ void dequant_k(const unsigned char* page, const float* a, const float* b, const float* c,
+                                          unsigned char* plane, int ch, int tok0, int lane) {
+  constexpr int W0 = plane_w0(KB), W1 = plane_w1(KB), F0 = 8 / W0, F1 = W1 ? 8 / W1 : 8;
+  constexpr int U0 = kD * W0 / 64 < 4 ? kD * W0 / 64 : 4, U1 = W1 ? (kD * W1 / 64 < 4 ? kD * W1 / 64 : 4) : 1;
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t x0[W0], x1[W1 ? W1 : 1];
+  load_words<W0>(page + 4 * U0 * (32 * ((ch * W0) / U0) + lane) + 4 * ((ch * W0) % U0), x0);
+  if constexpr (W1 != 0)
+    load_words<W1>(page + 2 * kD * W0 + 4 * U1 * (32 * ((ch * W1) / U1) + lane) + 4 * ((ch * W1) % U1), x1);
+  const float2 a2[2] = {f2(a[g]), f2(a[8 + g])}, b2[2] = {f2(b[g]), f2(b[8 + g])};
+  unsigned char* dst = plane + ch * (kStage * 128);
+  static_for<0, 4>([&](auto kq) {
+    constexpr int kc = decltype(kq)::value;
+    const float2 c0 = *reinterpret_cast<const float2*>(c + 64 * ch + 16 * kc + 2 * t);
+    const float2 c1 = *reinterpret_cast<const float2*>(c + 64 * ch + 16 * kc + 2 * t + 8);
+    static_for<0, 2>([&](auto ec) {
+      constexpr int e = decltype(ec)::value, fg = 2 * kc + e;
+      uint32_t w0, w1;
+      code_pair<KB, fg % F0, fg % F1>(x0[fg / F0], x1[(fg / F1) % (W1 ? W1 : 1)], w0, w1);
+      const int row = tok0 + 8 * e + g;
+      put_pair(dst, sw128_unit(row, 2 * kc) + 4 * t, f2mul(c0, f2fma(a2[e], __half22float2(u32_as_h2(w0)), b2[e])));
+      put_pair(dst, sw128_unit(row, 2 * kc + 1) + 4 * t, f2mul(c1, f2fma(a2[e], __half22float2(u32_as_h2(w1)), b2[e])));
+    });
+  });
+}
+
+// V of one page (p of the stage) and one group of 64 channels (hq).
+template <int VB>
+__device__ __forceinline__ void dequant_v(const unsigned char* page, const float* a, const float* b, const float* c,
+                                          unsigned char* plane, int hq, int p, int lane) {
+  constexpr int W0 = plane_w0(VB), W1 = plane_w1(VB), F0 = 8 / W0, F1 = W1 ? 8 / W1 : 8;
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t x0[W0], x1[W1 ? W1 : 1];
+  load_words<W0>(page + 4 * W0 * (32 * hq + lane), x0);
+  if constexpr (W1 != 0) load_words<W1>(page + 2 * kD * W0 + 4 * W1 * (32 * hq + lane), x1);
+  const float2 a0 = *reinterpret_cast<const float2*>(a + 2 * t), a1 = *reinterpret_cast<const float2*>(a + 8 + 2 * t);
+  const float2 b0 = *reinterpret_cast<const float2*>(b + 2 * t), b1 = *reinterpret_cast<const float2*>(b + 8 + 2 * t);
+  static_for<0, 8>([&](auto kc) {
+    constexpr int k = decltype(kc)::value;
+    uint32_t w0, w1;
+    code_pair<VB, k % F0, k % F1>(x0[k / F0], x1[(k / F1) % (W1 ? W1 : 1)], w0, w1);
+    const int chan = 64 * hq + 8 * k + g;
+    const float2 c2 = f2(c[chan]);
+    put_pair(plane, sw128_unit(chan, 2 * p) + 4 * t, f2mul(c2, f2fma(a0, __half22float2(u32_as_h2(w0)), b0)));
+    put_pair(plane, sw128_unit(chan, 2 * p + 1) + 4 * t, f2mul(c2, f2fma(a1, __half22float2(u32_as_h2(w1)), b1)));
+  });
+}
+
+__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedTcArgs A) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.x, unit = blockIdx.y;
+  const int kvh = unit % A.Hkv, blk = unit / A.Hkv;
+  const int t0 = split * A.tps, n = min(A.tps, A.tiles - t0);  // this CTA's tiles (n >= 1)
+  const int ppt = A.N / kPageTokens, spt = A.N / kStage, stages = n * spt;
+  unsigned char* sm = smem + ((1024u - (smem_addr(smem) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + kOffBar + kBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kOffBar + kBars * 8 + 4);
+  float* rscale = reinterpret_cast<float*>(sm + kOffScale);
+  // Bounded wait, uniform over the warp; gives up (and tells every role to)
+  // after about a second or once another warp has given up.
+  auto wait = [&](int bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, probe(bars + bar, parity))) return true;
+    bool ok = true;
+    const long long start = clock64();
+    while (!probe(bars + bar, parity)) {
+      if (*abort_flag || clock64() - start > kWait) {
+        ok = false;
+        break;
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) *abort_flag = 1;
+    return ok;
+  };
+
+  if (warp == kMmaWarp) tc_alloc(tslot, 512);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + B_KF + i, kDequant / 32);
+      mbar_init(bars + B_KE + i, 1);
+      mbar_init(bars + B_VF + i, kDequant / 32);
+      mbar_init(bars + B_VE + i, 1);
+      mbar_init(bars + B_SF + i, 1);
+      mbar_init(bars + B_PF + i, kSoftmax / 32);
+      mbar_init(bars + B_OF + i, 1);
+    }
+    for (int i = 0; i < kPages; ++i) {
+      mbar_init(bars + B_RF + i, 1);
+      mbar_init(bars + B_RE + i, kDequant / 32);
+    }
+    for (int i = 0; i < kMetaSlots; ++i) mbar_init(bars + B_META + i, 1);
+    mbar_init(bars + B_FIN, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // The own tokens' decode is launched as this kernel's dependent and may run
+  // beside it (DecArgs::late_wait), so it is let go only behind this wait.
+  pdl_wait_primary();
+  pdl_launch_dependents();
+
+  // ---- query rows: rotated, scaled, hi and lo, by way of shared memory into
+  //      tensor memory. Row r of the block is row 128 blk + r of the KV head:
+  //      token row (128 blk + r) / G, head kvh G + (128 blk + r) % G.
+  const int rows = A.rows_per_head - kM * blk;  // rows used (the others are zero)
+  {
+    constexpr int kWarps = kThreads / 32, kIter = (kM + kWarps - 1) / kWarps;
+    uint2 raw[kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int r = warp + i * kWarps;
+      raw[i] = make_uint2(0u, 0u);
+      if (r < kM && r < rows) {
+        const int pr = kM * blk + r;
+        const int64_t row = static_cast<int64_t>(pr / A.G) * A.Hq + kvh * A.G + pr % A.G;
+        raw[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(A.q) + row * kD + 4 * lane));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int r = warp + i * kWarps;
+      if (r >= kM) break;
+      float v[4];
+      if (A.bf16) {
+        v[0] = __uint_as_float(raw[i].x << 16);
+        v[1] = __uint_as_float(raw[i].x & 0xffff0000u);
+        v[2] = __uint_as_float(raw[i].y << 16);
+        v[3] = __uint_as_float(raw[i].y & 0xffff0000u);
+      } else {
+        const float2 f0 = __half22float2(u32_as_h2(raw[i].x)), f1 = __half22float2(u32_as_h2(raw[i].y));
+        v[0] = f0.x;
+        v[1] = f0.y;
+        v[2] = f1.x;
+        v[3] = f1.y;
+      }
+      warp_fwht<4>(v);
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] *= A.qscale;
+        mx = fmaxf(mx, fabsf(v[e]));
+      }
+      mx = warp_max_xor(mx, 1, 32);
+      const int e = exponent_of(mx);
+      // two factors, each a normal power of two
+      const float down0 = pow2i(-(e / 2)), down1 = pow2i(-(e - e / 2));
+      uint32_t h0, l0, h1, l1;
+      split_hi_lo2(make_float2(v[0] * down0 * down1, v[1] * down0 * down1), h0, l0);
+      split_hi_lo2(make_float2(v[2] * down0 * down1, v[3] * down0 * down1), h1, l1);
+      unsigned char* dst = sm + r * kQRow + 8 * lane;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
+      *reinterpret_cast<uint2*>(dst + 2 * kD) = make_uint2(l0, l1);
+      if (lane == 0) rscale[r] = pow2i(e);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
+  if (warp < kSoftmax / 32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // columns 0-63 hi, 64-127 lo
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 u = *reinterpret_cast<const uint4*>(sm + tid * kQRow + 128 * k + 16 * j);
+        w[4 * j] = u.x;
+        w[4 * j + 1] = u.y;
+        w[4 * j + 2] = u.z;
+        w[4 * j + 3] = u.w;
+      }
+      tc_st32(tl + kColQ + 32 * k, w);
+    }
+    tc_wait_st();
+    tc_fence_before();
+  }
+  __syncthreads();  // the staged rows are read: the rings are free
+  tc_fence_after();
+
+  if (warp < kSoftmax / 32) {
+    // ------------------------------------------------------------- softmax
+    const float kq = rscale[tid];
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    int e0 = 0;  // O is in units of 2^e0
+    for (int s = 0; s < stages; ++s) {
+      const int tile = s / spt;
+      // PV(s - 2) has completed by then; waiting for it keeps the parity of
+      // its barrier in step, since PV(s - 1) is only waited for when O is
+      // rescaled
+      if (s >= 2 && !wait(B_OF + (s & 1), ((s >> 1) & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
+      // the tile's exponents (their barrier can not have gone on by two
+      // phases: eight tiles ahead is further than the copies get)
+      if (!wait(B_SF + (s & 1), (s >> 1) & 1) || !wait(B_META + (tile & (kMetaSlots - 1)), (tile / kMetaSlots) & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float* meta = reinterpret_cast<const float*>(sm + kOffMeta + (tile & (kMetaSlots - 1)) * kMeta);
+      const float k = kq * meta[6 * 128];
+      const int ev = reinterpret_cast<const int*>(meta)[6 * 128 + 1];
+      e0 = reinterpret_cast<const int*>(meta)[6 * 128 + 2];
+      uint32_t x[2][32];
+      const uint32_t scol = tl + kColS + 64 * (s & 1);
+      tc_ld32(scol, x[0]);
+      tc_ld32(scol + 32, x[1]);
+      tc_wait_ld();
+      float mx[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mx[j] = __uint_as_float(x[0][j]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mx[j] = fmaxf(mx[j], __uint_as_float(x[i >> 2][(8 * i + j) & 31]));
+      }
+      const float mt = tree_reduce(mx, [](float a, float b) { return fmaxf(a, b); }) * k;
+      // a score far above the maximum so far: O and l are brought to the new
+      // one. The first stage has nothing to rescale.
+      const bool raise = mt > m + kRaise || (m == -INFINITY && mt > m);
+      if (__any_sync(0xffffffffu, raise)) {
+        const float m_new = raise ? mt : m;
+        const float alpha = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
+        if (s > 0) {
+          if (!wait(B_OF + ((s - 1) & 1), ((s - 1) >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < 2 * kD / 32; ++q) {  // O and its small products
+            uint32_t o[32];
+            tc_ld32(tl + kColO + 32 * q, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (raise ? alpha : 1.f));
+            tc_st32(tl + kColO + 32 * q, o);
+          }
+          tc_wait_st();
+        }
+        if (raise) {
+          l *= alpha;
+          m = m_new;
+        }
+      }
+      const float2 k2 = f2(k), z2 = f2(static_cast<float>(ev) - m);
+      float2 sum[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 z = f2fma(make_float2(__uint_as_float(x[hf][2 * i]), __uint_as_float(x[hf][2 * i + 1])), k2, z2);
+          const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+          sum[i & 3] = f2add(sum[i & 3], p);
+          split_hi_lo2(p, hi[i], lo[i]);
+        }
+        tc_st16(scol + 16 * hf, hi);
+        tc_st16(scol + 32 + 16 * hf, lo);
+      }
+      const float2 st = f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3]));
+      l = fmaf(st.x + st.y, pow2i(-ev), l);
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(bars + B_PF + (s & 1));
+    }
+    // ---- this split's partial: maximum, sum, O in the rotated basis
+    if (ok && (stages < 2 || wait(B_OF + (stages & 1), ((stages - 2) >> 1) & 1)) &&
+        wait(B_OF + ((stages - 1) & 1), ((stages - 1) >> 1) & 1)) {
+      tc_fence_after();
+      const bool row = tid < rows;
+      const int pr = kM * blk + (row ? tid : 0);
+      const int64_t at = static_cast<int64_t>(pr / A.G) * A.Hq + kvh * A.G + pr % A.G;
+      float* part = A.ws + (at * A.slots + split) * kPStride(kD);
+      if (row) {
+        part[0] = m;
+        part[1] = l;
+      }
+      const float u0 = pow2i(e0 / 2), u1 = pow2i(e0 - e0 / 2);
+#pragma unroll 1
+      for (int q = 0; q < kD / 32; ++q) {
+        uint32_t o[32], small[32];
+        tc_ld32(tl + kColO + 32 * q, o);
+        tc_ld32(tl + kColL + 32 * q, small);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(small[i]));
+        if (row)
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(part + 4 + 32 * q + i) =
+                make_float4(__uint_as_float(o[i]) * u0 * u1, __uint_as_float(o[i + 1]) * u0 * u1,
+                            __uint_as_float(o[i + 2]) * u0 * u1, __uint_as_float(o[i + 3]) * u0 * u1);
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ------------------------------------------------------ dequantisation
+    const int w = warp - kSoftmax / 32, p = w & 3, ch = w >> 2;  // page of the stage, 64-channel group
+    int ring = 0;        // page buffer of the tile, and the parity of its use
+    uint32_t use = 0;
+    for (int s = 0; s < stages; ++s) {
+      const int tile = s / spt, sub = s - tile * spt;
+      if (sub == 0) {
+        if (s > 0 && ++ring == A.ring) {
+          ring = 0;
+          use ^= 1;
+        }
+        if (!wait(B_META + (tile & (kMetaSlots - 1)), (tile / kMetaSlots) & 1) || !wait(B_RF + ring, use)) break;
+      }
+      const float* meta = reinterpret_cast<const float*>(sm + kOffMeta + (tile & (kMetaSlots - 1)) * kMeta);
+      const int pg = 4 * sub + p;  // page of the tile
+      const unsigned char* page = sm + kOffRaw + ring * A.tile_bytes + pg * A.page_bytes;
+      const int par = ((s >> 1) & 1) ^ 1, slot = s & 1;
+      if (s >= 2 && !wait(B_KE + slot, par)) break;
+      unsigned char* kpl = sm + kOffK + slot * 2 * kPlane;
+      const float *ka = meta + 256 + 16 * pg, *kb = ka + 128;
+      switch (A.k_bits) {
+        case 2: dequant_k<2>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+        case 3: dequant_k<3>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+        case 4: dequant_k<4>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+        case 5: dequant_k<5>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+        case 6: dequant_k<6>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+        default: dequant_k<8>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+      }
+      fence_proxy_async_smem();  // generic writes -> tensor-core reads
+      __syncwarp();
+      if (lane == 0) arrive(bars + B_KF + slot);
+      if (s >= 2 && !wait(B_VE + slot, par)) break;
+      unsigned char* vpl = sm + kOffV + slot * 2 * kPlane;
+      const float *va = meta + 512 + 16 * pg, *vb = va + 128;
+      const unsigned char* vpage = page + A.k_part;
+      switch (A.v_bits) {
+        case 2: dequant_v<2>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+        case 3: dequant_v<3>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+        case 4: dequant_v<4>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+        case 5: dequant_v<5>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+        case 6: dequant_v<6>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+        default: dequant_v<8>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        arrive(bars + B_VF + slot);
+        if (sub == spt - 1) arrive(bars + B_RE + ring);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ----------------------------------------------------------- MMA issue
+    const uint32_t kb = smem_addr(sm + kOffK), vb = smem_addr(sm + kOffV);
+    auto qk = [&](int s) -> bool {
+      if (!wait(B_KF + (s & 1), (s >> 1) & 1)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t b0 = kb + (s & 1) * 2 * kPlane, d = tmem + kColS + 64 * (s & 1);
+        // the small products first: the accumulator is truncated at every
+        // step, and while it is small that costs nothing
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            const uint32_t off = (ks / 4) * (kStage * 128) + 32 * (ks % 4) + (part == 1 ? kPlane : 0);
+            mma_ts(d, tmem + kColQ + (part == 0 ? 64 : 0) + 8 * ks, tc_desc_sw128(b0 + off, 16, 1024), kIdQK,
+                   part > 0 || ks > 0);
+          }
+        tc_commit(bars + B_SF + (s & 1));
+        tc_commit(bars + B_KE + (s & 1));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = qk(0);
+    if (ok && stages > 1) ok = qk(1);
+    for (int s = 0; ok && s < stages; ++s) {
+      if (!wait(B_VF + (s & 1), (s >> 1) & 1) || !wait(B_PF + (s & 1), (s >> 1) & 1)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t b0 = vb + (s & 1) * 2 * kPlane, a = tmem + kColS + 64 * (s & 1);
+#pragma unroll
+        for (int ks = 0; ks < kStage / 16; ++ks) {
+          const uint64_t hi = tc_desc_sw128(b0 + 32 * ks, 16, 1024), lo = tc_desc_sw128(b0 + kPlane + 32 * ks, 16, 1024);
+          mma_ts(tmem + kColO, a + 8 * ks, hi, kIdPV, s > 0 || ks > 0);
+          mma_ts(tmem + kColL, a + 32 + 8 * ks, hi, kIdPV, s > 0 || ks > 0);
+          mma_ts(tmem + kColL, a + 8 * ks, lo, kIdPV, true);
+        }
+        tc_commit(bars + B_OF + (s & 1));
+        tc_commit(bars + B_VE + (s & 1));
+      }
+      __syncwarp();
+      if (s + 2 < stages) ok = qk(s + 2);
+    }
+    if (lane == 0) tc_commit(bars + B_FIN);
+    __syncwarp();
+    mbar_wait_bounded(bars + B_FIN, 0, kWait);  // every MMA issued has completed
+  } else {
+    // ------------------------------------------- page copies and scales
+    const int ring = A.ring;
+    auto issue = [&](int tile) {
+      const int slot = tile % ring;
+      const int32_t* pt = A.table + static_cast<int64_t>(t0 + tile) * ppt;
+      if (lane == 0) mbar_arrive_expect_tx(bars + B_RF + slot, A.tile_bytes);
+      __syncwarp();
+      if (lane < ppt) {
+        int phys = pt[lane];
+        if (phys < 0 || phys >= A.num_pages) {
+          set_error(A.err, KVARN_DEVERR_PAGE_RANGE);
+          phys = 0;
+        }
+        bulk_g2s(sm + kOffRaw + slot * A.tile_bytes + lane * A.page_bytes,
+                 A.cache + (static_cast<int64_t>(phys) * A.Hkv + kvh) * A.page_bytes, A.page_bytes, bars + B_RF + slot);
+      }
+    };
+    int issued = min(n, ring);
+    for (int tile = 0; tile < issued; ++tile) issue(tile);
+    int ev0 = 0;
+    for (int tile = 0; tile < n; ++tile) {
+      if (!wait(B_RF + tile % ring, (tile / ring) & 1)) break;
+      const unsigned char* raw = sm + kOffRaw + (tile % ring) * A.tile_bytes;
+      float* meta = reinterpret_cast<float*>(sm + kOffMeta + (tile & (kMetaSlots - 1)) * kMeta);
+      auto scale_at = [&](int byte) -> float {
+        return A.scale_bytes == 4 ? *reinterpret_cast<const float*>(raw + byte)
+                                  : __half2float(*reinterpret_cast<const __half*>(raw + byte));
+      };
+      const int SB = A.scale_bytes, cols = kD * kPageTokens / A.N;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int bits = kv ? A.v_bits : A.k_bits;
+        const int base = (kv ? A.k_part : 0) + 2 * kD * bits;  // the part's scales within a page
+        const float kinv = bits == 2 || bits == 3 ? 2.f : 8.f;  // 1 / code_kappa
+        const float ctr = bits == 3 || bits == 5 || bits == 8 ? static_cast<float>(1 << (bits - 1)) : 0.f;
+        const float top = static_cast<float>((1 << bits) - 1);
+        float row_max = 0.f, col_max = 0.f, cv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = lane + 32 * j;
+          if (i < A.N) {
+            const int at = (i / kPageTokens) * A.page_bytes + base + (i % kPageTokens) * SB;
+            const float a = scale_at(at), b = scale_at(at + SB * kPageTokens);
+            meta[256 + 256 * kv + i] = a * kinv;
+            meta[256 + 256 * kv + 128 + i] = fmaf(a, ctr, b);
+            row_max = fmaxf(row_max, fmaxf(fabsf(b), fabsf(fmaf(a, top, b))));
+          }
+          cv[j] = scale_at((i / cols) * A.page_bytes + base + 2 * SB * kPageTokens + (i % cols) * SB);
+          col_max = fmaxf(col_max, fabsf(cv[j]));
+        }
+        row_max = warp_max_xor(row_max, 1, 32);
+        col_max = warp_max_xor(col_max, 1, 32);
+        int e = exponent_of(row_max) + exponent_of(col_max) + 1;
+        if (kv) {
+          // O keeps the first tile's unit; a tile's difference goes into its
+          // weights, within fp16's range (the largest is 2^kRaise)
+          if (tile == 0) ev0 = max(-100, min(100, e));
+          e = ev0 + max(-6, min(6, e - ev0));
+        } else {
+          e = max(-100, min(100, e));
+        }
+        const float d0 = pow2i(-(e / 2)), d1 = pow2i(-(e - e / 2));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) meta[128 * kv + lane + 32 * j] = cv[j] * d0 * d1;
+        if (lane == 0) {
+          if (kv) {
+            reinterpret_cast<int*>(meta)[6 * 128 + 1] = e - ev0;
+            reinterpret_cast<int*>(meta)[6 * 128 + 2] = ev0;
+          } else {
+            meta[6 * 128] = pow2i(e);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) arrive(bars + B_META + (tile & (kMetaSlots - 1)));
+      // the tile before this one is converted: its buffer takes the next copy
+      if (tile >= 1 && issued < n) {
+        if (!wait(B_RE + (tile - 1) % ring, ((tile - 1) / ring) & 1)) break;
+        fence_proxy_async_smem();
+        issue(issued++);
+      }
+    }
+    // copies still in flight land before the CTA exits
+    for (int tile = max(0, issued - ring); tile < issued; ++tile)
+      mbar_wait_bounded(bars + B_RF + tile % ring, (tile / ring) & 1, kWait);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tc_dealloc(tmem, 512);
+  }
+  if (tid == 0 && *abort_flag) set_error(A.err, KVARN_DEVERR_TIMEOUT);
+}
+
+}  // namespace
+
+int shared_tc_splits(int units, int tiles, int stages_per_tile, int* tps) {
+  // A split of t tiles costs its stages and about four stages more (query
+  // rows, pipeline fill, partial); one CTA per SM, so the call takes
+  // ceil(units x splits / SMs) such rounds: the split length of least cost.
+  const int sms = device_sm_count();
+  int64_t best = -1;
+  for (int k = 1; k <= tiles && k <= 2 * sms; ++k) {
+    const int t = (tiles + k - 1) / k;
+    const int splits = (tiles + t - 1) / t;
+    const int64_t rounds = (static_cast<int64_t>(units) * splits + sms - 1) / sms;
+    const int64_t cost = rounds * (t * stages_per_tile + 4);
+    if (best < 0 || cost < best) {
+      best = cost;
+      *tps = t;
+    }
+  }
+  return (tiles + *tps - 1) / *tps;
+}
+
+cudaError_t launch_shared_tc(const SharedTcArgs& args, int units, cudaStream_t st) {
+  SharedTcArgs A = args;
+  A.ring = std::min(kPages, (kSmemMax - 1024 - kOffRaw) / A.tile_bytes);  // two at least: the largest tile has 35840 bytes
+  const int smem = kOffRaw + A.ring * A.tile_bytes + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(A.slots, units);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_tc_kernel, A);
+}
+
+}  // namespace kvarn

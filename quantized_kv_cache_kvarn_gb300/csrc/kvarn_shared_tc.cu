@@ -19,21 +19,25 @@
 // column scales change q' with every tile and their row scales the output:
 // 576 + 320 more issue slots per SM and tile than this form spends.
 //
-// Roles (448 threads, one CTA per SM):
-//   warps 0-3    softmax: thread = row = tensor-memory lane. Reads the 64
-//                scores, keeps the running maximum (raised only when a score
-//                passes it by 2^8, so that O is rescaled a few times at most)
-//                and sum, writes P hi / lo over the scores as the A operand
-//   warps 4-11   dequantisation, warp = (page of the stage, 64-channel group):
-//                code planes -> exact fp16 (the decode's conversions) -> fp32
-//                c (a code + b) -> hi and lo, stored in the B operands'
-//                128-byte-swizzled rows: K as token rows of channels, V as
-//                channel rows of tokens, which is how the pages' fragments
-//                pair their codes, so every store is one conflict-free word
-//   warp 12      MMA issue: QK of stage s + 2 behind PV of stage s, so that the
+// Roles (896 threads, one CTA per SM; registers moved to them with setmaxnreg):
+//   warps 0-7    softmax: two threads per row (= tensor-memory lane), 32 of
+//                the stage's 64 tokens each; a pair of warps exchanges its
+//                maxima through shared memory. Keeps the running maximum
+//                (raised only when a score passes it by 2^8, so that O is
+//                rescaled a few times at most) and sum, writes P hi / lo over
+//                the scores as the A operand
+//   warps 8-23   dequantisation, K on eight and V on eight, warp = (page of the
+//                stage, 64-channel group): code planes -> exact fp16 (the
+//                decode's conversions) -> fp32 c (a code + b) -> hi and lo,
+//                stored in the B operands' 128-byte-swizzled rows: K as token
+//                rows of channels, V as channel rows of tokens, which is how
+//                the pages' fragments pair their codes, so every store is one
+//                conflict-free word
+//   warp 24      MMA issue: QK of stage s + 2 behind PV of stage s, so that the
 //                tensor pipe has work while the softmax runs
-//   warp 13      page copies (bulk copies, two tiles in flight) and, per tile,
-//                the scales unpacked to fp32 and the two exponents
+//   warps 25, 26 page copies (bulk copies, up to four tiles in flight) and, per
+//                tile, the scales of K and of V unpacked to fp32 and their
+//                exponents
 // Tensor memory: q' hi, lo 128 columns; S (then P) 2 x 64; O 128, and 128 for
 // the sum of its small products (lo hi + hi lo): the tensor cores truncate the
 // accumulator at every step, so the long sum takes four steps a stage instead
@@ -56,20 +60,23 @@ namespace kvarn {
 namespace {
 
 constexpr int kD = 128, kM = 128, kStage = 64;  // channels, rows of a CTA, tokens of a stage
-constexpr int kSoftmax = 128, kDequant = 256, kThreads = kSoftmax + kDequant + 64;
-constexpr int kMmaWarp = (kSoftmax + kDequant) / 32;  // the page copies' warp follows it
+constexpr int kSoftmax = 256, kDequant = 512, kThreads = kSoftmax + kDequant + 128;
+constexpr int kMmaWarp = (kSoftmax + kDequant) / 32;  // then the page copies' and scales' two
+// registers per thread: at launch, then per role (whole warpgroups)
+constexpr int kRegs = 72, kRegsSoftmax = 96, kRegsDequant = 64, kRegsOther = 56;
+static_assert(kSoftmax * kRegsSoftmax + kDequant * kRegsDequant + 128 * kRegsOther <= kThreads * kRegs, "register split");
 constexpr int kPlane = kStage * kD * 2;   // hi or lo operand plane: 16 KB
 constexpr int kRing = 2;                  // stages of K and of V in flight
 constexpr int kPages = 4;                 // most tiles whose pages are in shared memory or on their way
 constexpr int kMetaSlots = 8;             // tiles whose scales are kept: past kPages, the softmax may be three behind
 constexpr int kMeta = 6 * 128 * 4 + 16;   // cK, cV, aK, bK, aV, bV, 2^eK, eV
 constexpr int kOffK = 0, kOffV = kRing * 2 * kPlane, kOffMeta = 2 * kOffV, kOffScale = kOffMeta + kMetaSlots * kMeta;
-constexpr int kBarBytes = 320, kOffBar = kOffScale + kM * 4, kOffRaw = kOffBar + kBarBytes;
+constexpr int kBarBytes = 384, kOffMax = kOffScale + kM * 4, kOffBar = kOffMax + 4 * kM * 4, kOffRaw = kOffBar + kBarBytes;
 constexpr int kQRow = 2 * kD * 2 + 16;    // staged query row: hi, lo, padding
 static_assert(kM * kQRow <= kOffMeta, "query rows are staged in the operand rings");
 static_assert(kOffRaw % 16 == 0 && kOffMeta % 1024 == 0, "layout");
 enum { B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SF = 8, B_PF = 10, B_OF = 12, B_FIN = 14, B_RF = 15, B_RE = B_RF + kPages,
-       B_META = B_RE + kPages, kBars = B_META + kMetaSlots };
+       B_META = B_RE + kPages, B_X = B_META + kMetaSlots, kBars = B_X + 8 };
 static_assert(kBars * 8 + 8 <= kBarBytes, "barriers");
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256, kColL = 384;  // tensor-memory columns
 constexpr uint32_t kIdQK = tc_idesc_f16(kM, kStage, false, false), kIdPV = tc_idesc_f16(kM, kD, false, false);
@@ -91,6 +98,16 @@ __device__ __forceinline__ bool probe(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+
+// One thread of the warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // D (tensor memory) = A (tensor memory) * B^T (+ D if `accumulate`).
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
@@ -170,7 +187,7 @@ __device__ __forceinline__ void dequant_v(const unsigned char* page, const float
 
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedTcArgs A) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int split = blockIdx.x, unit = blockIdx.y;
   const int kvh = unit % A.Hkv, blk = unit / A.Hkv;
   const int t0 = split * A.tps, n = min(A.tps, A.tiles - t0);  // this CTA's tiles (n >= 1)
@@ -200,9 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   if (warp == kMmaWarp) tc_alloc(tslot, 512);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + B_KF + i, kDequant / 32);
+      mbar_init(bars + B_KF + i, kDequant / 64);
       mbar_init(bars + B_KE + i, 1);
-      mbar_init(bars + B_VF + i, kDequant / 32);
+      mbar_init(bars + B_VF + i, kDequant / 64);
       mbar_init(bars + B_VE + i, 1);
       mbar_init(bars + B_SF + i, 1);
       mbar_init(bars + B_PF + i, kSoftmax / 32);
@@ -212,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       mbar_init(bars + B_RF + i, 1);
       mbar_init(bars + B_RE + i, kDequant / 32);
     }
-    for (int i = 0; i < kMetaSlots; ++i) mbar_init(bars + B_META + i, 1);
+    for (int i = 0; i < kMetaSlots; ++i) mbar_init(bars + B_META + i, 2);
+    for (int i = 0; i < 8; ++i) mbar_init(bars + B_X + i, 2);
     mbar_init(bars + B_FIN, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -281,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
-  if (warp < kSoftmax / 32) {
+  if (warp < kM / 32) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {  // columns 0-63 hi, 64-127 lo
       uint32_t w[32];
@@ -303,12 +321,27 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 
   if (warp < kSoftmax / 32) {
     // ------------------------------------------------------------- softmax
-    const float kq = rscale[tid];
+    regs_inc<kRegsSoftmax>();
+    const int r = tid & (kM - 1), half = tid / kM;  // row; tokens [32 half, +32) of every stage
+    // warps w and w + 4 share rows and meet once a stage (bounded, like every
+    // wait): [stage parity][half][row] for what they exchange
+    float* xch = reinterpret_cast<float*>(sm + kOffMax);
+    auto meet = [&](int s, float mine, float& other) -> bool {
+      xch[((s & 1) * 2 + half) * kM + r] = mine;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(bars + B_X + 2 * (warp & 3) + (s & 1));
+      const bool met = wait(B_X + 2 * (warp & 3) + (s & 1), (s >> 1) & 1);
+      tc_fence_after();
+      other = xch[((s & 1) * 2 + (half ^ 1)) * kM + r];
+      return met;
+    };
+    const float kq = rscale[r];
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     int e0 = 0;  // O is in units of 2^e0
     for (int s = 0; s < stages; ++s) {
-      const int tile = s / spt;
+      const int tile = spt == 1 ? s : s >> 1;
       // PV(s - 2) has completed by then; waiting for it keeps the parity of
       // its barrier in step, since PV(s - 1) is only waited for when O is
       // rescaled
@@ -327,21 +360,27 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       const float k = kq * meta[6 * 128];
       const int ev = reinterpret_cast<const int*>(meta)[6 * 128 + 1];
       e0 = reinterpret_cast<const int*>(meta)[6 * 128 + 2];
-      uint32_t x[2][32];
+      uint32_t x[32];
       const uint32_t scol = tl + kColS + 64 * (s & 1);
-      tc_ld32(scol, x[0]);
-      tc_ld32(scol + 32, x[1]);
+      tc_ld32(scol + 32 * half, x);
       tc_wait_ld();
-      float mx[8];
+      float mx[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mx[j] = __uint_as_float(x[0][j]);
+      for (int j = 0; j < 4; ++j) {
+        mx[j] = __uint_as_float(x[j]);
 #pragma unroll
-        for (int i = 1; i < 8; ++i) mx[j] = fmaxf(mx[j], __uint_as_float(x[i >> 2][(8 * i + j) & 31]));
+        for (int i = 1; i < 8; ++i) mx[j] = fmaxf(mx[j], __uint_as_float(x[4 * i + j]));
       }
-      const float mt = tree_reduce(mx, [](float a, float b) { return fmaxf(a, b); }) * k;
+      const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      float other;
+      if (!meet(s, mine, other)) {  // both have read their scores, too: P may take their place
+        ok = false;
+        break;
+      }
+      const float mt = fmaxf(mine, other) * k;
       // a score far above the maximum so far: O and l are brought to the new
-      // one. The first stage has nothing to rescale.
+      // one. The first stage has nothing to rescale. Half 0 takes O, half 1
+      // its small products.
       const bool raise = mt > m + kRaise || (m == -INFINITY && mt > m);
       if (__any_sync(0xffffffffu, raise)) {
         const float m_new = raise ? mt : m;
@@ -353,13 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           }
           tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q < 2 * kD / 32; ++q) {  // O and its small products
+          for (int q = 0; q < kD / 32; ++q) {
             uint32_t o[32];
-            tc_ld32(tl + kColO + 32 * q, o);
+            const uint32_t col = tl + (half ? kColL : kColO) + 32 * q;
+            tc_ld32(col, o);
             tc_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (raise ? alpha : 1.f));
-            tc_st32(tl + kColO + 32 * q, o);
+            tc_st32(col, o);
           }
           tc_wait_st();
         }
@@ -369,21 +409,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         }
       }
       const float2 k2 = f2(k), z2 = f2(static_cast<float>(ev) - m);
-      float2 sum[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+      float2 sum[2] = {f2(0.f), f2(0.f)};
+      uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 z = f2fma(make_float2(__uint_as_float(x[hf][2 * i]), __uint_as_float(x[hf][2 * i + 1])), k2, z2);
-          const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-          sum[i & 3] = f2add(sum[i & 3], p);
-          split_hi_lo2(p, hi[i], lo[i]);
-        }
-        tc_st16(scol + 16 * hf, hi);
-        tc_st16(scol + 32 + 16 * hf, lo);
+      for (int i = 0; i < 16; ++i) {
+        const float2 z = f2fma(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), k2, z2);
+        const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+        sum[i & 1] = f2add(sum[i & 1], p);
+        split_hi_lo2(p, hi[i], lo[i]);
       }
-      const float2 st = f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3]));
+      // P over the scores: hi in the first 32 columns (16 a half), lo in the last
+      tc_st16(scol + 16 * half, hi);
+      tc_st16(scol + 32 + 16 * half, lo);
+      const float2 st = f2add(sum[0], sum[1]);
       l = fmaf(st.x + st.y, pow2i(-ev), l);
       tc_wait_st();
       tc_fence_before();
@@ -394,38 +432,39 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (ok && (stages < 2 || wait(B_OF + (stages & 1), ((stages - 2) >> 1) & 1)) &&
         wait(B_OF + ((stages - 1) & 1), ((stages - 1) >> 1) & 1)) {
       tc_fence_after();
-      const bool row = tid < rows;
-      const int pr = kM * blk + (row ? tid : 0);
+      const bool row = r < rows;
+      const int pr = kM * blk + (row ? r : 0);
       const int64_t at = static_cast<int64_t>(pr / A.G) * A.Hq + kvh * A.G + pr % A.G;
       float* part = A.ws + (at * A.slots + split) * kPStride(kD);
-      if (row) {
+      float l1;
+      ok = meet(stages, l, l1);
+      if (row && !half) {
         part[0] = m;
-        part[1] = l;
+        part[1] = l + l1;
       }
       const float u0 = pow2i(e0 / 2), u1 = pow2i(e0 - e0 / 2);
 #pragma unroll 1
-      for (int q = 0; q < kD / 32; ++q) {
+      for (int q = 2 * half; q < 2 * half + 2; ++q) {
         uint32_t o[32], small[32];
         tc_ld32(tl + kColO + 32 * q, o);
         tc_ld32(tl + kColL + 32 * q, small);
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(small[i]));
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint((__uint_as_float(o[i]) + __uint_as_float(small[i])) * u0 * u1);
         if (row)
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(part + 4 + 32 * q + i) =
-                make_float4(__uint_as_float(o[i]) * u0 * u1, __uint_as_float(o[i + 1]) * u0 * u1,
-                            __uint_as_float(o[i + 2]) * u0 * u1, __uint_as_float(o[i + 3]) * u0 * u1);
+            *reinterpret_cast<uint4*>(part + 4 + 32 * q + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
       }
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------ dequantisation
-    const int w = warp - kSoftmax / 32, p = w & 3, ch = w >> 2;  // page of the stage, 64-channel group
-    int ring = 0;        // page buffer of the tile, and the parity of its use
+    regs_dec<kRegsDequant>();
+    const int w = warp - kSoftmax / 32, p = w & 3, ch = (w >> 2) & 1, kv = w >> 3;  // page of the stage, 64-channel group
+    int ring = 0;  // page buffer of the tile, and the parity of its use
     uint32_t use = 0;
     for (int s = 0; s < stages; ++s) {
-      const int tile = s / spt, sub = s - tile * spt;
+      const int tile = spt == 1 ? s : s >> 1, sub = spt == 1 ? 0 : s & 1;
       if (sub == 0) {
         if (s > 0 && ++ring == A.ring) {
           ring = 0;
@@ -436,58 +475,60 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       const float* meta = reinterpret_cast<const float*>(sm + kOffMeta + (tile & (kMetaSlots - 1)) * kMeta);
       const int pg = 4 * sub + p;  // page of the tile
       const unsigned char* page = sm + kOffRaw + ring * A.tile_bytes + pg * A.page_bytes;
-      const int par = ((s >> 1) & 1) ^ 1, slot = s & 1;
-      if (s >= 2 && !wait(B_KE + slot, par)) break;
-      unsigned char* kpl = sm + kOffK + slot * 2 * kPlane;
-      const float *ka = meta + 256 + 16 * pg, *kb = ka + 128;
-      switch (A.k_bits) {
-        case 2: dequant_k<2>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
-        case 3: dequant_k<3>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
-        case 4: dequant_k<4>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
-        case 5: dequant_k<5>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
-        case 6: dequant_k<6>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
-        default: dequant_k<8>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+      const int slot = s & 1;
+      if (s >= 2 && !wait((kv ? B_VE : B_KE) + slot, ((s >> 1) & 1) ^ 1)) break;
+      if (kv == 0) {
+        unsigned char* kpl = sm + kOffK + slot * 2 * kPlane;
+        const float *ka = meta + 256 + 16 * pg, *kb = ka + 128;
+        switch (A.k_bits) {
+          case 2: dequant_k<2>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+          case 3: dequant_k<3>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+          case 4: dequant_k<4>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+          case 5: dequant_k<5>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+          case 6: dequant_k<6>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+          default: dequant_k<8>(page, ka, kb, meta, kpl, ch, 16 * p, lane); break;
+        }
+      } else {
+        unsigned char* vpl = sm + kOffV + slot * 2 * kPlane;
+        const float *va = meta + 512 + 16 * pg, *vb = va + 128;
+        const unsigned char* vpage = page + A.k_part;
+        switch (A.v_bits) {
+          case 2: dequant_v<2>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+          case 3: dequant_v<3>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+          case 4: dequant_v<4>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+          case 5: dequant_v<5>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+          case 6: dequant_v<6>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+          default: dequant_v<8>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
+        }
       }
       fence_proxy_async_smem();  // generic writes -> tensor-core reads
       __syncwarp();
-      if (lane == 0) arrive(bars + B_KF + slot);
-      if (s >= 2 && !wait(B_VE + slot, par)) break;
-      unsigned char* vpl = sm + kOffV + slot * 2 * kPlane;
-      const float *va = meta + 512 + 16 * pg, *vb = va + 128;
-      const unsigned char* vpage = page + A.k_part;
-      switch (A.v_bits) {
-        case 2: dequant_v<2>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
-        case 3: dequant_v<3>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
-        case 4: dequant_v<4>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
-        case 5: dequant_v<5>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
-        case 6: dequant_v<6>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
-        default: dequant_v<8>(vpage, va, vb, meta + 128, vpl, ch, p, lane); break;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
       if (lane == 0) {
-        arrive(bars + B_VF + slot);
+        arrive(bars + (kv ? B_VF : B_KF) + slot);
         if (sub == spt - 1) arrive(bars + B_RE + ring);
       }
     }
   } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------- MMA issue
-    const uint32_t kb = smem_addr(sm + kOffK), vb = smem_addr(sm + kOffV);
+    regs_dec<kRegsOther>();
+    // descriptors of the first plane of K and of V; offsets are added in
+    // units of 16 bytes (shared addresses stay below the field's range)
+    const uint64_t kd = tc_desc_sw128(smem_addr(sm + kOffK), 16, 1024), vd = tc_desc_sw128(smem_addr(sm + kOffV), 16, 1024);
     auto qk = [&](int s) -> bool {
       if (!wait(B_KF + (s & 1), (s >> 1) & 1)) return false;
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t b0 = kb + (s & 1) * 2 * kPlane, d = tmem + kColS + 64 * (s & 1);
+      const uint64_t b0 = kd + (s & 1) * (2 * kPlane / 16);
+      const uint32_t d = tmem + kColS + 64 * (s & 1);
+      if (elect_one()) {
         // the small products first: the accumulator is truncated at every
         // step, and while it is small that costs nothing
 #pragma unroll
         for (int part = 0; part < 3; ++part)
 #pragma unroll
-          for (int ks = 0; ks < kD / 16; ++ks) {
-            const uint32_t off = (ks / 4) * (kStage * 128) + 32 * (ks % 4) + (part == 1 ? kPlane : 0);
-            mma_ts(d, tmem + kColQ + (part == 0 ? 64 : 0) + 8 * ks, tc_desc_sw128(b0 + off, 16, 1024), kIdQK,
+          for (int ks = 0; ks < kD / 16; ++ks)
+            mma_ts(d, tmem + kColQ + (part == 0 ? 64 : 0) + 8 * ks,
+                   b0 + ((ks / 4) * (kStage * 128) + 32 * (ks % 4) + (part == 1 ? kPlane : 0)) / 16, kIdQK,
                    part > 0 || ks > 0);
-          }
         tc_commit(bars + B_SF + (s & 1));
         tc_commit(bars + B_KE + (s & 1));
       }
@@ -499,11 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     for (int s = 0; ok && s < stages; ++s) {
       if (!wait(B_VF + (s & 1), (s >> 1) & 1) || !wait(B_PF + (s & 1), (s >> 1) & 1)) break;
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t b0 = vb + (s & 1) * 2 * kPlane, a = tmem + kColS + 64 * (s & 1);
+      const uint64_t b0 = vd + (s & 1) * (2 * kPlane / 16);
+      const uint32_t a = tmem + kColS + 64 * (s & 1);
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < kStage / 16; ++ks) {
-          const uint64_t hi = tc_desc_sw128(b0 + 32 * ks, 16, 1024), lo = tc_desc_sw128(b0 + kPlane + 32 * ks, 16, 1024);
+          const uint64_t hi = b0 + 2 * ks, lo = hi + kPlane / 16;
           mma_ts(tmem + kColO, a + 8 * ks, hi, kIdPV, s > 0 || ks > 0);
           mma_ts(tmem + kColL, a + 32 + 8 * ks, hi, kIdPV, s > 0 || ks > 0);
           mma_ts(tmem + kColL, a + 8 * ks, lo, kIdPV, true);
@@ -514,11 +556,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       __syncwarp();
       if (s + 2 < stages) ok = qk(s + 2);
     }
-    if (lane == 0) tc_commit(bars + B_FIN);
+    if (elect_one()) tc_commit(bars + B_FIN);
     __syncwarp();
     mbar_wait_bounded(bars + B_FIN, 0, kWait);  // every MMA issued has completed
   } else {
     // ------------------------------------------- page copies and scales
+    regs_dec<kRegsOther>();
+    const int kv = warp - kMmaWarp - 1;  // 0: copies and K's scales, 1: V's scales
     const int ring = A.ring;
     auto issue = [&](int tile) {
       const int slot = tile % ring;
@@ -535,66 +579,73 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
                  A.cache + (static_cast<int64_t>(phys) * A.Hkv + kvh) * A.page_bytes, A.page_bytes, bars + B_RF + slot);
       }
     };
-    int issued = min(n, ring);
-    for (int tile = 0; tile < issued; ++tile) issue(tile);
+    int issued = 0;
+    if (kv == 0)
+      for (; issued < min(n, ring); ++issued) issue(issued);
+    const int bits = kv ? A.v_bits : A.k_bits;
+    const int base = (kv ? A.k_part : 0) + 2 * kD * bits;  // the part's scales within a page
+    const float kinv = bits == 2 || bits == 3 ? 2.f : 8.f;  // 1 / code_kappa
+    const float ctr = bits == 3 || bits == 5 || bits == 8 ? static_cast<float>(1 << (bits - 1)) : 0.f;
+    const float top = static_cast<float>((1 << bits) - 1);
+    const int cshift = spt == 1 ? 5 : 4, cmask = (1 << cshift) - 1;  // columns per page: 32 or 16
     int ev0 = 0;
-    for (int tile = 0; tile < n; ++tile) {
+    for (int tile = 0; kv < 2 && tile < n; ++tile) {
       if (!wait(B_RF + tile % ring, (tile / ring) & 1)) break;
-      const unsigned char* raw = sm + kOffRaw + (tile % ring) * A.tile_bytes;
+      const unsigned char* raw = sm + kOffRaw + (tile % ring) * A.tile_bytes + base;
       float* meta = reinterpret_cast<float*>(sm + kOffMeta + (tile & (kMetaSlots - 1)) * kMeta);
-      auto scale_at = [&](int byte) -> float {
-        return A.scale_bytes == 4 ? *reinterpret_cast<const float*>(raw + byte)
-                                  : __half2float(*reinterpret_cast<const __half*>(raw + byte));
-      };
-      const int SB = A.scale_bytes, cols = kD * kPageTokens / A.N;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int bits = kv ? A.v_bits : A.k_bits;
-        const int base = (kv ? A.k_part : 0) + 2 * kD * bits;  // the part's scales within a page
-        const float kinv = bits == 2 || bits == 3 ? 2.f : 8.f;  // 1 / code_kappa
-        const float ctr = bits == 3 || bits == 5 || bits == 8 ? static_cast<float>(1 << (bits - 1)) : 0.f;
-        const float top = static_cast<float>((1 << bits) - 1);
-        float row_max = 0.f, col_max = 0.f, cv[4];
+      float av[4], bv[4], cv[4];
+      auto load = [&](auto sb) {  // this lane's row scales (tokens lane + 32 j) and column scales
+        using T = decltype(sb);
+        constexpr int SB = sizeof(T);
+        auto get = [&](int at) -> float {
+          if constexpr (SB == 4) return *reinterpret_cast<const float*>(raw + at);
+          else return __half2float(*reinterpret_cast<const __half*>(raw + at));
+        };
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = lane + 32 * j;
-          if (i < A.N) {
-            const int at = (i / kPageTokens) * A.page_bytes + base + (i % kPageTokens) * SB;
-            const float a = scale_at(at), b = scale_at(at + SB * kPageTokens);
-            meta[256 + 256 * kv + i] = a * kinv;
-            meta[256 + 256 * kv + 128 + i] = fmaf(a, ctr, b);
-            row_max = fmaxf(row_max, fmaxf(fabsf(b), fabsf(fmaf(a, top, b))));
-          }
-          cv[j] = scale_at((i / cols) * A.page_bytes + base + 2 * SB * kPageTokens + (i % cols) * SB);
-          col_max = fmaxf(col_max, fabsf(cv[j]));
+          const int at = (i / kPageTokens) * A.page_bytes + (i % kPageTokens) * SB;
+          av[j] = i < A.N ? get(at) : 0.f;
+          bv[j] = i < A.N ? get(at + SB * kPageTokens) : 0.f;
+          cv[j] = get((i >> cshift) * A.page_bytes + 2 * SB * kPageTokens + (i & cmask) * SB);
         }
-        row_max = warp_max_xor(row_max, 1, 32);
-        col_max = warp_max_xor(col_max, 1, 32);
-        int e = exponent_of(row_max) + exponent_of(col_max) + 1;
-        if (kv) {
-          // O keeps the first tile's unit; a tile's difference goes into its
-          // weights, within fp16's range (the largest is 2^kRaise)
-          if (tile == 0) ev0 = max(-100, min(100, e));
-          e = ev0 + max(-6, min(6, e - ev0));
-        } else {
-          e = max(-100, min(100, e));
-        }
-        const float d0 = pow2i(-(e / 2)), d1 = pow2i(-(e - e / 2));
+      };
+      if (A.scale_bytes == 4) load(0.f);
+      else load(__half());
+      float row_max = 0.f, col_max = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) meta[128 * kv + lane + 32 * j] = cv[j] * d0 * d1;
-        if (lane == 0) {
-          if (kv) {
-            reinterpret_cast<int*>(meta)[6 * 128 + 1] = e - ev0;
-            reinterpret_cast<int*>(meta)[6 * 128 + 2] = ev0;
-          } else {
-            meta[6 * 128] = pow2i(e);
-          }
+      for (int j = 0; j < 4; ++j) {
+        meta[256 + 256 * kv + lane + 32 * j] = av[j] * kinv;
+        meta[256 + 256 * kv + 128 + lane + 32 * j] = fmaf(av[j], ctr, bv[j]);
+        row_max = fmaxf(row_max, fmaxf(fabsf(bv[j]), fabsf(fmaf(av[j], top, bv[j]))));
+        col_max = fmaxf(col_max, fabsf(cv[j]));
+      }
+      row_max = warp_max_xor(row_max, 1, 32);
+      col_max = warp_max_xor(col_max, 1, 32);
+      int e = exponent_of(row_max) + exponent_of(col_max) + 1;
+      if (kv) {
+        // O keeps the first tile's unit; a tile's difference goes into its
+        // weights, within fp16's range (the largest is 2^kRaise)
+        if (tile == 0) ev0 = max(-100, min(100, e));
+        e = ev0 + max(-6, min(6, e - ev0));
+      } else {
+        e = max(-100, min(100, e));
+      }
+      const float d0 = pow2i(-(e / 2)), d1 = pow2i(-(e - e / 2));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) meta[128 * kv + lane + 32 * j] = cv[j] * d0 * d1;
+      if (lane == 0) {
+        if (kv) {
+          reinterpret_cast<int*>(meta)[6 * 128 + 1] = e - ev0;
+          reinterpret_cast<int*>(meta)[6 * 128 + 2] = ev0;
+        } else {
+          meta[6 * 128] = pow2i(e);
         }
       }
       __syncwarp();
       if (lane == 0) arrive(bars + B_META + (tile & (kMetaSlots - 1)));
       // the tile before this one is converted: its buffer takes the next copy
-      if (tile >= 1 && issued < n) {
+      if (kv == 0 && tile >= 1 && issued < n) {
         if (!wait(B_RE + (tile - 1) % ring, ((tile - 1) / ring) & 1)) break;
         fence_proxy_async_smem();
         issue(issued++);

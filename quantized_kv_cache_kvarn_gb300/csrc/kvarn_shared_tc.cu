@@ -71,12 +71,12 @@ constexpr int kPages = 4;                 // most tiles whose pages are in share
 constexpr int kMetaSlots = 8;             // tiles whose scales are kept: past kPages, the softmax may be three behind
 constexpr int kMeta = 6 * 128 * 4 + 16;   // cK, cV, aK, bK, aV, bV, 2^eK, eV
 constexpr int kOffK = 0, kOffV = kRing * 2 * kPlane, kOffMeta = 2 * kOffV, kOffScale = kOffMeta + kMetaSlots * kMeta;
-constexpr int kBarBytes = 384, kOffMax = kOffScale + kM * 4, kOffBar = kOffMax + 4 * kM * 4, kOffRaw = kOffBar + kBarBytes;
+constexpr int kBarBytes = 320, kOffMax = kOffScale + kM * 4, kOffBar = kOffMax + 4 * kM * 4, kOffRaw = kOffBar + kBarBytes;
 constexpr int kQRow = 2 * kD * 2 + 16;    // staged query row: hi, lo, padding
 static_assert(kM * kQRow <= kOffMeta, "query rows are staged in the operand rings");
 static_assert(kOffRaw % 16 == 0 && kOffMeta % 1024 == 0, "layout");
 enum { B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SF = 8, B_PF = 10, B_OF = 12, B_FIN = 14, B_RF = 15, B_RE = B_RF + kPages,
-       B_META = B_RE + kPages, B_X = B_META + kMetaSlots, kBars = B_X + 8 };
+       B_META = B_RE + kPages, kBars = B_META + kMetaSlots };
 static_assert(kBars * 8 + 8 <= kBarBytes, "barriers");
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256, kColL = 384;  // tensor-memory columns
 constexpr uint32_t kIdQK = tc_idesc_f16(kM, kStage, false, false), kIdPV = tc_idesc_f16(kM, kD, false, false);
@@ -133,56 +133,102 @@ __device__ __forceinline__ void put_pair(unsigned char* plane, uint32_t off, flo
   *reinterpret_cast<uint32_t*>(plane + kPlane + off) = lo;
 }
 
+// The code words of one lane for eight fragments, taken W0 times F0 = 8 / W0
+// fragments: after a step the words move down, so that a step's fragments
+// are always slots 0 .. F0 - 1 of the first word of each plane and the loop
+// over the steps stays rolled (unrolled, the six widths of K and of V, the
+// softmax and the MMA issue of one scheduler do not fit its instruction
+// cache: no-instruction stalls were the largest).
+template <int B>
+struct CodeWords {
+  static constexpr int W0 = plane_w0(B), W1 = plane_w1(B), F0 = 8 / W0;
+  uint32_t x0[W0], x1[W1 ? W1 : 1];
+  template <int SLOT>
+  __device__ __forceinline__ void pair(uint32_t& b0, uint32_t& b1) const {
+    code_pair<B, SLOT, SLOT>(x0[0], x1[0], b0, b1);
+  }
+  __device__ __forceinline__ void next() {
+#pragma unroll
+    for (int i = 0; i + 1 < W0; ++i) x0[i] = x0[i + 1];
+    if constexpr (W1 == 4) {  // two fragments a word, as in the first plane
+#pragma unroll
+      for (int i = 0; i + 1 < W1; ++i) x1[i] = x1[i + 1];
+    } else if constexpr (W1 == 2) {  // four a word, a byte each: two bytes on
+      x1[0] = __funnelshift_r(x1[0], x1[1], 16);
+      x1[1] >>= 16;
+    } else if constexpr (W1 == 1) {  // eight a word, a bit of each byte each
+      x1[0] >>= F0;
+    }
+  }
+};
+
 // K of one page and one group of 64 channels (ch): 16 pairs a lane. page: the
 // raw K part; a, b: the page's 16 row scales (a / kappa, b + a centre); c: the
 // tile's column scales; tok0: the page's first token in the stage.
 template <int KB>
 __device__ __forceinline__ void dequant_k(const unsigned char* page, const float* a, const float* b, const float* c,
                                           unsigned char* plane, int ch, int tok0, int lane) {
-  constexpr int W0 = plane_w0(KB), W1 = plane_w1(KB), F0 = 8 / W0, F1 = W1 ? 8 / W1 : 8;
+  using C = CodeWords<KB>;
+  constexpr int W0 = C::W0, W1 = C::W1;
   constexpr int U0 = kD * W0 / 64 < 4 ? kD * W0 / 64 : 4, U1 = W1 ? (kD * W1 / 64 < 4 ? kD * W1 / 64 : 4) : 1;
   const int g = lane >> 2, t = lane & 3;
-  uint32_t x0[W0], x1[W1 ? W1 : 1];
-  load_words<W0>(page + 4 * U0 * (32 * ((ch * W0) / U0) + lane) + 4 * ((ch * W0) % U0), x0);
+  C x;
+  load_words<W0>(page + 4 * U0 * (32 * ((ch * W0) / U0) + lane) + 4 * ((ch * W0) % U0), x.x0);
   if constexpr (W1 != 0)
-    load_words<W1>(page + 2 * kD * W0 + 4 * U1 * (32 * ((ch * W1) / U1) + lane) + 4 * ((ch * W1) % U1), x1);
+    load_words<W1>(page + 2 * kD * W0 + 4 * U1 * (32 * ((ch * W1) / U1) + lane) + 4 * ((ch * W1) % U1), x.x1);
   const float2 a2[2] = {f2(a[g]), f2(a[8 + g])}, b2[2] = {f2(b[g]), f2(b[8 + g])};
-  unsigned char* dst = plane + ch * (kStage * 128);
-  static_for<0, 4>([&](auto kq) {
-    constexpr int kc = decltype(kq)::value;
-    const float2 c0 = *reinterpret_cast<const float2*>(c + 64 * ch + 16 * kc + 2 * t);
-    const float2 c1 = *reinterpret_cast<const float2*>(c + 64 * ch + 16 * kc + 2 * t + 8);
-    static_for<0, 2>([&](auto ec) {
-      constexpr int e = decltype(ec)::value, fg = 2 * kc + e;
-      uint32_t w0, w1;
-      code_pair<KB, fg % F0, fg % F1>(x0[fg / F0], x1[(fg / F1) % (W1 ? W1 : 1)], w0, w1);
-      const int row = tok0 + 8 * e + g;
-      put_pair(dst, sw128_unit(row, 2 * kc) + 4 * t, f2mul(c0, f2fma(a2[e], __half22float2(u32_as_h2(w0)), b2[e])));
-      put_pair(dst, sw128_unit(row, 2 * kc + 1) + 4 * t, f2mul(c1, f2fma(a2[e], __half22float2(u32_as_h2(w1)), b2[e])));
+  unsigned char* dst = plane + ch * (kStage * 128) + (tok0 + g) * 128 + 4 * t;  // row g of the first token block
+  c += 64 * ch + 2 * t;
+#pragma unroll 1
+  for (int step = 0; step < W0; ++step) {
+    static_for<0, C::F0 / 2>([&](auto kq) {  // k-chunks of the step (16 channels), two token blocks each
+      constexpr int q = decltype(kq)::value;
+      const int kc = step * (C::F0 / 2) + q;
+      const float2 c0 = *reinterpret_cast<const float2*>(c + 16 * kc);
+      const float2 c1 = *reinterpret_cast<const float2*>(c + 16 * kc + 8);
+      const uint32_t u0 = ((2 * kc) ^ g) << 4, u1 = ((2 * kc + 1) ^ g) << 4;  // 128-byte swizzle (rows are g modulo 8)
+      static_for<0, 2>([&](auto ec) {
+        constexpr int e = decltype(ec)::value;
+        uint32_t w0, w1;
+        x.template pair<2 * q + e>(w0, w1);
+        put_pair(dst, 1024 * e + u0, f2mul(c0, f2fma(a2[e], __half22float2(u32_as_h2(w0)), b2[e])));
+        put_pair(dst, 1024 * e + u1, f2mul(c1, f2fma(a2[e], __half22float2(u32_as_h2(w1)), b2[e])));
+      });
     });
-  });
+    x.next();
+  }
 }
 
 // V of one page (p of the stage) and one group of 64 channels (hq).
 template <int VB>
 __device__ __forceinline__ void dequant_v(const unsigned char* page, const float* a, const float* b, const float* c,
                                           unsigned char* plane, int hq, int p, int lane) {
-  constexpr int W0 = plane_w0(VB), W1 = plane_w1(VB), F0 = 8 / W0, F1 = W1 ? 8 / W1 : 8;
+  using C = CodeWords<VB>;
+  constexpr int W0 = C::W0, W1 = C::W1;
   const int g = lane >> 2, t = lane & 3;
-  uint32_t x0[W0], x1[W1 ? W1 : 1];
-  load_words<W0>(page + 4 * W0 * (32 * hq + lane), x0);
-  if constexpr (W1 != 0) load_words<W1>(page + 2 * kD * W0 + 4 * W1 * (32 * hq + lane), x1);
+  C x;
+  load_words<W0>(page + 4 * W0 * (32 * hq + lane), x.x0);
+  if constexpr (W1 != 0) load_words<W1>(page + 2 * kD * W0 + 4 * W1 * (32 * hq + lane), x.x1);
   const float2 a0 = *reinterpret_cast<const float2*>(a + 2 * t), a1 = *reinterpret_cast<const float2*>(a + 8 + 2 * t);
   const float2 b0 = *reinterpret_cast<const float2*>(b + 2 * t), b1 = *reinterpret_cast<const float2*>(b + 8 + 2 * t);
-  static_for<0, 8>([&](auto kc) {
-    constexpr int k = decltype(kc)::value;
-    uint32_t w0, w1;
-    code_pair<VB, k % F0, k % F1>(x0[k / F0], x1[(k / F1) % (W1 ? W1 : 1)], w0, w1);
-    const int chan = 64 * hq + 8 * k + g;
-    const float2 c2 = f2(c[chan]);
-    put_pair(plane, sw128_unit(chan, 2 * p) + 4 * t, f2mul(c2, f2fma(a0, __half22float2(u32_as_h2(w0)), b0)));
-    put_pair(plane, sw128_unit(chan, 2 * p + 1) + 4 * t, f2mul(c2, f2fma(a1, __half22float2(u32_as_h2(w1)), b1)));
-  });
+  unsigned char* dst0 = plane + (64 * hq + g) * 128 + (((2 * p) ^ g) << 4) + 4 * t;  // channel row g of the first block
+  unsigned char* dst1 = plane + (64 * hq + g) * 128 + (((2 * p + 1) ^ g) << 4) + 4 * t;
+  c += 64 * hq + g;
+#pragma unroll 1
+  for (int step = 0; step < W0; ++step) {
+    static_for<0, C::F0>([&](auto kc) {  // channel blocks of the step
+      constexpr int k = decltype(kc)::value;
+      uint32_t w0, w1;
+      x.template pair<k>(w0, w1);
+      const float2 c2 = f2(c[8 * k]);
+      put_pair(dst0, 1024 * k, f2mul(c2, f2fma(a0, __half22float2(u32_as_h2(w0)), b0)));
+      put_pair(dst1, 1024 * k, f2mul(c2, f2fma(a1, __half22float2(u32_as_h2(w1)), b1)));
+    });
+    x.next();
+    c += 8 * C::F0;
+    dst0 += 1024 * C::F0;
+    dst1 += 1024 * C::F0;
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedTcArgs A) {
@@ -230,7 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       mbar_init(bars + B_RE + i, kDequant / 32);
     }
     for (int i = 0; i < kMetaSlots; ++i) mbar_init(bars + B_META + i, 2);
-    for (int i = 0; i < 8; ++i) mbar_init(bars + B_X + i, 2);
     mbar_init(bars + B_FIN, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -323,18 +368,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     // ------------------------------------------------------------- softmax
     regs_inc<kRegsSoftmax>();
     const int r = tid & (kM - 1), half = tid / kM;  // row; tokens [32 half, +32) of every stage
-    // warps w and w + 4 share rows and meet once a stage (bounded, like every
-    // wait): [stage parity][half][row] for what they exchange
+    // warps w and w + 4 share rows and meet once a stage at a named barrier;
+    // [stage parity][half][row] for what they exchange. The barrier itself
+    // has no time limit: a warp that gives up arrives there once without
+    // waiting (leave), after it has set the abort flag, and its partner
+    // looks at the flag behind the barrier and leaves too.
     float* xch = reinterpret_cast<float*>(sm + kOffMax);
+    const int pair = 1 + (warp & 3);
     auto meet = [&](int s, float mine, float& other) -> bool {
       xch[((s & 1) * 2 + half) * kM + r] = mine;
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive(bars + B_X + 2 * (warp & 3) + (s & 1));
-      const bool met = wait(B_X + 2 * (warp & 3) + (s & 1), (s >> 1) & 1);
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
       tc_fence_after();
       other = xch[((s & 1) * 2 + (half ^ 1)) * kM + r];
-      return met;
+      return __all_sync(0xffffffffu, *abort_flag == 0);
+    };
+    auto leave = [&]() {
+      __syncwarp();
+      asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
     };
     const float kq = rscale[r];
     float m = -INFINITY, l = 0.f;
@@ -347,12 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       // rescaled
       if (s >= 2 && !wait(B_OF + (s & 1), ((s >> 1) & 1) ^ 1)) {
         ok = false;
+        leave();
         break;
       }
       // the tile's exponents (their barrier can not have gone on by two
       // phases: eight tiles ahead is further than the copies get)
       if (!wait(B_SF + (s & 1), (s >> 1) & 1) || !wait(B_META + (tile & (kMetaSlots - 1)), (tile / kMetaSlots) & 1)) {
         ok = false;
+        leave();
         break;
       }
       tc_fence_after();
@@ -388,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         if (s > 0) {
           if (!wait(B_OF + ((s - 1) & 1), ((s - 1) >> 1) & 1)) {
             ok = false;
+            leave();
             break;
           }
           tc_fence_after();
@@ -429,15 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       if (lane == 0) arrive(bars + B_PF + (s & 1));
     }
     // ---- this split's partial: maximum, sum, O in the rotated basis
-    if (ok && (stages < 2 || wait(B_OF + (stages & 1), ((stages - 2) >> 1) & 1)) &&
-        wait(B_OF + ((stages - 1) & 1), ((stages - 1) >> 1) & 1)) {
+    if (ok) {
+      ok = (stages < 2 || wait(B_OF + (stages & 1), ((stages - 2) >> 1) & 1)) &&
+           wait(B_OF + ((stages - 1) & 1), ((stages - 1) >> 1) & 1);
+      if (!ok) leave();
+    }
+    float l1;
+    if (ok && meet(stages, l, l1)) {
       tc_fence_after();
       const bool row = r < rows;
       const int pr = kM * blk + (row ? r : 0);
       const int64_t at = static_cast<int64_t>(pr / A.G) * A.Hq + kvh * A.G + pr % A.G;
       float* part = A.ws + (at * A.slots + split) * kPStride(kD);
-      float l1;
-      ok = meet(stages, l, l1);
       if (row && !half) {
         part[0] = m;
         part[1] = l + l1;

@@ -587,7 +587,7 @@ int32_t kvarn_decode_mass(const void* q, int32_t num_q_heads, float sm_scale, co
  *   keep_tiles         >= sink_tiles + recent_tiles
  * The outputs may be the inputs (mass_out = mass_in and so on); freed is a
  * buffer of its own. A length outside [0, max_seq_len] sets
- * KVARN_DEVERR_SEQ_LEN and is clamped.
+ * KVARN_DEVERR_SEQ_LEN and is clamped. num_seqs is at most 65535.
  */
 int32_t kvarn_evict_tiles(const float* mass_in, float* mass_out, int32_t mass_stride, const int32_t* block_table,
                           int32_t* block_table_out, int32_t* freed, int32_t bt_stride, const int32_t* seq_lens,
@@ -656,7 +656,8 @@ int32_t kvarn_decode_shared(const void* q, int32_t num_q_heads, int32_t num_quer
  *                pos_stride of 0: shared by the batch); any value
  *   inv_freq     device fp64 [R/2], finite
  *   rope_dim     even, rope_offset + rope_dim <= head_dim
- * head_dim is at most KVARN_ROPE_MAX_DIM. Tensors whose addresses and strides
+ * head_dim is at most KVARN_ROPE_MAX_DIM, num_seqs * num_tokens 2^30, the heads
+ * of all tensors 2^20 together. Tensors whose addresses and strides
  * are all multiples of 16 bytes, with R/2 and rope_offset multiples of 16
  * bytes' worth of elements, take the vector path; others one element at a
  * time.

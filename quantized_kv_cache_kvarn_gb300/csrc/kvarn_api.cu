@@ -709,6 +709,7 @@ int32_t kvarn_evict_tiles(const float* mass_in, float* mass_out, int32_t mass_st
       keep_tiles - sink_tiles < recent_tiles)
     return KVARN_EINVAL;
   if (num_seqs == 0) return KVARN_OK;
+  if (num_seqs > 65535) return KVARN_EUNSUPPORTED;
   const int32_t tiles = max_seq_len / L->tile_tokens;
   if (!seq_lens || !seq_lens_out || !freed_count || !error_flags) return KVARN_EINVAL;
   if (tiles > 0 && (!mass_in || !mass_out || !block_table || !block_table_out || !freed || mass_stride < tiles ||
@@ -759,7 +760,7 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
     if (t.head_dim > KVARN_ROPE_MAX_DIM) return KVARN_EUNSUPPORTED;
     heads += t.num_heads;
   }
-  if (heads > (1 << 20) || static_cast<int64_t>(num_seqs) * num_tokens > INT32_MAX) return KVARN_EUNSUPPORTED;
+  if (heads > (1 << 20) || static_cast<int64_t>(num_seqs) * num_tokens > (1 << 30)) return KVARN_EUNSUPPORTED;
   if (num_seqs == 0 || num_tokens == 0 || heads == 0) return KVARN_OK;
   if (!positions || !inv_freq) return KVARN_EINVAL;
   if (!aligned(positions, 4) || !aligned(inv_freq, 8)) return KVARN_EALIGN;
@@ -774,7 +775,6 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
       return KVARN_EINVAL;
     p.t[p.num_tensors++] = {t.in,            t.out,            t.in_seq_stride,   t.in_token_stride, t.in_head_stride,
                             t.out_seq_stride, t.out_token_stride, t.out_head_stride, t.num_heads,      t.head_dim};
-    if (t.in != t.out && t.head_dim > rope_dim) p.copy_rest = 1;
   }
   p.total_heads = static_cast<int32_t>(heads);
   p.dtype = dtype;

@@ -298,40 +298,81 @@ cudaError_t run_decode_kernel(const DecodeParams& p, const DecArgs& A, int ctas,
   return e;
 }
 
-// Attention mass of a tile: its weights summed over the query heads, from
-// each head's (maximum, sum) of the tile and lse: sum l 2^(m - lse log2 e).
-// A CTA takes 32 tiles of a sequence, a warp every 8th head, lanes the tiles
-// (the pairs of a row are contiguous); the warps' sums are added in a fixed
-// order. Reads 8 bytes per head and tile.
-constexpr int kMassWarps = 8;
-__global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(const DecArgs A, int N, const float* lse,
-                                                               const float* mass_in, float* mass_out, int mass_stride,
-                                                               float decay) {
-  __shared__ float part[kMassWarps][32];
+// The merge, and beside it in the same launch (CTAs from merge_ctas on) the
+// attention mass of the tiles: weights summed over the query heads, from each
+// head's (maximum, sum) of the tile and of its whole row, l 2^(m - M) / L. A
+// mass CTA takes 32 tiles of a sequence: its threads form M and 1 / L of up
+// to 128 heads from the decode's partials (so that it does not wait for the
+// merge), then a warp takes every fourth head and the lanes the tiles, whose
+// pairs are contiguous; the warps' sums are added in a fixed order. Reads 8
+// bytes per head and tile; two dependent trips to memory bound it.
+template <int D>
+__global__ void __launch_bounds__(128) merge_mass_kernel(const __grid_constant__ DecArgs A, int N, int rows,
+                                                         int merge_ctas, int mass_x, float* out, float* lse,
+                                                         const float* mass_in, float* mass_out, int mass_stride,
+                                                         float decay) {
+  constexpr int S = kPStride(D);
+  __shared__ float2 whole[128];  // M, 1 / L of a head
+  __shared__ float part[4][32];
   pdl_wait_primary();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
-  const int t = blockIdx.x * 32 + lane, C = seq_tiles(A, N, b);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (static_cast<int>(blockIdx.x) < merge_ctas) {
+    const int row = blockIdx.x * 4 + warp;
+    if (row < rows) merge_row<D, true>(A.ws, A.slots, row, A.counts, 0, A.tile_slots, out, lse);
+    return;
+  }
+  const int item = blockIdx.x - merge_ctas, b = item / mass_x;
+  const int t = item % mass_x * 32 + lane, C = seq_tiles(A, N, b);
   float sum = 0.f;
-  if (t < C) {
-    const float2* st = A.stats + static_cast<int64_t>(b) * A.Hq * A.stat_tiles + t;
-#pragma unroll 8
-    for (int h = warp; h < A.Hq; h += kMassWarps) {
-      const float2 v = st[static_cast<int64_t>(h) * A.stat_tiles];
-      sum = fmaf(v.y, exp2f(v.x - lse[b * A.Hq + h] * kLog2e), sum);
+  for (int h0 = 0; h0 < A.Hq; h0 += 128) {
+    const int h = h0 + threadIdx.x;
+    if (h < A.Hq) {
+      const int row = b * A.Hq + h, nt = min(A.counts[row], A.tile_slots);
+      const float* P = A.ws + static_cast<int64_t>(row) * A.slots * S;
+      float M = -INFINITY, L = 0.f;
+      for (int s = 0; s < A.slots; ++s)
+        if (s < nt || s >= A.tile_slots) M = fmaxf(M, P[s * S]);
+      for (int s = 0; s < A.slots; ++s)
+        if (s < nt || s >= A.tile_slots) L = fmaf(P[s * S + 1], M == -INFINITY ? 0.f : exp2f(P[s * S] - M), L);
+      whole[threadIdx.x] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
     }
+    __syncthreads();
+    if (t < C) {
+      const float2* st = A.stats + (static_cast<int64_t>(b) * A.Hq + h0) * A.stat_tiles + t;
+      const int n = min(128, A.Hq - h0);
+#pragma unroll 8
+      for (int i = warp; i < n; i += 4) {
+        const float2 v = st[static_cast<int64_t>(i) * A.stat_tiles], w = whole[i];
+        sum = fmaf(v.y, exp2f(v.x - w.x) * w.y, sum);
+      }
+    }
+    __syncthreads();
   }
   part[warp][lane] = sum;
   __syncthreads();
   if (warp == 0 && t < A.stat_tiles) {
-#pragma unroll
-    for (int w = 1; w < kMassWarps; ++w) sum += part[w][lane];
     const int64_t at = static_cast<int64_t>(b) * mass_stride + t;
+    sum = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
     mass_out[at] = t < C ? fmaf(decay, mass_in[at], sum) : 0.f;
   }
 }
 
-int64_t mass_workspace_bytes(int64_t rows, int32_t max_tiles) {
-  return rows * max_tiles * 8 + (rows * 4 + 15) / 16 * 16;
+int64_t mass_workspace_bytes(int64_t rows, int32_t max_tiles) { return (rows * max_tiles * 8 + 15) / 16 * 16; }
+
+template <int D>
+static cudaError_t launch_merge_mass(const DecArgs& A, int rows, const DecodeParams& p, cudaStream_t st) {
+  const int merge_ctas = (rows + 3) / 4, mass_x = (A.stat_tiles + 31) / 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(merge_ctas + mass_x * p.num_seqs);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_mass_kernel<D>, A, p.N, rows, merge_ctas, mass_x, p.out, p.lse, p.mass_in,
+                            p.mass_out, p.mass_stride, p.mass_decay);
 }
 
 cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cudaStream_t st) {
@@ -340,31 +381,20 @@ cudaError_t launch_decode_dense(const DecodeParams& p, const DensePlan& plan, cu
   cudaError_t e = dense_args(p, plan, A);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * A.Q * p.num_q_heads;
-  float* lse = p.lse;
   if (p.mass_out) {
     A.stat_tiles = p.max_seq_len / p.N;
     A.stats = reinterpret_cast<float2*>(static_cast<char*>(p.workspace) + dense_stream_workspace_bytes(rows, p.D, plan));
-    if (!lse) lse = reinterpret_cast<float*>(A.stats + rows * A.stat_tiles);
   }
   e = run_decode_kernel(p, A, plan.ctas, st);
   if (e != cudaSuccess) return e;
   if (p.codec != 0)  // the affine and fp16 pages are in the original basis
     return p.D == 128 ? launch_merge<128, false>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st)
                       : launch_merge<256, false>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st);
-  e = p.D == 128 ? launch_merge<128>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, lse, st)
-                 : launch_merge<256>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, lse, st);
-  if (e != cudaSuccess || !p.mass_out || A.stat_tiles == 0) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((A.stat_tiles + 31) / 32, p.num_seqs);
-  cfg.blockDim = dim3(32 * kMassWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mass_kernel, A, p.N, static_cast<const float*>(lse), p.mass_in, p.mass_out,
-                            p.mass_stride, p.mass_decay);
+  if (p.mass_out && A.stat_tiles > 0)
+    return p.D == 128 ? launch_merge_mass<128>(A, static_cast<int>(rows), p, st)
+                      : launch_merge_mass<256>(A, static_cast<int>(rows), p, st);
+  return p.D == 128 ? launch_merge<128>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st)
+                    : launch_merge<256>(A.ws, A.slots, rows, A.counts, 0, A.tile_slots, p.out, p.lse, st);
 }
 
 }  // namespace kvarn

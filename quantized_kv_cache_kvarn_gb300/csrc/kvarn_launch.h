@@ -190,8 +190,7 @@ cudaError_t launch_store_fp16(const StoreFp16Params& p, cudaStream_t st);
 int raw_decode_ctas_per_sm(int32_t D);
 
 // Tile masses of the dense decode: one (base-2 maximum, sum) pair per output
-// row and committed tile in the workspace, and one lse per row where the
-// caller takes none.
+// row and committed tile in the workspace.
 int64_t mass_workspace_bytes(int64_t rows, int32_t max_tiles);
 
 // Rotary positions (kvarn_rope.cu).
@@ -214,7 +213,6 @@ struct RopeParams {
   int32_t interleaved;
   float scale;
   int32_t inverse;
-  int32_t copy_rest;  // some tensor has channels outside the rotated ones to copy
 };
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t st);
 
@@ -232,7 +230,8 @@ struct EvictParams {
   int32_t* lens_out;
   int32_t max_seq_len, num_seqs, N;
   int32_t keep, sink, recent;
-  int32_t key_cap;
+  int32_t range;  // tiles of a CTA (set by the launch)
+  int32_t held;   // whether they fit its shared memory
   uint32_t* err;
 };
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);

@@ -67,15 +67,12 @@ __device__ __forceinline__ void accumulate_slots(const float* P, int stride, int
 // [raw_begin, slots)). The lanes read the slot maxima and sums in parallel.
 // ROT = false: the tile partials are in the original basis too (the affine
 // comparison codec) and are added without the transform.
-template <int D, bool ROT = true>
-__global__ void __launch_bounds__(128) merge_kernel(const float* __restrict__ ws, int slots, int rows,
-                                                    const int32_t* __restrict__ counts, int rotated_slots,
-                                                    int raw_begin, float* out, float* lse) {
+template <int D, bool ROT>
+__device__ __forceinline__ void merge_row(const float* __restrict__ ws, int slots, int row,
+                                          const int32_t* __restrict__ counts, int rotated_slots, int raw_begin,
+                                          float* out, float* lse) {
   constexpr int E = D / 32;
-  pdl_wait_primary();
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= rows) return;
   const int rot_end = counts ? min(counts[row], raw_begin) : rotated_slots;
   auto used = [&](int s) { return s < rot_end || s >= raw_begin; };
   const float* P = ws + static_cast<int64_t>(row) * slots * kPStride(D);
@@ -102,6 +99,15 @@ __global__ void __launch_bounds__(128) merge_kernel(const float* __restrict__ ws
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = fmaf(rot[e], sc, tl[e] * invL);
   if (lse && lane == 0) lse[row] = (M + log2f(L)) * kLn2;
+}
+
+template <int D, bool ROT = true>
+__global__ void __launch_bounds__(128) merge_kernel(const float* __restrict__ ws, int slots, int rows,
+                                                    const int32_t* __restrict__ counts, int rotated_slots,
+                                                    int raw_begin, float* out, float* lse) {
+  pdl_wait_primary();
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row < rows) merge_row<D, ROT>(ws, slots, row, counts, rotated_slots, raw_begin, out, lse);
 }
 
 // Launches the merge as a programmatic dependent of the kernel before it on

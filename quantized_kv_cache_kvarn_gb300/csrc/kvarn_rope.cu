@@ -19,6 +19,8 @@
 // 16-byte vectors a head, kBatch heads in flight (in place, a load can not
 // move above a store by itself). What bounds it is HBM for prompts and the
 // launch for single tokens.
+#include <algorithm>
+
 #include "kvarn_common.cuh"
 #include "kvarn_launch.h"
 
@@ -139,10 +141,12 @@ struct HeadAt {
   }
 };
 
-// Every address a multiple of 16 bytes: `chunks` = R / (2 V) pair chunks of V
-// = 16 / sizeof(T) pairs, two vectors each.
+// Every address a multiple of 16 bytes. A thread owns one column of the head,
+// two vectors of V = 16 / sizeof(T) elements: a pair chunk (V pairs; `chunks` =
+// R / (2 V) of them) or, where outputs are not in place, two vectors of the
+// channels outside the rotated ones.
 template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams A, int tok,
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams A, int columns, int tok,
                                                             int head_slots, int heads_per_y) {
   using V = RopeVec<T>;
   constexpr int N = V::N;
@@ -150,25 +154,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int pairs = A.rope_dim / 2, chunks = pairs / N;
   uint64_t* frac = reinterpret_cast<uint64_t*>(smem);                   // [pairs]
   float2* cs = reinterpret_cast<float2*>(smem + 8 * ((pairs + 1) & ~1));  // [tok][pairs]
-  const int64_t tokens = static_cast<int64_t>(A.num_seqs) * A.num_tokens;
-  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * tok;
+  const int tokens = A.num_seqs * A.num_tokens;  // fits 32 bits
+  const int tok0 = blockIdx.x * tok;
   for (int i = threadIdx.x; i < pairs; i += kRopeThreads) frac[i] = turn_fraction(A.inv_freq[i]);
   __syncthreads();
   for (int i = threadIdx.x; i < tok * pairs; i += kRopeThreads) {
-    const int64_t n = tok0 + i / pairs;
+    const int n = tok0 + i / pairs;
     if (n < tokens) {
-      const int p = A.positions[(n / A.num_tokens) * A.pos_stride + n % A.num_tokens];
+      const int p = A.positions[static_cast<int64_t>(n / A.num_tokens) * A.pos_stride + n % A.num_tokens];
       cs[i] = turn_cos_sin(frac[i % pairs] * static_cast<uint64_t>(static_cast<int64_t>(p)), A.scale, A.inverse);
     }
   }
   __syncthreads();
 
   const int h0 = blockIdx.y * heads_per_y, h1 = min(A.total_heads, h0 + heads_per_y);
-  const int c = threadIdx.x % chunks, tt = (threadIdx.x / chunks) % tok, hs = threadIdx.x / (chunks * tok);
-  const int64_t n = tok0 + tt;
-  if (hs < head_slots && n < tokens) {
-    const int64_t seq = n / A.num_tokens, pos_in = n % A.num_tokens;
-    float cv[N], sv[N];
+  const int c = threadIdx.x % columns, tt = (threadIdx.x / columns) % tok, hs = threadIdx.x / (columns * tok);
+  const int n = tok0 + tt;
+  if (hs >= head_slots || n >= tokens) return;
+  const int seq = n / A.num_tokens, pos_in = n % A.num_tokens;
+  const bool turn = c < chunks;
+  float cv[N], sv[N];
+  int first, second;
+  if (turn) {
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
       const float4 v = *reinterpret_cast<const float4*>(cs + tt * pairs + c * N + e);
@@ -177,55 +184,49 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       cv[e + 1] = v.z;
       sv[e + 1] = v.w;
     }
-    const int first = A.offset + (INTERLEAVED ? 2 * N * c : N * c);
-    const int second = first + (INTERLEAVED ? N : pairs);
-    for (int h = h0 + hs; h < h1; h += kBatch * head_slots) {
-      uint4 x[kBatch], y[kBatch];
-      T* dst[kBatch];
+    first = A.offset + (INTERLEAVED ? 2 * N * c : N * c);
+    second = first + (INTERLEAVED ? N : pairs);
+  } else {
+    const int j = 2 * N * (c - chunks);  // of the channels left over
+    first = j < A.offset ? j : j + A.rope_dim;
+    second = j + N < A.offset ? j + N : j + N + A.rope_dim;
+  }
+  for (int h = h0 + hs; h < h1; h += kBatch * head_slots) {
+    uint4 x[kBatch], y[kBatch];
+    T* dst[kBatch];
+    int width[kBatch];  // channels to write; 0: none
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int hh = h + u * head_slots;
-        if (hh < h1) {
-          const HeadAt at(A, hh, seq, pos_in);
-          const T* src = static_cast<const T*>(A.t[at.k].in) + at.in;
-          dst[u] = static_cast<T*>(A.t[at.k].out) + at.out;
-          x[u] = *reinterpret_cast<const uint4*>(src + first);
-          y[u] = *reinterpret_cast<const uint4*>(src + second);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (h + u * head_slots < h1) {
-          float f[2 * N], r[2 * N];
-          V::unpack(x[u], f);
-          V::unpack(y[u], f + N);
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const int a = INTERLEAVED ? 2 * e : e, b = INTERLEAVED ? 2 * e + 1 : N + e;
-            r[a] = fmaf(f[a], cv[e], -f[b] * sv[e]);
-            r[b] = fmaf(f[a], sv[e], f[b] * cv[e]);
-          }
-          *reinterpret_cast<uint4*>(dst[u] + first) = V::pack(r);
-          *reinterpret_cast<uint4*>(dst[u] + second) = V::pack(r + N);
-        }
+    for (int u = 0; u < kBatch; ++u) {
+      const int hh = h + u * head_slots;
+      width[u] = 0;
+      if (hh < h1) {
+        const HeadAt at(A, hh, seq, pos_in);
+        const RopeTensor& t = A.t[at.k];
+        const T* src = static_cast<const T*>(t.in) + at.in;
+        dst[u] = static_cast<T*>(t.out) + at.out;
+        width[u] = turn || t.in != t.out ? t.dim : 0;
+        if (first < width[u]) x[u] = *reinterpret_cast<const uint4*>(src + first);
+        if (second < width[u]) y[u] = *reinterpret_cast<const uint4*>(src + second);
       }
     }
-  }
-  // channels outside the rotated ones (nothing to do in place)
-  if (!A.copy_rest) return;
-  int dim_max = 0;
-  for (int k = 0; k < A.num_tensors; ++k) dim_max = max(dim_max, A.t[k].dim);
-  const int rest = (dim_max - A.rope_dim) / N;
-  for (int i = threadIdx.x; i < rest * tok * (h1 - h0); i += kRopeThreads) {
-    const int r = i % rest, rt = (i / rest) % tok, h = h0 + i / (rest * tok);
-    const int64_t m = tok0 + rt;
-    if (m >= tokens) continue;
-    const HeadAt at(A, h, m / A.num_tokens, m % A.num_tokens);
-    const RopeTensor& t = A.t[at.k];
-    const int ch = r * N < A.offset ? r * N : r * N + A.rope_dim;
-    if (t.in != t.out && ch < t.dim)
-      *reinterpret_cast<uint4*>(static_cast<T*>(t.out) + at.out + ch) =
-          *reinterpret_cast<const uint4*>(static_cast<const T*>(t.in) + at.in + ch);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (turn && width[u]) {
+        float f[2 * N], r[2 * N];
+        V::unpack(x[u], f);
+        V::unpack(y[u], f + N);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const int a = INTERLEAVED ? 2 * e : e, b = INTERLEAVED ? 2 * e + 1 : N + e;
+          r[a] = fmaf(f[a], cv[e], -f[b] * sv[e]);
+          r[b] = fmaf(f[a], sv[e], f[b] * cv[e]);
+        }
+        x[u] = V::pack(r);
+        y[u] = V::pack(r + N);
+      }
+      if (first < width[u]) *reinterpret_cast<uint4*>(dst[u] + first) = x[u];
+      if (second < width[u]) *reinterpret_cast<uint4*>(dst[u] + second) = y[u];
+    }
   }
 }
 
@@ -268,7 +269,7 @@ cudaError_t launch(const RopeParams& A, cudaStream_t st) {
   constexpr int N = RopeVec<T>::N;
   const int64_t tokens = static_cast<int64_t>(A.num_seqs) * A.num_tokens;
   const int pairs = A.rope_dim / 2, chunks = pairs / N;
-  bool vec = pairs % N == 0 && A.offset % N == 0 && chunks >= 1 && chunks <= kRopeThreads;
+  bool vec = pairs % N == 0 && A.offset % N == 0 && chunks >= 1;  // at most 128 + 128 columns
   for (int k = 0; k < A.num_tensors; ++k) {
     const RopeTensor& t = A.t[k];
     vec = vec && t.dim % N == 0 && (reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) % 16 == 0 &&
@@ -281,10 +282,15 @@ cudaError_t launch(const RopeParams& A, cudaStream_t st) {
     rope_any_kernel<T><<<static_cast<unsigned>(ctas < 16LL * sms ? ctas : 16LL * sms), kRopeThreads, 0, st>>>(A);
     return cudaGetLastError();
   }
-  // Tokens per CTA: as many as the CTA's threads hold, halved while fewer
-  // than four CTAs per SM remain. More tokens share the fractions of a CTA;
-  // the cosines and sines cost the same per token.
-  const int slots = kRopeThreads / chunks;
+  // columns: the pair chunks, then the vectors left over two by two
+  int rest = 0;
+  for (int k = 0; k < A.num_tensors; ++k)
+    if (A.t[k].in != A.t[k].out) rest = std::max(rest, (A.t[k].dim - A.rope_dim) / N);
+  const int columns = chunks + (rest + 1) / 2;
+  // Tokens per CTA: as many as the CTA's threads hold (at most eight), halved
+  // while fewer than four CTAs per SM remain. More tokens share the fractions
+  // of a CTA; the cosines and sines cost the same per token.
+  const int slots = kRopeThreads / columns;
   int tok = 1;
   while (tok * 2 <= slots && tok < 8 && tok * 2 * pairs <= 2048 && (tokens + 2 * tok - 1) / (2 * tok) >= 4LL * sms) tok *= 2;
   const int head_slots = slots / tok;
@@ -298,9 +304,9 @@ cudaError_t launch(const RopeParams& A, cudaStream_t st) {
   const int smem = 8 * ((pairs + 1) & ~1) + 8 * tok * pairs;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
   if (A.interleaved)
-    rope_kernel<T, true><<<grid, kRopeThreads, smem, st>>>(A, tok, head_slots, heads_per_y);
+    rope_kernel<T, true><<<grid, kRopeThreads, smem, st>>>(A, columns, tok, head_slots, heads_per_y);
   else
-    rope_kernel<T, false><<<grid, kRopeThreads, smem, st>>>(A, tok, head_slots, heads_per_y);
+    rope_kernel<T, false><<<grid, kRopeThreads, smem, st>>>(A, columns, tok, head_slots, heads_per_y);
   return cudaGetLastError();
 }
 

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -424,13 +425,6 @@ def _raw_stream(what: str, stream, dev: int) -> int:
     return stream.cuda_stream
 
 
-def _tensor(what: str, name: str, t, dtype, shape):
-    """t is contiguous, of this type and shape."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _refuse(what, f"{name} must be contiguous {dtype} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)} "
-                      f"with strides {t.stride()}")
-
-
 def _row_stride(what: str, name: str, t, dtype, rows: int) -> int:
     """Row stride of a matrix of `rows` rows, contiguous within a row."""
     if t.dtype is dtype and t.dim() == 2:
@@ -451,23 +445,26 @@ def _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspac
     kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
     shape = q.shape
     B, Hkv, D = shape[0], layout.num_kv_heads, layout.head_dim
-    _tensor(what, "q", q, kv_dtype, (*shape[:-1], D))
+    if q.dtype is not kv_dtype or shape[-1] != D or not q.is_contiguous():
+        _refuse(what, f"q must be contiguous {kv_dtype} with head_dim {D}, not {q.dtype} {tuple(shape)}")
     if (cache.dtype is not torch.uint8 or not cache.is_contiguous()
             or cache.numel() < layout.num_pages * Hkv * page_bytes(layout)):
         _refuse(what, "cache is not contiguous bytes of the layout's pages")
     bt_stride = _row_stride(what, "block_table", block_table, torch.int32, B)
-    _tensor(what, "seq_lens", seq_lens, torch.int32, (B,))
-    _tensor(what, "out", out, torch.float32, shape)
-    if lse is not None:
-        _tensor(what, "lse", lse, torch.float32, shape[:-1])
-    if (tail_k is None) != (tail_v is None):
-        _refuse(what, "tail_k and tail_v come together")
-    if tail_k is not None:
-        _tensor(what, "tail_k", tail_k, kv_dtype, (B, Hkv, cap, D))
-        _tensor(what, "tail_v", tail_v, kv_dtype, (B, Hkv, cap, D))
+    if seq_lens.dtype is not torch.int32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+        _refuse(what, f"seq_lens must be a contiguous int32 vector of {B}")
+    if out.dtype is not torch.float32 or out.shape != shape or not out.is_contiguous():
+        _refuse(what, f"out must be contiguous float32 of shape {tuple(shape)}")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:-1] or not lse.is_contiguous()):
+        _refuse(what, f"lse must be contiguous float32 of shape {tuple(shape[:-1])}")
+    if tail_k is not None or tail_v is not None:
+        for t in (tail_k, tail_v):
+            if t is None or t.dtype is not kv_dtype or t.shape != (B, Hkv, cap, D) or not t.is_contiguous():
+                _refuse(what, f"tail_k and tail_v must be contiguous {kv_dtype} of shape {(B, Hkv, cap, D)}")
     if not workspace.is_contiguous():
         _refuse(what, "workspace must be contiguous")
-    _tensor(what, "err", err, torch.int32, (1,))
+    if err.dtype is not torch.int32 or err.numel() != 1:
+        _refuse(what, "err must be one int32")
     return bt_stride
 
 
@@ -512,6 +509,9 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.
     return inv.to(device or "cuda"), scale
 
 
+_ROPE_ROWS = [None] + [(RopeTensor * n, struct.Struct("@" + "PPqqqqqqii" * n)) for n in range(1, 5)]
+
+
 def _rope(what, xs, outs, positions, inv_freq, rope_offset, interleaved, scale, inverse, stream):
     if isinstance(xs, torch.Tensor):
         xs, outs = (xs,), (outs,)
@@ -520,33 +520,42 @@ def _rope(what, xs, outs, positions, inv_freq, rope_offset, interleaved, scale, 
         _refuse(what, "one to four tensors, each with an output")
     x0 = xs[0]
     dtype = x0.dtype
-    if x0.dim() != 4 or dtype not in ROPE_DTYPES:
+    code = ROPE_DTYPES.get(dtype, -1)
+    if x0.dim() != 4 or code < 0:
         _refuse(what, f"tensors must be float16, bfloat16 or float32 [seqs, tokens, heads, head_dim], not {dtype} "
                       f"{tuple(x0.shape)}")
-    B, S = x0.shape[0], x0.shape[1]
+    B, S, _, _ = x0.shape
     dev = _device_of(what, *xs, *outs, positions, inv_freq)
-    arr = (RopeTensor * n)()
-    for k in range(n):
-        x, y = xs[k], outs[k]
-        shape = x.shape
-        if len(shape) != 4 or shape[0] != B or shape[1] != S or y.shape != shape or x.dtype is not dtype or y.dtype is not dtype:
-            _refuse(what, "tensors must share sequences, tokens and type, and each output its tensor's shape")
-        xb, xt, xh, xe = x.stride()
-        yb, yt, yh, ye = y.stride()
-        if (xe != 1 or ye != 1) and shape[3] > 1:
+    rows = []
+    for x, y in zip(xs, outs):
+        shape, strides, ostrides = x.shape, x.stride(), y.stride()
+        if len(shape) != 4 or y.shape != shape or x.dtype is not dtype or y.dtype is not dtype:
+            _refuse(what, "tensors must share their type, and each output its tensor's shape")
+        xb, xt, xh, xe = strides
+        b, t, heads, dim = shape
+        if b != B or t != S:
+            _refuse(what, "tensors must share sequences and tokens")
+        if ostrides != strides or 0 in strides:
+            yb, yt, yh, ye = ostrides
+            if ye != 1 and dim > 1:
+                _refuse(what, "the channels of a head must be contiguous")
+            if (yb == 0 and B > 1) or (yt == 0 and S > 1) or (yh == 0 and heads > 1):
+                _refuse(what, "an output may not be broadcast")
+        else:
+            yb, yt, yh = xb, xt, xh
+        if xe != 1 and dim > 1:
             _refuse(what, "the channels of a head must be contiguous")
-        if (yb == 0 and B > 1) or (yt == 0 and S > 1) or (yh == 0 and shape[2] > 1):
-            _refuse(what, "an output may not be broadcast")
-        arr[k] = (x.data_ptr(), y.data_ptr(), xb, xt, xh, yb, yt, yh, shape[2], shape[3])
-    rows = positions.shape[0] if positions.dim() == 2 else -1
-    if positions.dtype is not torch.int32 or (rows != B and rows != 1) or positions.shape[1] != S or (
-            S > 1 and positions.stride(1) != 1):
+        rows += (x.data_ptr(), y.data_ptr(), xb, xt, xh, yb, yt, yh, heads, dim)
+    pb, ps = positions.stride() if positions.dim() == 2 else (0, 0)
+    shape = positions.shape
+    if positions.dtype is not torch.int32 or not (shape == (B, S) or shape == (1, S)) or (ps != 1 and S > 1):
         _refuse(what, "positions must be int32 [seqs or 1, tokens], rows contiguous")
     if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         _refuse(what, "inv_freq must be a contiguous float64 vector")
-    _check(lib().kvarn_rope(arr, n, ROPE_DTYPES[dtype], B, S, positions.data_ptr(), positions.stride(0) if rows > 1 else 0,
-                            inv_freq.data_ptr(), 2 * inv_freq.numel(), rope_offset, 1 if interleaved else 0, scale,
-                            1 if inverse else 0, _raw_stream(what, stream, dev)), what)
+    array, packer = _ROPE_ROWS[n]
+    _check(lib().kvarn_rope(array.from_buffer_copy(packer.pack(*rows)), n, code, B, S, positions.data_ptr(),
+                            pb if shape[0] > 1 else 0, inv_freq.data_ptr(), 2 * inv_freq.numel(), rope_offset,
+                            1 if interleaved else 0, scale, 1 if inverse else 0, _raw_stream(what, stream, dev)), what)
 
 
 def rope(xs, outs, positions, inv_freq, *, rope_offset=0, interleaved=False, scale=1.0, stream=None):
@@ -606,20 +615,23 @@ def evict_tiles(mass_in, block_table, seq_lens, layout: Layout, max_seq_len, kee
     B = seq_lens.shape[0]
     dev = _device_of(what, mass_in, block_table, seq_lens, mass_out, block_table_out, seq_lens_out, freed, freed_count, err)
     rows = _row_stride(what, "block_table", block_table, torch.int32, B)
-    shape = block_table.shape
+    shape, strides = block_table.shape, block_table.stride()
     for name, t in (("block_table_out", block_table_out), ("freed", freed)):
-        if _row_stride(what, name, t, torch.int32, B) != rows or t.shape != shape:
-            _refuse(what, f"{name} differs from block_table in shape or stride")
+        if t.dtype is not torch.int32 or t.shape != shape or t.stride() != strides:
+            _refuse(what, f"{name} differs from block_table in type, shape or stride")
     masses = _row_stride(what, "mass_in", mass_in, torch.float32, B)
-    if _row_stride(what, "mass_out", mass_out, torch.float32, B) != masses or mass_out.shape != mass_in.shape:
-        _refuse(what, "mass_in and mass_out differ in shape or stride")
-    tiles = max_seq_len // layout.tile_tokens
-    if mass_in.shape[1] < tiles or shape[1] < tiles * (layout.tile_tokens // 16):
+    mshape = mass_in.shape
+    if mass_out.dtype is not torch.float32 or mass_out.shape != mshape or mass_out.stride() != mass_in.stride():
+        _refuse(what, "mass_out differs from mass_in in type, shape or stride")
+    N = layout.tile_tokens
+    tiles = max_seq_len // N
+    if mshape[1] < tiles or shape[1] < tiles * (N // 16):
         _refuse(what, "a table has fewer columns than max_seq_len has tiles")
-    _tensor(what, "seq_lens", seq_lens, torch.int32, (B,))
-    _tensor(what, "seq_lens_out", seq_lens_out, torch.int32, (B,))
-    _tensor(what, "freed_count", freed_count, torch.int32, (B,))
-    _tensor(what, "err", err, torch.int32, (1,))
+    for name, t in (("seq_lens", seq_lens), ("seq_lens_out", seq_lens_out), ("freed_count", freed_count)):
+        if t.dtype is not torch.int32 or t.shape != (B,) or not t.is_contiguous():
+            _refuse(what, f"{name} must be a contiguous int32 vector of {B}")
+    if err.dtype is not torch.int32 or err.numel() != 1:
+        _refuse(what, "err must be one int32")
     _check(lib().kvarn_evict_tiles(mass_in.data_ptr(), mass_out.data_ptr(), masses, block_table.data_ptr(),
                                    block_table_out.data_ptr(), freed.data_ptr(), rows, seq_lens.data_ptr(),
                                    seq_lens_out.data_ptr(), freed_count.data_ptr(), max_seq_len, B, ctypes.byref(layout),

@@ -330,10 +330,23 @@ __global__ void __launch_bounds__(128) merge_mass_kernel(const __grid_constant__
       const int row = b * A.Hq + h, nt = min(A.counts[row], A.tile_slots);
       const float* P = A.ws + static_cast<int64_t>(row) * A.slots * S;
       float M = -INFINITY, L = 0.f;
-      for (int s = 0; s < A.slots; ++s)
-        if (s < nt || s >= A.tile_slots) M = fmaxf(M, P[s * S]);
-      for (int s = 0; s < A.slots; ++s)
-        if (s < nt || s >= A.tile_slots) L = fmaf(P[s * S + 1], M == -INFINITY ? 0.f : exp2f(P[s * S] - M), L);
+      for (int s0 = 0; s0 < A.slots; s0 += 8) {  // eight slots in flight
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int s = s0 + i;
+          const bool used = s < A.slots && (s < nt || s >= A.tile_slots);
+          v[i] = used ? *reinterpret_cast<const float2*>(P + s * S) : make_float2(-INFINITY, 0.f);
+        }
+        float Mn = M;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) Mn = fmaxf(Mn, v[i].x);
+        if (Mn == -INFINITY) continue;
+        L *= exp2f(M - Mn);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) L = fmaf(v[i].y, exp2f(v[i].x - Mn), L);
+        M = Mn;
+      }
       whole[threadIdx.x] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
     }
     __syncthreads();

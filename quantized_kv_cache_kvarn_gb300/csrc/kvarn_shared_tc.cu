@@ -85,18 +85,20 @@ static_assert(kOffRaw + 2 * 8 * DensePage(kD, 128, 8, 8, 4).bytes() + 1024 <= kS
 constexpr long long kWait = 2000000000LL;
 constexpr float kRaise = 8.f;  // log2 of how far a score may pass the running maximum
 
-__device__ __forceinline__ bool probe(uint64_t* bar, uint32_t parity) {
+// Barriers by shared-memory address: one probe (the hardware may hold the
+// thread a short time; with a time hint it would poll with sleeps between),
+// and an arrival.
+__device__ __forceinline__ bool probe(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
-
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // One thread of the warp, always the same.
@@ -243,18 +245,20 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + kOffBar + kBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kOffBar + kBars * 8 + 4);
   float* rscale = reinterpret_cast<float*>(sm + kOffScale);
+  const uint32_t bar0 = smem_addr(bars);
   // Bounded wait, uniform over the warp; gives up (and tells every role to)
-  // after about a second or once another warp has given up.
+  // after about a second or once another warp has given up. The clock and the
+  // flag are looked at every 32 probes only: a waiting warp takes issue slots
+  // from the working ones.
   auto wait = [&](int bar, uint32_t parity) -> bool {
-    if (__all_sync(0xffffffffu, probe(bars + bar, parity))) return true;
-    bool ok = true;
+    const uint32_t at = bar0 + 8 * bar;
+    if (__all_sync(0xffffffffu, probe(at, parity))) return true;
+    bool ok = false;
     const long long start = clock64();
-    while (!probe(bars + bar, parity)) {
-      if (*abort_flag || clock64() - start > kWait) {
-        ok = false;
-        break;
-      }
-    }
+    do {
+#pragma unroll 1
+      for (int i = 0; i < 32 && !ok; ++i) ok = probe(at, parity);
+    } while (!ok && !*abort_flag && clock64() - start <= kWait);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *abort_flag = 1;
     return ok;
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive(bars + B_PF + (s & 1));
+      if (lane == 0) arrive(bar0 + 8 * (B_PF + (s & 1)));
     }
     // ---- this split's partial: maximum, sum, O in the rotated basis
     if (ok) {
@@ -561,8 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       fence_proxy_async_smem();  // generic writes -> tensor-core reads
       __syncwarp();
       if (lane == 0) {
-        arrive(bars + (kv ? B_VF : B_KF) + slot);
-        if (sub == spt - 1) arrive(bars + B_RE + ring);
+        arrive(bar0 + 8 * ((kv ? B_VF : B_KF) + slot));
+        if (sub == spt - 1) arrive(bar0 + 8 * (B_RE + ring));
       }
     }
   } else if (warp == kMmaWarp) {
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         }
       }
       __syncwarp();
-      if (lane == 0) arrive(bars + B_META + (tile & (kMetaSlots - 1)));
+      if (lane == 0) arrive(bar0 + 8 * (B_META + (tile & (kMetaSlots - 1))));
       // the tile before this one is converted: its buffer takes the next copy
       if (kv == 0 && tile >= 1 && issued < n) {
         if (!wait(B_RE + (tile - 1) % ring, ((tile - 1) / ring) & 1)) break;

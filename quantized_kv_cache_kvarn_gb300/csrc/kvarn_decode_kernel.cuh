@@ -187,8 +187,11 @@ struct DecArgs {
   int32_t withhold;       // diagnostic: every copy is announced this many bytes larger (its phase never completes)
   int32_t piece;          // > 0: tiles are cut into pieces of so many within each unit, a CTA per piece in turn, piece k
                           // of a unit into slot k (0: stream-K over the flattened list)
+  int32_t late_trigger;   // let the dependent kernel go only once this call's inputs are complete, so that it may run
+                          // beside this one without waiting (late_wait)
   int32_t late_wait;      // the kernel before on the stream started after this call's inputs were complete (it triggers
-                          // its dependents behind its own wait): run beside it and wait for its end before ending
+                          // its dependents behind its own wait): run beside it. The last CTA alone waits for its end
+                          // before ending, so that this grid does not complete earlier, and the others make room
   int32_t fixed_tiles;    // > 0: every sequence has this many committed tiles and seq_lens is not read
   float2* stats;          // per output row and tile (base-2 maximum, sum) of its scores, or null
   int32_t stat_tiles;     // row length of stats
@@ -1386,7 +1389,7 @@ template <int D, int N, int W, int KB = 4, int VB = 2, int SB = 4, int CD = kCod
 __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_dense_kernel(const __grid_constant__ DecArgs A) {
   using S = DecShape<D, N, W, KB, VB, SB, CD>;
   extern __shared__ __align__(128) unsigned char smem[];
-  pdl_launch_dependents();
+  if (!A.late_trigger) pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   {
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BARS);
@@ -1401,6 +1404,7 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
   // or whatever wrote the queries, lengths or tails): nothing in global
   // memory is read before that kernel has completed
   if (!A.late_wait) pdl_wait_primary();
+  if (A.late_trigger) pdl_launch_dependents();
 
   // ---- raw records: items r = 0, 1, ... of (sequence, unit, raw chunk) go to
   //      the CTAs from the last one down, so that while the grid has CTAs
@@ -1448,7 +1452,7 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
   }
   __syncthreads();  // mbarrier initialisation visible to every warp
   if (A.piece == 0 && (total == 0 || static_cast<int>(blockIdx.x) >= C)) {
-    if (A.late_wait) pdl_wait_primary();
+    if (A.late_wait && blockIdx.x == gridDim.x - 1) pdl_wait_primary();
     return;
   }
 
@@ -1501,7 +1505,7 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
     t1 += A.sink_tiles;
     dead = !dense_segment<D, N, W, KB, VB, SB, CD>(A, smem, b, x, t0, t1, slot, ph, dead) || dead;
   }
-  if (A.late_wait) pdl_wait_primary();
+  if (A.late_wait && blockIdx.x == gridDim.x - 1) pdl_wait_primary();
 }
 
 // The arguments of the decode kernels for a call's parameters, and the kernel

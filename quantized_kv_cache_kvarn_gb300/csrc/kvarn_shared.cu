@@ -152,6 +152,11 @@ cudaError_t launch_decode_shared(const DecodeParams& p, const SharedPlan& plan, 
   DecArgs A;
   cudaError_t e = dense_args(p, plan.own, A);
   if (e != cudaSuccess) return e;
+  // The own tokens go first: their CTAs end at different times, and the
+  // prefix's, which need an SM each, start as they leave.
+  A.late_trigger = 1;
+  e = run_decode_kernel(p, A, plan.own.ctas, st);
+  if (e != cudaSuccess) return e;
   float* pre = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + dense_stream_workspace_bytes(rows, p.D, plan.own));
   const int32_t* pcounts = nullptr;
   const int kb = p.k_bits ? p.k_bits : 4, vb = p.v_bits ? p.v_bits : 2, sb = p.scale_bytes ? p.scale_bytes : 4;
@@ -181,7 +186,6 @@ cudaError_t launch_decode_shared(const DecodeParams& p, const SharedPlan& plan, 
     T.slots = plan.prefix.slots;
     T.err = p.err;
     e = launch_shared_tc(T, plan.tc_units, st);
-    A.late_wait = 1;
   } else {
     DecArgs P;
     DecodeParams pp = p;
@@ -194,9 +198,9 @@ cudaError_t launch_decode_shared(const DecodeParams& p, const SharedPlan& plan, 
     if (e != cudaSuccess) return e;
     P.fixed_tiles = p.skip_tokens / p.N;
     pcounts = P.counts;
+    P.late_wait = 1;
     e = run_decode_kernel(pp, P, plan.prefix.ctas, st);
   }
-  if (e == cudaSuccess) e = run_decode_kernel(p, A, plan.own.ctas, st);
   if (e != cudaSuccess) return e;
   const int shortest = p.skip_tokens + Q - 1 > 0 ? p.skip_tokens + Q - 1 : 1;
   return p.D == 128 ? launch_shared_merge<128>(pre, plan.prefix.slots, pcounts, A, static_cast<int>(rows), shortest, p.out, p.lse, st)

@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     *abort_flag = 0;
     fence_mbar_init();
   }
-  // The own tokens' decode is launched as this kernel's dependent and may run
-  // beside it (DecArgs::late_wait), so it is let go only behind this wait.
-  pdl_wait_primary();
+  // Launched as the dependent of the own tokens' decode, which lets it go
+  // once the call's inputs are complete (DecArgs::late_trigger): it starts as
+  // that kernel's CTAs leave and waits for its end only before ending itself.
   pdl_launch_dependents();
 
   // ---- query rows: rotated, scaled, hi and lo, by way of shared memory into
@@ -724,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     tc_dealloc(tmem, 512);
   }
   if (tid == 0 && *abort_flag) set_error(A.err, KVARN_DEVERR_TIMEOUT);
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) pdl_wait_primary();
 }
 
 }  // namespace

@@ -48,10 +48,13 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const float* __restri
   for (int s = lane; s < slots; s += 32)
     if (used(s)) M = fmaxf(M, O[s * S]);
   M = warp_max_xor(M, 1, 32);
-  if (len < shortest || M == -INFINITY) {  // nothing to see, as in the plain decode's merge
-    if (len != 0 && len < shortest && threadIdx.x == 0) set_error(err, KVARN_DEVERR_SEQ_LEN);
-    for (int j = threadIdx.x; j < D; j += 128) o[j] = 0.f;
-    if (lse && threadIdx.x == 0) lse[row] = -INFINITY;
+  if (len < shortest || M == -INFINITY) {
+    // a padding row; or a row that sees the prefix without one finite score
+    // (a query of nan or infinities), whose softmax is undefined
+    const bool undefined = len >= shortest;
+    if (len != 0 && !undefined && threadIdx.x == 0) set_error(err, KVARN_DEVERR_SEQ_LEN);
+    for (int j = threadIdx.x; j < D; j += 128) o[j] = undefined ? NAN : 0.f;
+    if (lse && threadIdx.x == 0) lse[row] = undefined ? NAN : -INFINITY;
     return;
   }
   float rot[E], raw[E], L = 0.f;
@@ -115,11 +118,23 @@ cudaError_t launch_shared_merge(const float* pre, int pslots, const int32_t* pco
                             shortest, out, lse, A.err);
 }
 
-// Rows of a KV head from which the tensor-core kernel takes the prefix: it
-// spends the time of 128 rows on any number of them.
-#ifndef KVARN_SHARED_TC_ROWS
-#define KVARN_SHARED_TC_ROWS 16
-#endif
+// Whether the tensor-core kernel takes the prefix (head_dim 128). It spends
+// the time of 128 rows on any number of them and starts later (its CTAs need
+// an SM each), so the dense decode kernel keeps short prefixes and few rows.
+// Estimated beyond what both share, in ns of the whole GPU, from calls
+// with 16 to 256 rows of 1 and 8 KV heads over 1024 to 16384 tokens (K4V2,
+// us, dense / tensor cores: 8 x 32 rows over 16384 tokens 34 / 44, 8 x 64 rows
+// 46 / 44, 8 x 256 rows 127 / 68; over 4096 tokens 8 x 96 rows 28 / 32, 8 x 128
+// rows 36 / 33; over 1024 tokens 8 x 128 rows 18 / 28):
+//   dense: 4.5 per (eight rows, 128 tokens), 2.5 more for a width of two code
+//          planes (K or V each), 4 more for 8-bit K and V (two-warp CTAs)
+//   tensor cores: 10000, and 11.5 per (128 rows, 64 tokens)
+bool prefix_on_tensor_cores(int64_t rows_per_head, int64_t heads, int64_t tokens, int kb, int vb) {
+  const double per = 4.5 + (plane_w1(kb) ? 2.5 : 0.0) + (plane_w1(vb) ? 2.5 : 0.0) + (kb + vb == 16 ? 4.0 : 0.0);
+  const double dense = per * static_cast<double>((rows_per_head + 7) / 8 * heads) * static_cast<double>(tokens) / 128.0;
+  const double tc = 10000.0 + 11.5 * static_cast<double>((rows_per_head + 127) / 128 * heads) * static_cast<double>(tokens) / 64.0;
+  return dense > tc;
+}
 
 }  // namespace
 
@@ -129,7 +144,7 @@ SharedPlan plan_shared(int32_t num_seqs, int32_t num_kv_heads, int32_t G, int32_
   s.own = plan_dense_pieces(num_seqs, num_kv_heads * row_groups(G, num_queries), own_tiles, D, N, raw_max, kb, vb, sb);
   const int64_t rows = static_cast<int64_t>(num_seqs) * num_queries * G;
   const int64_t units = (rows + 127) / 128 * num_kv_heads;
-  if (D == 128 && rows >= KVARN_SHARED_TC_ROWS && units <= 65535 && prefix_tiles > 0) {
+  if (D == 128 && units <= 65535 && prefix_on_tensor_cores(rows, num_kv_heads, static_cast<int64_t>(prefix_tiles) * N, kb, vb)) {
     s.tc_units = static_cast<int32_t>(units);
     s.prefix.slots = s.prefix.tile_slots = shared_tc_splits(s.tc_units, prefix_tiles, N / 64, &s.tc_tps);
     return s;

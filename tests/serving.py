@@ -14,7 +14,8 @@ class Batch:
     """Sequences over pages the oracle wrote: a shared prefix (whole tiles,
     possibly none) and each sequence's own tokens, the last ones raw."""
 
-    def __init__(self, D, N, Hq, Hkv, lens, Q=1, prefix=0, dtype=torch.float16, widths=(4, 2, 4), seed=0, peak=2.0):
+    def __init__(self, D, N, Hq, Hkv, lens, Q=1, prefix=0, dtype=torch.float16, widths=(4, 2, 4), seed=0, peak=2.0,
+                 size=1.0, first=1.0):
         g = torch.Generator().manual_seed(seed)
         kb, vb, sb = widths
         self.D, self.N, self.Hq, self.Hkv, self.Q, self.prefix, self.dtype = D, N, Hq, Hkv, Q, prefix, dtype
@@ -32,9 +33,10 @@ class Batch:
         self.bt = np.full((B, max(1, longest // 16)), -1, np.int32)
         self.prefix_table = order[:prefix // 16].copy()
 
-        def rows(n):  # [1, Hkv, n, D], one channel of ten larger
-            x = torch.randn((1, Hkv, n, D), generator=g)
+        def rows(n):  # [1, Hkv, n, D], one channel of ten larger; the values' size, and the first tile's
+            x = size * torch.randn((1, Hkv, n, D), generator=g)
             x[..., ::10] *= 3.0
+            x[:, :, :N] *= first if n == prefix else 1.0
             return x.to(dtype)
 
         if prefix:
@@ -54,7 +56,7 @@ class Batch:
                 at += n
             if L > e:
                 self.tail_k[b, :, :L - e], self.tail_v[b, :, :L - e] = rows(L - e)[0], rows(L - e)[0]
-        self.q = (peak * torch.randn((B, Q, Hq, D), generator=g)).to(dtype)
+        self.q = (peak / size * torch.randn((B, Q, Hq, D), generator=g)).to(dtype)
         self.sm = 1.0 / np.sqrt(D)
 
     def full_table(self):
@@ -74,6 +76,34 @@ class Batch:
         return attention.decode_verify(parity.f64(self.q), self.cache, self.lay, self.full_table(), self.lens, self.sm,
                                        tk, tv)
 
+    def reference(self, device="cuda"):
+        """oracle() for many rows over a long prefix: the same definition, the
+        prefix dequantised once and the sums in 64 bits on the GPU."""
+        B, Q, Hq, Hkv, D, P = len(self.lens), self.Q, self.Hq, self.Hkv, self.D, self.prefix
+        G = Hq // Hkv
+        out, lse = np.zeros((B, Q, Hq, D)), np.full((B, Q, Hq), -np.inf)
+        q = torch.from_numpy(parity.f64(self.q)).to(device)
+        tk, tv = (np.nan_to_num(parity.f64(t)) for t in (self.tail_k, self.tail_v))
+        for h in range(Hkv):
+            pk, pv = (torch.from_numpy(np.ascontiguousarray(x)).to(device)
+                      for x in attention.sequence_kv(self.cache, self.lay, self.prefix_table, P, h))
+            for b, L in enumerate(self.lens):
+                if L == 0:
+                    continue
+                end = max(P, attention.verify_committed(int(L), Q, self.N))
+                ok, ov = attention.sequence_kv(self.cache, self.lay, self.bt[b, P // 16:], end - P, h) if end > P else \
+                    (np.zeros((0, D)), np.zeros((0, D)))
+                k, v = (torch.cat([a, torch.from_numpy(np.concatenate([o, t[b, h, :L - end]])).to(device)])
+                        for a, o, t in ((pk, ok, tk), (pv, ov, tv)))
+                qb = q[b, :, h * G:(h + 1) * G]  # [Q, G, D]
+                s = self.sm * torch.einsum("qgd,ld->qgl", qb, k)
+                seen = torch.tensor([attention.verify_visible(int(L), Q, j) for j in range(Q)], device=device)
+                s = s.masked_fill(torch.arange(len(k), device=device) >= seen[:, None, None], -torch.inf)
+                z = torch.logsumexp(s, -1)
+                out[b, :, h * G:(h + 1) * G] = torch.einsum("qgl,ld->qgd", torch.exp(s - z[..., None]), v).cpu().numpy()
+                lse[b, :, h * G:(h + 1) * G] = z.cpu().numpy()
+        return out, lse
+
     def bounds(self):
         """(score error, output error) bounds of the decode arithmetic. A
         score is a sum of 2^-22-exact products and of at most 64 fp32 or
@@ -88,7 +118,7 @@ class Batch:
         raw_q1 = float(np.abs(parity.f64(self.q)).sum(-1).max())
         A = V = 0.0
         ppt = self.N // 16
-        for row in self.full_table():
+        for row in [self.prefix_table] + [r[self.prefix // 16:] for r in self.bt]:
             pages = [int(x) for x in row if x >= 0]
             for t in range(len(pages) // ppt):
                 for h in range(self.Hkv):

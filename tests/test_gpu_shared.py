@@ -61,6 +61,75 @@ def test_matches_oracle(name):
     assert np.abs(lse[fin] - rlse[fin]).max() <= score + 2.0 ** -20 * (1 + np.abs(rlse[fin]).max())
 
 
+# Batches large enough that the tensor-core kernel takes the prefix (its rule:
+# 4.5 to 13.5 ns per eight rows and 128 tokens, by the widths, above 10 us and
+# 11.5 ns per 128 rows and 64 tokens): every width of K and of V, both tile
+# sizes and scale types, blocks of 128 rows that are not full, odd groups,
+# caches of large and of small values, and a first tile far from the others.
+LARGE = {
+    # N, Hq, Hkv, prefix, sequences, own tokens past the queries at most, Q, dtype, widths, more
+    "k4v2": (128, 8, 1, 8192, 61, 200, 2, h, (4, 2, 4), {}),
+    "k4v2_tile64_bf16": (64, 8, 1, 4096, 61, 90, 2, b16, (4, 2, 4), {}),
+    "k4v2_group7_two_heads": (128, 14, 2, 4096, 70, 140, 1, h, (4, 2, 4), {}),
+    "k6v6": (128, 8, 2, 4096, 50, 5, 1, h, (6, 6, 2), {}),
+    "k8v8_fp32_scales": (128, 8, 1, 8192, 20, 129, 1, h, (8, 8, 4), {}),
+    "k2v8_tile64": (64, 8, 1, 8192, 40, 3, 1, h, (2, 8, 2), {}),
+    "k3v5": (128, 8, 1, 8192, 30, 20, 1, b16, (3, 5, 2), {}),
+    "k8v3": (128, 8, 1, 8192, 30, 20, 1, h, (8, 3, 4), {}),
+    "k5v4": (128, 8, 1, 8192, 40, 20, 1, h, (5, 4, 2), {}),
+    "large_values": (128, 8, 1, 8192, 61, 9, 2, h, (4, 2, 4), dict(size=300.0)),
+    "small_values": (128, 8, 1, 8192, 61, 9, 2, h, (4, 2, 4), dict(size=2.0 ** -9)),
+    "first_tile_large": (128, 8, 1, 8192, 61, 9, 2, h, (4, 2, 4), dict(first=200.0, peak=0.05)),
+    "first_tile_small": (64, 8, 1, 8192, 61, 9, 2, h, (4, 2, 4), dict(first=2.0 ** -9)),
+    "sharp": (128, 8, 1, 8192, 61, 9, 2, h, (4, 2, 4), dict(peak=12.0)),
+    "padding_verify": (128, 8, 1, 8192, 33, 150, 4, b16, (4, 2, 4), dict(pad=True)),
+}
+
+
+@pytest.mark.parametrize("name", list(LARGE))
+def test_large_batches_match_the_definition(name):
+    N, Hq, Hkv, prefix, B, most, Q, dtype, widths, more = LARGE[name]
+    more = dict(more)
+    pad = more.pop("pad", False)
+    lens = [0 if pad and b % 5 == 3 else prefix + Q + (37 * b) % (most + 1) for b in range(B)]
+    x = serving.Batch(128, N, Hq, Hkv, lens, Q=Q, prefix=prefix, dtype=dtype, widths=widths, seed=4, **more)
+    ref, rlse = x.reference()
+    out, lse, flags = serving.run_shared(x)
+    assert flags == 0
+    score, tol = x.bounds()
+    out, lse = parity.f64(out), parity.f64(lse)
+    print(f"\n{name}: max |out - definition| = {np.abs(out - ref).max():.3e} (bound {tol:.3e}), relative "
+          f"{np.linalg.norm(out - ref) / np.linalg.norm(ref):.2e}")
+    assert np.abs(out - ref).max() <= tol
+    fin = np.isfinite(rlse)
+    np.testing.assert_array_equal(np.isfinite(lse), fin)
+    assert np.abs(lse[fin] - rlse[fin]).max() <= score + 2.0 ** -20 * (1 + np.abs(rlse[fin]).max())
+    # the norm over the whole batch, where errors do not all add up: operands
+    # split to 2^-22, a few hundred truncated fp32 accumulation steps
+    assert np.linalg.norm(out - ref) <= 2.0 ** -14 * np.linalg.norm(ref)
+
+
+def test_bad_pages_are_flagged_by_the_large_path():
+    x = serving.Batch(128, 64, 8, 1, [4096 + 3] * 61, Q=2, prefix=4096, seed=4)
+    good = x.prefix_table.copy()
+    for at, page in ((200, x.cache.shape[0]), (0, -1), (255, 2 ** 31 - 1)):
+        x.prefix_table[:] = good
+        x.prefix_table[at] = page
+        assert serving.run_shared(x)[2] == kv.DEVERR_PAGE_RANGE
+
+
+def test_infinite_and_nan_queries_stay_in_their_rows():
+    x = serving.Batch(128, 64, 8, 1, [4096 + 3] * 61, Q=2, prefix=4096, seed=4)
+    want, _, _ = serving.run_shared(x)
+    x.q[7, 1, 3, 5], x.q[20, 0, 0, 100] = float("nan"), float("inf")
+    got, _, flags = serving.run_shared(x)
+    assert flags == 0
+    bad = torch.zeros(want.shape[:3], dtype=torch.bool, device="cuda")
+    bad[7, 1, 3] = bad[20, 0, 0] = True
+    assert torch.equal(got[~bad], want[~bad])
+    assert not torch.isfinite(got[bad]).any()
+
+
 def test_agrees_with_the_decode_that_reads_the_prefix_per_sequence():
     x = batch("g8_many")
     out, lse, _ = serving.run_shared(x)

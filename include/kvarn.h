@@ -545,6 +545,8 @@ int32_t kvarn_affine_decode(const void* q, int32_t num_q_heads, float sm_scale, 
  *   mass_stride        >= max_seq_len / N
  *   decay              in [0, 1]
  *   workspace          >= kvarn_decode_mass_workspace_bytes(...)
+ * Layouts: K4V2 (either scale type), or fp16 scales with k_bits = v_bits = 4,
+ * 6 or 8; KVARN_EUNSUPPORTED for other widths.
  * Other arguments and results as kvarn_decode; out and lse are bit for bit
  * those of kvarn_decode. The sums are taken in a fixed order: the same call
  * gives the same masses. num_seqs is at most 65535.

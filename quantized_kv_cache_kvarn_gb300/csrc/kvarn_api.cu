@@ -584,9 +584,15 @@ int32_t kvarn_affine_decode(const void* q, int32_t num_q_heads, float sm_scale, 
                              out, lse, workspace, workspace_bytes, error_flags, stream, true);
 }
 
+static int32_t check_mass(const kvarn_layout* L) {
+  const int32_t s = check_dense(L);
+  if (s != KVARN_OK) return s;
+  return mass_widths_supported(L->k_bits, L->v_bits, L->scale_dtype == 1 ? 2 : 4) ? KVARN_OK : KVARN_EUNSUPPORTED;
+}
+
 int64_t kvarn_decode_mass_workspace_bytes(const kvarn_layout* L, int32_t num_seqs, int32_t num_q_heads,
                                           int32_t max_seq_len) {
-  if (check_dense(L) != KVARN_OK || num_seqs < 0 || num_q_heads < 1 || max_seq_len < 0 ||
+  if (check_mass(L) != KVARN_OK || num_seqs < 0 || num_q_heads < 1 || max_seq_len < 0 ||
       num_q_heads % L->num_kv_heads)
     return -1;
   const DensePlan plan = dense_plan(L, num_seqs, num_q_heads, 1, max_seq_len, raw_bound(L, max_seq_len, 1, 0, 0));
@@ -601,7 +607,7 @@ int32_t kvarn_decode_mass(const void* q, int32_t num_q_heads, float sm_scale, co
                           int32_t mass_stride, float decay, void* workspace, int64_t workspace_bytes,
                           uint32_t* error_flags, kvarn_stream_t stream) {
   if (!L) return KVARN_EINVAL;
-  const int32_t s = check_dense(L);
+  const int32_t s = check_mass(L);
   if (s != KVARN_OK) return s;
   if (num_seqs > 0) {
     const int32_t tiles = std::max(0, max_seq_len) / L->tile_tokens;

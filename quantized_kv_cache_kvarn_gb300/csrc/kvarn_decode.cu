@@ -71,6 +71,7 @@ DensePlan plan_dense_stream(int32_t num_seqs, int32_t units_per_seq, int32_t max
   const int64_t tile_ctas = (most + p.min_tiles - 1) / p.min_tiles;
   const int64_t raw_items = units * p.raw_splits;
   p.ctas = static_cast<int32_t>(std::max<int64_t>(1, std::min(resident, tile_ctas + raw_items)));
+  p.raw_last = tile_ctas + raw_items <= resident;
   return p;
 }
 
@@ -92,6 +93,7 @@ DensePlan plan_dense_pieces(int32_t num_seqs, int32_t units_per_seq, int32_t max
   p.raw_splits = raw_max > p.raw_chunk ? (raw_max + p.raw_chunk - 1) / p.raw_chunk : 1;
   p.slots = p.tile_slots + p.raw_splits;
   p.ctas = static_cast<int32_t>(std::max<int64_t>(1, std::min(resident, units * (p.tile_slots + p.raw_splits))));
+  p.raw_last = 1;
   return p;
 }
 
@@ -231,6 +233,7 @@ cudaError_t dense_args(const DecodeParams& p, const DensePlan& plan, DecArgs& A)
   A.raw_chunk = plan.raw_chunk;
   A.slots = plan.slots;
   A.piece = plan.piece;
+  A.raw_last = plan.raw_last;
   A.err = p.err;
   A.bf16 = p.bf16 ? 1 : 0;
   A.partial_tiles = p.codec == 2;
@@ -260,6 +263,13 @@ cudaError_t run_decode_kernel(const DecodeParams& p, const DecArgs& A, int ctas,
       default: break;
     }
     return e;
+  }
+  if (A.stats) {
+#define KVARN_MASS_CASE(K, V, S) \
+  if (kb == K && vb == V && sb == S) return run_mass_widths<K, V, S>(A, p.D, p.N, ctas, st);
+    KVARN_MASS_WIDTHS(KVARN_MASS_CASE)
+#undef KVARN_MASS_CASE
+    return cudaErrorInvalidValue;
   }
   if (kb == 4 && vb == 2 && sb == 4) {
 #define KV_DISPATCH(DD, NN, WW)                                                              \

@@ -179,6 +179,7 @@ struct DecArgs {
   int32_t tile_slots;  // partial slots reserved for compressed tiles; raw slots follow them
   int32_t raw_splits;  // raw slots (chunks of raw_chunk raw tokens)
   int32_t raw_chunk;   // raw tokens per raw split
+  int32_t raw_last;    // raw items from the last CTA down
   int32_t slots;       // tile_slots + raw_splits
   uint32_t* err;
   int32_t partial_tiles;  // uncompressed pages: a sequence's last tile may be partial (tokens past len masked)
@@ -835,7 +836,7 @@ __device__ __forceinline__ int cta_of_tile(int64_t t, int C, int64_t total, int 
 // 24), each counted mod 256 (only parities are read). `dead`: a copy timed
 // out earlier; the segment then only writes empty partials. Returns false
 // when a copy timed out (in this segment or before).
-template <int D, int N, int W, int KB, int VB, int SB, int CD>
+template <int D, int N, int W, int KB, int VB, int SB, int CD, bool MASS>
 __device__ __forceinline__ bool dense_segment(const DecArgs& A, unsigned char* smem, int b, int x, int t0, int t1,
                                               int slot, uint32_t& ph,
                                               bool dead) {
@@ -956,10 +957,9 @@ __device__ __forceinline__ bool dense_segment(const DecArgs& A, unsigned char* s
 
   // where the unit's first tile of this segment goes in the tile masses'
   // pairs; in shared memory, so that no register holds it over the tiles
-  __shared__ int64_t stat_base[UNITS];
-  volatile int64_t* stat_at = stat_base + unit;
-  if (!PLAIN_Q && A.stats && leader && lane == 0)
-    *stat_at = static_cast<int64_t>(b * A.Hq + kvh * A.G) * A.stat_tiles + first;
+  __shared__ int64_t stat_base[MASS ? UNITS : 1];
+  volatile int64_t* stat_at = stat_base + (MASS ? unit : 0);
+  if (MASS && leader && lane == 0) *stat_at = static_cast<int64_t>(b * A.Hq + kvh * A.G) * A.stat_tiles + first;
 
   // ---- rotated, scaled query rows of the row group (unused rows are zero)
   for (int h = warp; h < 8; h += W) {
@@ -1195,7 +1195,7 @@ __device__ __forceinline__ bool dense_segment(const DecArgs& A, unsigned char* s
     const float2 pt = tree_reduce(ps2, [](float2 a, float2 b) { return f2add(a, b); });
     lsum = fmaf(lsum, alpha, pt.x + pt.y);
     m = m_new;
-    if (!PLAIN_Q && A.stats) {  // the tile's share of each row, for the tile masses (one query: row g is head g)
+    if constexpr (MASS) {  // the tile's share of each row (one query: row g is head g)
       const float lt = warp_sum_xor(pt.x + pt.y, 1, 4);
       if (t == 0 && leader && g < A.G)
         A.stats[*stat_at + static_cast<int64_t>(g) * A.stat_tiles + i * UNITS] = make_float2(m_new, lt);
@@ -1385,7 +1385,7 @@ __device__ __forceinline__ bool dense_segment(const DecArgs& A, unsigned char* s
   return !any_late;
 }
 
-template <int D, int N, int W, int KB = 4, int VB = 2, int SB = 4, int CD = kCodecKvarn>
+template <int D, int N, int W, int KB = 4, int VB = 2, int SB = 4, int CD = kCodecKvarn, bool MASS = false>
 __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_dense_kernel(const __grid_constant__ DecArgs A) {
   using S = DecShape<D, N, W, KB, VB, SB, CD>;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -1406,11 +1406,11 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
   if (!A.late_wait) pdl_wait_primary();
   if (A.late_trigger) pdl_launch_dependents();
 
-  // ---- raw records: items r = 0, 1, ... of (sequence, unit, raw chunk) go to
-  //      the CTAs from the last one down, so that while the grid has CTAs
-  //      to spare the raw items and the tiles run side by side
+  // ---- raw records: items r = 0, 1, ... of (sequence, unit, raw chunk). While
+  //      the grid has CTAs to spare they go to the CTAs from the last one
+  //      down, beside the tiles; else to the first ones, which start first
   const int64_t units = static_cast<int64_t>(A.num_seqs) * A.X;
-  for (int64_t r = gridDim.x - 1 - blockIdx.x; r < units * A.raw_splits; r += gridDim.x) {
+  for (int64_t r = A.raw_last ? gridDim.x - 1 - blockIdx.x : blockIdx.x; r < units * A.raw_splits; r += gridDim.x) {
     const int chunk = static_cast<int>(r % A.raw_splits);
     const int64_t u = r / A.raw_splits;
     const int b = static_cast<int>(u / A.X), x = static_cast<int>(u % A.X);
@@ -1503,7 +1503,7 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
     }
     t0 += A.sink_tiles;
     t1 += A.sink_tiles;
-    dead = !dense_segment<D, N, W, KB, VB, SB, CD>(A, smem, b, x, t0, t1, slot, ph, dead) || dead;
+    dead = !dense_segment<D, N, W, KB, VB, SB, CD, MASS>(A, smem, b, x, t0, t1, slot, ph, dead) || dead;
   }
   if (A.late_wait && blockIdx.x == gridDim.x - 1) pdl_wait_primary();
 }
@@ -1513,10 +1513,10 @@ __global__ void __launch_bounds__(W * 32, (decode_min_ctas<D, W, CD>())) decode_
 cudaError_t dense_args(const DecodeParams& p, const DensePlan& plan, DecArgs& A);
 cudaError_t run_decode_kernel(const DecodeParams& p, const DecArgs& A, int ctas, cudaStream_t st);
 
-template <int D, int N, int W, int KB, int VB, int SB, int CD = kCodecKvarn>
+template <int D, int N, int W, int KB, int VB, int SB, int CD = kCodecKvarn, bool MASS = false>
 cudaError_t run_dense(const DecArgs& A, int ctas, cudaStream_t st) {
   using S = DecShape<D, N, W, KB, VB, SB, CD>;
-  auto kern = decode_dense_kernel<D, N, W, KB, VB, SB, CD>;
+  auto kern = decode_dense_kernel<D, N, W, KB, VB, SB, CD, MASS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
   // a programmatic dependent of the kernel before it on the stream: the
@@ -1536,10 +1536,10 @@ cudaError_t run_dense(const DecArgs& A, int ctas, cudaStream_t st) {
 }
 
 // CTAs of one decode kernel resident per SM (registers and shared memory).
-template <int D, int N, int W, int KB, int VB, int SB, int CD = kCodecKvarn>
+template <int D, int N, int W, int KB, int VB, int SB, int CD = kCodecKvarn, bool MASS = false>
 int resident_dense() {
   using S = DecShape<D, N, W, KB, VB, SB, CD>;
-  auto kern = decode_dense_kernel<D, N, W, KB, VB, SB, CD>;
+  auto kern = decode_dense_kernel<D, N, W, KB, VB, SB, CD, MASS>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess) return 1;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, W * 32, S::SMEM) != cudaSuccess || n < 1) return 1;
@@ -1591,6 +1591,29 @@ int resident_widths256(int N);
   int resident_widths256<KB, VB, 2>(int N);
 KVARN_WIDTH_PAIRS_256(KVARN_DECLARE_WIDTHS_256)
 #undef KVARN_DECLARE_WIDTHS_256
+
+// The decode that gathers the tiles' (maximum, sum) pairs (DecArgs::stats), a
+// kernel of its own: asking in the tile loop whether to would cost the plain
+// decode 1% (K4V2) to 15% (K8V3, where it spills). Compiled in
+// kvarn_decode_mass*.cu for the widths of mass_widths_supported.
+template <int KB, int VB, int SB>
+cudaError_t run_mass_widths(const DecArgs& A, int D, int N, int ctas, cudaStream_t st);
+#define KVARN_MASS_WIDTHS(X) X(4, 2, 4) X(4, 2, 2) X(4, 4, 2) X(6, 6, 2) X(8, 8, 2)
+#define KVARN_DECLARE_MASS(KB, VB, SB) \
+  template <>                          \
+  cudaError_t run_mass_widths<KB, VB, SB>(const DecArgs& A, int D, int N, int ctas, cudaStream_t st);
+KVARN_MASS_WIDTHS(KVARN_DECLARE_MASS)
+#undef KVARN_DECLARE_MASS
+#define KVARN_DECODE_MASS(KB, VB, SB)                                                                              \
+  template <>                                                                                                      \
+  cudaError_t run_mass_widths<KB, VB, SB>(const DecArgs& A, int D, int N, int ctas, cudaStream_t st) {             \
+    constexpr int W1 = width_warps<128, 128, KB, VB, SB>(), W2 = width_warps<128, 64, KB, VB, SB>();               \
+    if (D == 128 && N == 128) return run_dense<128, 128, W1, KB, VB, SB, kCodecKvarn, true>(A, ctas, st);          \
+    if (D == 128 && N == 64) return run_dense<128, 64, W2, KB, VB, SB, kCodecKvarn, true>(A, ctas, st);            \
+    if (D == 256 && N == 128) return run_dense<256, 128, 2, KB, VB, SB, kCodecKvarn, true>(A, ctas, st);           \
+    if (D == 256 && N == 64) return run_dense<256, 64, 2, KB, VB, SB, kCodecKvarn, true>(A, ctas, st);             \
+    return cudaErrorInvalidValue;                                                                                  \
+  }
 
 // The decode over uncompressed fp16 pages (the same kernel with no codec;
 // 32-token tiles, 4 warps at head_dim 128, warp pairs at 256), compiled in

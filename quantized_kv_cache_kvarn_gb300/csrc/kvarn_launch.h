@@ -144,6 +144,7 @@ struct DensePlan {
   int32_t raw_chunk;   // raw tokens per raw split (kRawChunk times a power of two)
   int32_t slots;       // tile_slots + raw_splits
   int32_t piece;       // > 0: pieces of so many tiles within each unit instead of stream-K ranges
+  int32_t raw_last;    // raw items from the last CTA down (the grid has CTAs to spare for them)
 };
 
 // units_per_seq: KV heads x row groups; max_tiles: compressed tiles a unit
@@ -189,6 +190,12 @@ cudaError_t launch_store_fp16(const StoreFp16Params& p, cudaStream_t st);
 // decode kernel with no codec: DecodeParams::codec = 2, N = 32).
 int raw_decode_ctas_per_sm(int32_t D);
 
+// Widths whose decode gathers tile masses: the preset, and with fp16 scales
+// K4V2 and equal widths of 4, 6 and 8 bits.
+inline bool mass_widths_supported(int32_t kb, int32_t vb, int32_t sb) {
+  if (kb == 4 && vb == 2) return true;
+  return sb == 2 && kb == vb && (kb == 4 || kb == 6 || kb == 8);
+}
 // Tile masses of the dense decode: one (base-2 maximum, sum) pair per output
 // row and committed tile in the workspace.
 int64_t mass_workspace_bytes(int64_t rows, int32_t max_tiles);

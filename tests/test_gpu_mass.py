@@ -15,7 +15,10 @@ CASES = {
     "g8": (128, 128, 16, 2, [700, 128, 127, 0, 1290], torch.float16, (4, 2, 4)),
     "tile64": (128, 64, 6, 2, [1, 64, 333, 65, 640], torch.float16, (4, 2, 4)),
     "wide_bf16": (256, 128, 12, 4, [517, 384], torch.bfloat16, (4, 2, 4)),
-    "k6v3_fp16_scales": (128, 128, 7, 7, [400, 256], torch.bfloat16, (6, 3, 2)),
+    "k6v6_group1": (128, 128, 7, 7, [400, 256], torch.bfloat16, (6, 6, 2)),
+    "k4v2_fp16_scales_tile64": (128, 64, 14, 2, [400, 256, 63], torch.float16, (4, 2, 2)),
+    "k4v4_wide": (256, 128, 8, 2, [300, 256], torch.float16, (4, 4, 2)),
+    "k8v8": (128, 128, 8, 1, [700, 128], torch.float16, (8, 8, 2)),
     "k8v8_wide_tile64": (256, 64, 8, 1, [200, 70], torch.float16, (8, 8, 2)),
     "only_tails": (128, 128, 4, 1, [5, 127], torch.float16, (4, 2, 4)),
 }

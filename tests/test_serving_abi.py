@@ -72,6 +72,11 @@ def test_mass_workspace_is_the_decodes_and_the_pairs(L):
         kv.decode_mass_workspace_bytes(kv.latent_layout(4), 1, 64, 100)
     with pytest.raises(kv.KvarnError):
         kv.decode_mass_workspace_bytes(lay, 1, 12, 100)
+    for kb, vb, s16, ok in ((4, 2, True, 1), (6, 6, True, 1), (8, 8, True, 1), (4, 4, True, 1), (6, 6, False, 0),
+                            (6, 3, True, 0), (3, 3, True, 0)):
+        wide = kv.dense_layout(128, 128, 8, 10, k_bits=kb, v_bits=vb, fp16_scales=s16)
+        assert (mass(L, lay=wide, size=1024) == EWORKSPACE) == bool(ok)
+        assert (mass(L, lay=wide) == EUNSUPPORTED) == (not ok) if not ok else True
 
 
 def shared(L, lay=None, q=A16, Hq=64, Q=1, cache=A16, pt=A16, S=1024, bt=A16, bts=1024, lens=A16, n=16384, cap=128, B=4, out=A16,

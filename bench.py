@@ -440,7 +440,50 @@ class DenseHarness:
         self.appending = True
         self.encode_tokens = sum(1 for L in self.lens if L % N == 0) * N
 
+    def use_rope(self):
+        """The step turns its queries and newest keys to their positions
+        before the append (kvarn_rope, one launch for both)."""
+        import torch
+        c = self.case
+        self.positions = (c.seq_lens - 1)[:, None].contiguous()
+        self.inv_freq, _ = self.kv.rope_frequencies(self.wl.head_dim, device=self.dev)
+        self.raw = (c.q[:, None].clone(), self.ap_k[:, None].clone())
+        self.turned = (c.q[:, None], self.ap_k[:, None])
+        self.launches += 1
+
+    def use_prefix(self, tokens):
+        """The batch shares its first tokens: they are read from sequence 0's
+        pages, once (kvarn_decode_shared)."""
+        import torch
+        c, wl = self.case, self.wl
+        if tokens % wl.tile_tokens or tokens > min(self.lens):
+            raise SystemExit("--prefix must be whole tiles that every sequence holds")
+        table = c.block_table[0, :tokens // 16].contiguous()
+        ws = torch.empty(self.kv.decode_shared_workspace_bytes(self.lay, wl.num_seqs, wl.num_q_heads, 1, self.Lmax, tokens),
+                         dtype=torch.uint8, device=self.dev)
+
+        def decode(q, lay, cache, bt, lens, longest, out, _ws, err, sm, tail_k, tail_v):
+            self.kv.decode_shared(q[:, None], lay, cache, table, tokens, bt, lens, longest, out[:, None], ws, err, sm, tail_k,
+                                  tail_v)
+        self._dec = decode
+        self.packed -= (wl.num_seqs - 1) * wl.num_kv_heads * tokens * self._pb(self.lay) // 16
+        self.launches += 1
+
+    def use_mass(self):
+        """The decode also gathers every tile's attention mass (kvarn_decode_mass)."""
+        import torch
+        wl = self.wl
+        self.mass = torch.zeros((wl.num_seqs, max(1, self.Lmax // wl.tile_tokens)), device=self.dev)
+        self.ws = torch.empty(self.kv.decode_mass_workspace_bytes(self.lay, wl.num_seqs, wl.num_q_heads, self.Lmax),
+                              dtype=torch.uint8, device=self.dev)
+
+        def decode(q, lay, cache, bt, lens, longest, out, ws, err, sm, tail_k, tail_v):
+            self.kv.decode_mass(q, lay, cache, bt, lens, longest, out, self.mass, self.mass, ws, err, sm, tail_k, tail_v)
+        self._dec = decode
+
     def encode(self):
+        if getattr(self, "turned", None):
+            self.kv.rope(self.raw, self.turned, self.positions, self.inv_freq)
         if getattr(self, "appending", False):
             self.kv.append(self.ap_k, self.ap_v, self.case.seq_lens, self.Lmax, self.ap_tail_k, self.ap_tail_v,
                            self.case.block_table, self.lay, self.cache, self.err)
@@ -845,6 +888,17 @@ def run_kvarn(args):
         if wl.rope_dim or args.queries > 1 or args.sink or args.recent or wl.encode_chunk:
             raise SystemExit("--append applies to the plain dense step")
         H.use_append()
+    if args.rope or args.prefix or args.mass:
+        if type(H) is not DenseHarness or args.codec != "kvarn" or (args.prefix and args.mass):
+            raise SystemExit("--rope, --prefix and --mass apply to the plain dense step, --prefix and --mass not together")
+        if args.rope:
+            if not args.append:
+                raise SystemExit("--rope turns the appended token: it needs --append")
+            H.use_rope()
+        if args.prefix:
+            H.use_prefix(args.prefix)
+        if args.mass:
+            H.use_mass()
     stream = torch.cuda.current_stream()
     B = wl.num_seqs
 
@@ -1042,7 +1096,9 @@ def run_kvarn(args):
         "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
         "dtype": (f"f32 (codes u{args.kbits}/u{args.vbits}, {'fp16' if args.fp16_scales else 'fp32'} scales; "
                   f"fp16 hi/lo mma operands)"), "data": "synthetic",
-        "config": {"workload": _workload_desc(wl) + (" fp16-scales" if args.fp16_scales else ""),
+        "config": {"workload": _workload_desc(wl) + (" fp16-scales" if args.fp16_scales else "")
+                   + (" rope" if args.rope else "") + (f" shared-prefix-{args.prefix}" if args.prefix else "")
+                   + (" tile-mass" if args.mass else ""),
                    "step": (f"commit one compressed tile per (seq, KV head), then {args.queries} query token(s) "
                             f"per seq, raw sink {args.sink} + recent {args.recent} (kvarn_decode_window)"
                             if args.sink or args.recent else
@@ -1073,6 +1129,7 @@ def run_kvarn(args):
         "cpu_baseline": cpu,
     }
     plain = not (args.num_seqs or args.queries > 1 or args.sink or args.recent or args.append
+                 or args.rope or args.prefix or args.mass
                  or widths != (4, 2, 4) or args.no_extra or args.codec != "kvarn")
     if plain and world == 1 and args.workload == WORKLOAD:
         # the other workloads of the same family, each measured on its own
@@ -1151,6 +1208,9 @@ def main():
                     help="commit through kvarn_append of the newest token (fused append + commit)")
     ap.add_argument("--sink", type=int, default=0, help="raw sink tokens (a multiple of the tile)")
     ap.add_argument("--recent", type=int, default=0, help="newest accepted tokens kept raw")
+    ap.add_argument("--rope", action="store_true", help="turn the queries and the appended key to their positions first")
+    ap.add_argument("--prefix", type=int, default=0, help="tokens at the start that the batch shares (whole tiles)")
+    ap.add_argument("--mass", action="store_true", help="decode that also gathers every tile's attention mass")
     ap.add_argument("--no-extra", action="store_true",
                     help="measure only the named workload (a default run adds the toy, g64, hybrid and MLA "
                          "workloads as extra keys)")

@@ -543,7 +543,7 @@ int32_t kvarn_affine_decode(const void* q, int32_t num_q_heads, float sm_scale, 
  *
  *   mass_in, mass_out  device fp32, row b at b * mass_stride; may be the same
  *   mass_stride        >= max_seq_len / N
- *   decay              in [0, 1]
+ *   decay              in [0, 1]; 0 does not read mass_in's values
  *   workspace          >= kvarn_decode_mass_workspace_bytes(...)
  * Layouts: K4V2 (either scale type), or fp16 scales with k_bits = v_bits = 4,
  * 6 or 8; KVARN_EUNSUPPORTED for other widths.
@@ -683,7 +683,8 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
 
 /*
  * kvarn_set_copy_wait_test - diagnostic of the dense decode kernels'
- * (kvarn_decode, _verify, _window, _fp16, _noalloc, kvarn_affine_decode)
+ * (kvarn_decode, _verify, _window, _fp16, _noalloc, _mass, _shared's dense
+ * part, kvarn_affine_decode)
  * bounded waits for their page copies, so that a test can drive the time-out
  * path without making a copy fail. `cycles`: how long a wait lasts before the
  * kernel gives up (0 restores the default, 2e9 cycles, about a second; a limit

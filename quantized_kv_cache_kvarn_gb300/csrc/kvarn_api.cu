@@ -664,7 +664,7 @@ int32_t kvarn_decode_shared(const void* q, int32_t num_q_heads, int32_t num_quer
   if (s != KVARN_OK || num_seqs == 0) return s;
   if (!shared_sizes_ok(L, num_seqs, num_q_heads, num_queries, max_seq_len, prefix_tokens)) return KVARN_EINVAL;
   if (tail_capacity < L->tile_tokens + num_queries - 2 || tail_capacity < 1) return KVARN_EINVAL;
-  if (!q || !cache || !prefix_table) return KVARN_EINVAL;
+  if (!q || !cache || !prefix_table || L->num_pages < 1) return KVARN_EINVAL;
   if (num_q_heads / L->num_kv_heads > 8) return KVARN_EUNSUPPORTED;
   const int32_t committed = std::max(0, max_seq_len - num_queries + 1) / L->tile_tokens * L->tile_tokens;
   if (committed > prefix_tokens && bt_stride < committed / kPageTokens) return KVARN_EINVAL;

@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(128) merge_mass_kernel(const __grid_constant__
   if (warp == 0 && t < A.stat_tiles) {
     const int64_t at = static_cast<int64_t>(b) * mass_stride + t;
     sum = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
-    mass_out[at] = t < C ? fmaf(decay, mass_in[at], sum) : 0.f;
+    // decay 0 does not look at what was there (it may be anything)
+    mass_out[at] = t >= C ? 0.f : decay == 0.f ? sum : fmaf(decay, mass_in[at], sum);
   }
 }
 

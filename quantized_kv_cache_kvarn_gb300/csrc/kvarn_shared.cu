@@ -141,7 +141,18 @@ bool prefix_on_tensor_cores(int64_t rows_per_head, int64_t heads, int64_t tokens
 SharedPlan plan_shared(int32_t num_seqs, int32_t num_kv_heads, int32_t G, int32_t num_queries, int32_t prefix_tiles,
                        int32_t own_tiles, int32_t D, int32_t N, int32_t raw_max, int32_t kb, int32_t vb, int32_t sb) {
   SharedPlan s{};
-  s.own = plan_dense_pieces(num_seqs, num_kv_heads * row_groups(G, num_queries), own_tiles, D, N, raw_max, kb, vb, sb);
+  // Own tokens: pieces of units while they are short, equal ranges of the
+  // flattened tile list where every CTA has about six rounds of tiles or
+  // more (32 sequences of 8 KV heads over a 4096-token prefix, us, ranges /
+  // pieces: 300 own tokens 52 / 50, up to 2000 of ragged length 74 / 59, 8000
+  // 105 / 114, up to 8000 78 / 88; 4 sequences of one head, 8000: 20 / 14).
+  constexpr int64_t kOwnRounds = 6;
+  const int32_t per_seq = num_kv_heads * row_groups(G, num_queries);
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * dense_decode_ctas_per_sm(D, N, kb, vb, sb) *
+                        (D == 256 ? dense_decode_warps(D) / 2 : dense_decode_warps(D));
+  s.own = static_cast<int64_t>(num_seqs) * per_seq * own_tiles >= kOwnRounds * slots
+              ? plan_dense_stream(num_seqs, per_seq, own_tiles, D, N, raw_max, kb, vb, sb)
+              : plan_dense_pieces(num_seqs, per_seq, own_tiles, D, N, raw_max, kb, vb, sb);
   const int64_t rows = static_cast<int64_t>(num_seqs) * num_queries * G;
   const int64_t units = (rows + 127) / 128 * num_kv_heads;
   if (D == 128 && units <= 65535 && prefix_on_tensor_cores(rows, num_kv_heads, static_cast<int64_t>(prefix_tiles) * N, kb, vb)) {

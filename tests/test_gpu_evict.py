@@ -73,10 +73,13 @@ def test_matches_definition(N, lens, keep, sink, recent, kind, inplace):
         np.testing.assert_array_equal(a, b)
 
 
-def test_rows_longer_than_the_key_buffer():
-    N, T = 64, 26001
+@pytest.mark.parametrize("T,inplace", [(26001, False), (83001, False), (83001, True)])
+def test_long_rows(T, inplace):
+    """Rows over a whole cluster's shared memory, and longer ones, which one
+    CTA walks chunk by chunk."""
+    N = 64
     mass, table, lens = inputs([64 * T, 64 * 25000 + 9], N, T, 4, "ties")
-    got, flags = run(mass, table, lens, N, 64 * T, 13000, 4, 100)
+    got, flags = run(mass, table, lens, N, 64 * T, 13000, 4, 100, inplace)
     assert flags == 0
     want = []
     for b in range(2):  # the definition by sorting (stable: equal masses stay from the left)

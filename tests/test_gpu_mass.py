@@ -105,6 +105,15 @@ def test_accumulates_in_place_without_lse_and_repeats_exactly():
     assert (runs[0].sum(1) <= 3 * 8 * (1 + 1e-5)).all()
 
 
+def test_decay_zero_forgets_whatever_was_there():
+    x = serving.Batch(128, 128, 8, 2, [900, 260], seed=5)
+    ref = tile_masses(x)
+    _, _, new, flags = serving.run_mass(x, torch.full((2, 7), float("nan")), 0.0)
+    assert flags == 0
+    score, _ = x.bounds()
+    assert (np.abs(parity.f64(new) - ref) <= ref * (2 * score + 2.0 ** -19) + 1e-30).all()
+
+
 def test_length_out_of_range_is_flagged():
     x = serving.Batch(128, 128, 4, 1, [300, 256], seed=6)
     lens = torch.tensor([300, 1000], dtype=torch.int32).cuda()

@@ -109,6 +109,41 @@ def test_large_batches_match_the_definition(name):
     assert np.linalg.norm(out - ref) <= 2.0 ** -14 * np.linalg.norm(ref)
 
 
+def test_long_own_tokens():
+    """Own tokens long enough for equal ranges of the tile list (six rounds
+    of tiles per CTA) instead of pieces of units: only whole tiles differ, so
+    the plain decode over the same pages is the reference."""
+    own, B, Hkv, N = 64 * 64, 64, 8, 64
+    lay = kv.dense_layout(128, N, Hkv, 64 * 40)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn((1, Hkv, lay.num_pages * 16, 128), generator=g, device="cuda").half() for _ in range(2))
+    cache, err = kv.alloc_cache(lay), kv.new_error_word()
+    pages = torch.arange(lay.num_pages, dtype=torch.int32, device="cuda")
+    kv.encode_tiles(k, v, lay, torch.zeros(1, dtype=torch.int32, device="cuda"), pages[None], cache, err)
+    prefix, L = 2 * N, 2 * N + own
+    tiles = torch.randint(0, lay.num_pages // 4, (B, L // N), generator=g, device="cuda")
+    tiles[:, :2] = tiles[0, :2]
+    bt = (tiles[..., None] * 4 + torch.arange(4, device="cuda")).flatten(1).to(torch.int32).contiguous()
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda") - torch.arange(B, device="cuda", dtype=torch.int32) % 5 * N
+    q = torch.randn((B, 1, 8, 128), generator=g, device="cuda").half()
+    outs = []
+    for shared in (True, False):
+        out, lse = torch.empty((B, 1, 8, 128), device="cuda"), torch.empty((B, 1, 8), device="cuda")
+        if shared:
+            ws = torch.empty(kv.decode_shared_workspace_bytes(lay, B, 8, 1, L, prefix), dtype=torch.uint8, device="cuda")
+            kv.decode_shared(q, lay, cache, bt[0, :prefix // 16].contiguous(), prefix, bt, lens, L, out, ws, err, 0.1, lse=lse)
+        else:
+            ws = torch.empty(kv.decode_verify_workspace_bytes(lay, B, 8, 1, L), dtype=torch.uint8, device="cuda")
+            kv.decode_verify(q, lay, cache, bt, lens, L, out, ws, err, 0.1, lse=lse)
+        torch.cuda.synchronize()
+        outs.append((out, lse))
+    assert kv.read_error_flags(err) == 0
+    # both sides: 64 accumulation steps of 2^-23 and exponents off by 2^-17
+    # of scores below 16
+    assert float((outs[0][0] - outs[1][0]).norm()) <= 2.0 ** -13 * float(outs[1][0].norm())
+    assert float((outs[0][1] - outs[1][1]).abs().max()) <= 2.0 ** -13
+
+
 def test_bad_pages_are_flagged_by_the_large_path():
     x = serving.Batch(128, 64, 8, 1, [4096 + 3] * 61, Q=2, prefix=4096, seed=4)
     good = x.prefix_table.copy()

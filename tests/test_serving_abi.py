@@ -93,6 +93,7 @@ def shared(L, lay=None, q=A16, Hq=64, Q=1, cache=A16, pt=A16, S=1024, bt=A16, bt
     (EINVAL, dict(cap=126)), (EINVAL, dict(Q=3, cap=128)), (EALIGN, dict(q=BAD)), (EALIGN, dict(tail=BAD)),
     (EALIGN, dict(cache=P((1 << 20) + 64))), (EWORKSPACE, dict(size=4096)), (EINVAL, dict(B=-1)), (EINVAL, dict(n=-1)),
     (EINVAL, dict(B=1 << 25)), (OK, dict(B=0)), (EINVAL, dict(out=None)), (EINVAL, dict(err=None)),
+    (EINVAL, dict(lay=kv.dense_layout(128, 128, 8, 0))),
 ])
 def test_shared_refusals(L, code, kw):
     assert shared(L, **kw) == code

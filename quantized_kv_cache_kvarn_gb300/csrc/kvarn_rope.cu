@@ -18,9 +18,9 @@
 // in registers and walks the heads of every tensor of the call with them, two
 // 16-byte vectors a head, kBatch heads in flight (in place, a load can not
 // move above a store by itself). What bounds it is HBM for prompts and the
-// launch for single tokens: 4 x 4096 tokens of 72 fp16 heads of 128 take 98
-// us, 0.91 of the measured copy bandwidth; 8 x 1021 tokens of 28 bf16 heads of
-// 256 with 64 turned channels 47 us, 0.73 (87 with the copied channels in a
+// launch for single tokens: 4 x 4096 tokens of 72 fp16 heads of 128 take 97
+// us, 0.92 of the measured copy bandwidth; 8 x 1021 tokens of 28 bf16 heads of
+// 256 with 64 turned channels 43 us, 0.80 (87 with the copied channels in a
 // loop of their own); 32 single tokens of 72 heads 3.5 us under a profiler.
 #include <algorithm>
 
@@ -32,7 +32,11 @@ namespace kvarn {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kBatch = 4;  // heads a thread has in flight
+// Heads a thread has in flight. Two keep 64 registers, and so more CTAs than
+// four (80) do: us with 1 / 2 / 3 / 4 / 8 heads, 8 x 1021 tokens of 256-wide
+// heads partly turned 48 / 44 / 48 / 48 / 50, 4 x 4096 tokens of 72 heads
+// 106 / 98 / 99 / 99 / 102, fp32 25 / 23 / 23 / 24 / 28.
+constexpr int kBatch = 2;
 
 // f / 2 pi modulo 1 as a 64-bit fraction, rounded to nearest. f = m 2^e with
 // a 53-bit m; 1 / 2 pi as a 128-bit fraction times m, shifted.

@@ -21,7 +21,7 @@
 // launch for single tokens: 4 x 4096 tokens of 72 fp16 heads of 128 take 97
 // us, 0.92 of the measured copy bandwidth; 8 x 1021 tokens of 28 bf16 heads of
 // 256 with 64 turned channels 43 us, 0.80 (87 with the copied channels in a
-// loop of their own); 32 single tokens of 72 heads 3.5 us under a profiler.
+// loop of their own); 32 single tokens of 72 heads 3.4 us under a profiler.
 #include <algorithm>
 
 #include "kvarn_common.cuh"

@@ -11,21 +11,27 @@
 //
 // fp32 results need more than one fp16 product: every operand is x = hi + lo
 // in fp16 (off by 2^-22 of its tile's or row's magnitude, which a power of two
-// brings to about 1 first: 2^eK, 2^eV per tile, 2^eq per row, put back with
-// the softmax's own scale, so that neither large nor small caches leave
-// fp16's range), and each product is hi hi + lo hi + hi lo, three MMAs with
-// fp32 accumulators in tensor memory. Codes as exact operands with the scales
-// folded around them (as in the dense decode) would need two, but their
-// column scales change q' with every tile and their row scales the output:
-// 576 + 320 more issue slots per SM and tile than this form spends.
+// brings to about 1 first: 2^eK, 2^eV per tile, 2^eq per row), and each
+// product is hi hi + lo hi + hi lo, three MMAs with fp32 accumulators in
+// tensor memory. eK and eq return with the scores' scale. eV goes into the
+// weights: P = 2^(S + eV - m), where m follows the largest S + eV of the row,
+// the bound of a token's share of the output, instead of the largest S alone.
+// So O = sum P V 2^-eV is in units of 2^m whichever tiles it adds up, tiles of
+// values of any sizes fit fp16 as operands, and what P loses below 2^-25 is
+// lost against the largest share. The sum of the weights takes 2^-eV back in
+// fp32. Codes as exact operands with the scales folded around them (as in the
+// dense decode) would need two, but their column scales change q' with every
+// tile and their row scales the output: 576 + 320 more issue slots per SM and
+// tile than this form spends.
 //
 // Roles (896 threads, one CTA per SM; registers moved to them with setmaxnreg):
 //   warps 0-7    softmax: two threads per row (= tensor-memory lane), 32 of
 //                the stage's 64 tokens each; a pair of warps exchanges its
 //                maxima through shared memory. Keeps the running maximum
-//                (raised only when a score passes it by 2^8, so that O is
-//                rescaled a few times at most) and sum, writes P hi / lo over
-//                the scores as the A operand
+//                of S + eV (an integer, so that it adds to eV and to the
+//                partial's exponent without rounding; raised only when passed
+//                by 2^8, so that O is rescaled a few times at most) and sum,
+//                writes P hi / lo over the scores as the A operand
 //   warps 8-23   dequantisation, K on eight and V on eight, warp = (page of the
 //                stage, 64-channel group): code planes -> exact fp16 (the
 //                decode's conversions) -> fp32 c (a code + b) -> hi and lo,
@@ -72,7 +78,7 @@ constexpr int kPlane = kStage * kD * 2;   // hi or lo operand plane: 16 KB
 constexpr int kRing = 2;                  // stages of K and of V in flight
 constexpr int kPages = 4;                 // most tiles whose pages are in shared memory or on their way
 constexpr int kMetaSlots = 8;             // tiles whose scales are kept: past kPages, the softmax may be three behind
-constexpr int kMeta = 6 * 128 * 4 + 16;   // cK, cV, aK, bK, aV, bV, 2^eK, eV
+constexpr int kMeta = 6 * 128 * 4 + 16;   // cK, cV, aK, bK, aV, bV, 2^eK, eV, 2^-eV
 constexpr int kOffK = 0, kOffV = kRing * 2 * kPlane, kOffMeta = 2 * kOffV, kOffScale = kOffMeta + kMetaSlots * kMeta;
 constexpr int kBarBytes = 320, kOffMax = kOffScale + kM * 4, kOffBar = kOffMax + 4 * kM * 4, kOffRaw = kOffBar + kBarBytes;
 constexpr int kQRow = 2 * kD * 2 + 16;    // staged query row: hi, lo, padding
@@ -86,7 +92,14 @@ constexpr uint32_t kIdQK = tc_idesc_f16(kM, kStage, false, false), kIdPV = tc_id
 constexpr int kSmemMax = 232448;
 static_assert(kOffRaw + 2 * 8 * DensePage(kD, 128, 8, 8, 4).bytes() + 1024 <= kSmemMax, "two tiles of the widest pages");
 constexpr long long kWait = 2000000000LL;
-constexpr float kRaise = 8.f;  // log2 of how far a score may pass the running maximum
+constexpr float kRaise = 8.f;  // log2 of how far a share may pass the running maximum
+// Exponents of a tile's values: 2^-60 to 2^60 is beyond what pages of fp16
+// values hold (2^-24 to 2^16 sqrt(128)), and keeps 2^-eV times a sum of
+// weights in fp32's range. A tile of zeros takes no share: an exponent kZeros
+// below that of the tile before (the first one: of 2^kFirstExp) keeps it from
+// raising the maximum unless its scores are as far above, and its weights,
+// down to 2^-126 of the maximum, in the sum.
+constexpr int kMostExp = 60, kZeros = 40, kFirstExp = -20;
 
 // Barriers by shared-memory address: one probe (the hardware may hold the
 // thread a short time; with a time hint it would poll with sleeps between),
@@ -395,9 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
     };
     const float kq = rscale[r];
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;  // O and l are in units of 2^m
     bool ok = true;
-    int e0 = 0;  // O is in units of 2^e0
     for (int s = 0; s < stages; ++s) {
       const int tile = spt == 1 ? s : s >> 1;
       // PV(s - 2) has completed by then; waiting for it keeps the parity of
@@ -418,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       tc_fence_after();
       const float* meta = reinterpret_cast<const float*>(sm + kOffMeta + (tile & (kMetaSlots - 1)) * kMeta);
       const float k = kq * meta[6 * 128];
-      const int ev = reinterpret_cast<const int*>(meta)[6 * 128 + 1];
-      e0 = reinterpret_cast<const int*>(meta)[6 * 128 + 2];
+      const float ev = meta[6 * 128 + 1];
       uint32_t x[32];
       const uint32_t scol = tl + kColS + 64 * (s & 1);
       tc_ld32(scol + 32 * half, x);
@@ -437,14 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         ok = false;
         break;
       }
-      const float mt = fmaxf(mine, other) * k;
-      // a score far above the maximum so far: O and l are brought to the new
+      const float mt = fmaf(fmaxf(mine, other), k, ev);
+      // a share far above the maximum so far: O and l are brought to the new
       // one. The first stage has nothing to rescale. Half 0 takes O, half 1
-      // its small products.
+      // its small products. l takes the factor's square root twice: after a
+      // tile of small values it is as much larger (2^-eV) as the factor is
+      // below fp32's range.
       const bool raise = mt > m + kRaise || (m == -INFINITY && mt > m);
       if (__any_sync(0xffffffffu, raise)) {
-        const float m_new = raise ? mt : m;
-        const float alpha = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
+        const float m_new = raise ? ceilf(mt) : m;
+        const float root = m == -INFINITY ? 0.f : fast_exp2(0.5f * (m - m_new)), alpha = root * root;
         if (s > 0) {
           if (!wait(B_OF + ((s - 1) & 1), ((s - 1) >> 1) & 1)) {
             ok = false;
@@ -465,11 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           tc_wait_st();
         }
         if (raise) {
-          l *= alpha;
+          l = l * root * root;
           m = m_new;
         }
       }
-      const float2 k2 = f2(k), z2 = f2(static_cast<float>(ev) - m);
+      const float2 k2 = f2(k), z2 = f2(ev - m);
       float2 sum[2] = {f2(0.f), f2(0.f)};
       uint32_t hi[16], lo[16];
 #pragma unroll
@@ -483,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       tc_st16(scol + 16 * half, hi);
       tc_st16(scol + 32 + 16 * half, lo);
       const float2 st = f2add(sum[0], sum[1]);
-      l = fmaf(st.x + st.y, pow2i(-ev), l);
+      l = fmaf(st.x + st.y, meta[6 * 128 + 2], l);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -502,11 +515,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       const int pr = kM * blk + (row ? r : 0);
       const int64_t at = static_cast<int64_t>(pr / A.G) * A.Hq + kvh * A.G + pr % A.G;
       float* part = A.ws + (at * A.slots + split) * kPStride(kD);
+      // in units that bring the sum to [1, 2), as the other partials of the
+      // row have it to within their number of tokens
+      l += l1;
+      const int el = exponent_of(l);
+      const float u0 = pow2i(-(el / 2)), u1 = pow2i(-(el - el / 2));
       if (row && !half) {
-        part[0] = m;
-        part[1] = l + l1;
+        part[0] = m + static_cast<float>(el);
+        part[1] = l * u0 * u1;
       }
-      const float u0 = pow2i(e0 / 2), u1 = pow2i(e0 - e0 / 2);
 #pragma unroll 1
       for (int q = 2 * half; q < 2 * half + 2; ++q) {
         uint32_t o[32], small[32];
@@ -652,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const float ctr = bits == 3 || bits == 5 || bits == 8 ? static_cast<float>(1 << (bits - 1)) : 0.f;
     const float top = static_cast<float>((1 << bits) - 1);
     const int cshift = spt == 1 ? 5 : 4, cmask = (1 << cshift) - 1;  // columns per page: 32 or 16
-    int ev0 = 0;
+    int ev = kFirstExp;
     for (int tile = 0; kv < 2 && tile < n; ++tile) {
       if (!wait(B_RF + tile % ring, (tile / ring) & 1)) break;
       const unsigned char* raw = sm + kOffRaw + (tile % ring) * A.tile_bytes + base;
@@ -687,21 +704,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       row_max = warp_max_xor(row_max, 1, 32);
       col_max = warp_max_xor(col_max, 1, 32);
       int e = exponent_of(row_max) + exponent_of(col_max) + 1;
-      if (kv) {
-        // O keeps the first tile's unit; a tile's difference goes into its
-        // weights, within fp16's range (the largest is 2^kRaise)
-        if (tile == 0) ev0 = max(-100, min(100, e));
-        e = ev0 + max(-6, min(6, e - ev0));
-      } else {
-        e = max(-100, min(100, e));
-      }
+      if (!kv) e = max(-100, min(100, e));
+      else if (row_max * col_max == 0.f) e = ev - kZeros;
+      else e = ev = max(-kMostExp, min(kMostExp, e));
       const float d0 = pow2i(-(e / 2)), d1 = pow2i(-(e - e / 2));
 #pragma unroll
       for (int j = 0; j < 4; ++j) meta[128 * kv + lane + 32 * j] = cv[j] * d0 * d1;
       if (lane == 0) {
         if (kv) {
-          reinterpret_cast<int*>(meta)[6 * 128 + 1] = e - ev0;
-          reinterpret_cast<int*>(meta)[6 * 128 + 2] = ev0;
+          meta[6 * 128 + 1] = static_cast<float>(e);
+          meta[6 * 128 + 2] = pow2i(-e);
         } else {
           meta[6 * 128] = pow2i(e);
         }

@@ -390,9 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const int r = tid & (kM - 1), half = tid / kM;  // row; tokens [32 half, +32) of every stage
     // warps w and w + 4 share rows and meet once a stage at a named barrier;
     // [stage parity][half][row] for what they exchange. The barrier itself
-    // has no time limit: a warp that gives up arrives there once without
-    // waiting (leave), after it has set the abort flag, and its partner
-    // looks at the flag behind the barrier and leaves too.
+    // has no time limit, so a warp never goes without its arrival at the next
+    // one (leave), whether a wait of its own ran out or it found the abort
+    // flag set behind a barrier: its partner may have looked a moment before
+    // another role set the flag, and be on its way to the next barrier. There
+    // it finds the flag set and leaves too; an arrival that nobody meets
+    // does no harm.
     float* xch = reinterpret_cast<float*>(sm + kOffMax);
     const int pair = 1 + (warp & 3);
     auto meet = [&](int s, float mine, float& other) -> bool {
@@ -446,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       float other;
       if (!meet(s, mine, other)) {  // both have read their scores, too: P may take their place
         ok = false;
+        leave();
         break;
       }
       const float mt = fmaf(fmaxf(mine, other), k, ev);

@@ -86,7 +86,7 @@ static_assert(kM * kQRow <= kOffMeta, "query rows are staged in the operand ring
 static_assert(kOffRaw % 16 == 0 && kOffMeta % 1024 == 0, "layout");
 enum { B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SF = 8, B_PF = 10, B_OF = 12, B_FIN = 14, B_RF = 15, B_RE = B_RF + kPages,
        B_META = B_RE + kPages, kBars = B_META + kMetaSlots };
-static_assert(kBars * 8 + 8 <= kBarBytes, "barriers");
+static_assert(kBars * 8 + 8 + 2 * 8 * 4 <= kBarBytes, "barriers, tensor-memory address, abort flag, the pairs' views of it");
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256, kColL = 384;  // tensor-memory columns
 constexpr uint32_t kIdQK = tc_idesc_f16(kM, kStage, false, false), kIdPV = tc_idesc_f16(kM, kD, false, false);
 constexpr int kSmemMax = 232448;
@@ -390,23 +390,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const int r = tid & (kM - 1), half = tid / kM;  // row; tokens [32 half, +32) of every stage
     // warps w and w + 4 share rows and meet once a stage at a named barrier;
     // [stage parity][half][row] for what they exchange. The barrier itself
-    // has no time limit, so a warp never goes without its arrival at the next
-    // one (leave), whether a wait of its own ran out or it found the abort
-    // flag set behind a barrier: its partner may have looked a moment before
-    // another role set the flag, and be on its way to the next barrier. There
-    // it finds the flag set and leaves too; an arrival that nobody meets
-    // does no harm.
+    // has no time limit, so both act on the same view of the abort flag: what
+    // each saw before the barrier, [stage parity][pair][half], either of which
+    // sends both away. (Behind the barrier each might see another state of
+    // the flag, and one would go and the other wait at the next meeting.) A
+    // warp whose wait runs out says so and arrives at the next meeting, s,
+    // without waiting (leave).
     float* xch = reinterpret_cast<float*>(sm + kOffMax);
+    volatile int* seen = abort_flag + 1 + 2 * (warp & 3);
     const int pair = 1 + (warp & 3);
     auto meet = [&](int s, float mine, float& other) -> bool {
       xch[((s & 1) * 2 + half) * kM + r] = mine;
+      if (lane == 0) seen[(s & 1) * 8 + half] = *abort_flag;
       tc_fence_before();
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
       tc_fence_after();
       other = xch[((s & 1) * 2 + (half ^ 1)) * kM + r];
-      return __all_sync(0xffffffffu, *abort_flag == 0);
+      return __all_sync(0xffffffffu, (seen[(s & 1) * 8] | seen[(s & 1) * 8 + 1]) == 0);
     };
-    auto leave = [&]() {
+    auto leave = [&](int s) {
+      if (lane == 0) seen[(s & 1) * 8 + half] = 1;
       __syncwarp();
       asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
     };
@@ -420,14 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       // rescaled
       if (s >= 2 && !wait(B_OF + (s & 1), ((s >> 1) & 1) ^ 1)) {
         ok = false;
-        leave();
+        leave(s);
         break;
       }
       // the tile's exponents (their barrier can not have gone on by two
       // phases: eight tiles ahead is further than the copies get)
       if (!wait(B_SF + (s & 1), (s >> 1) & 1) || !wait(B_META + (tile & (kMetaSlots - 1)), (tile / kMetaSlots) & 1)) {
         ok = false;
-        leave();
+        leave(s);
         break;
       }
       tc_fence_after();
@@ -449,7 +452,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       float other;
       if (!meet(s, mine, other)) {  // both have read their scores, too: P may take their place
         ok = false;
-        leave();
         break;
       }
       const float mt = fmaf(fmaxf(mine, other), k, ev);
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         if (s > 0) {
           if (!wait(B_OF + ((s - 1) & 1), ((s - 1) >> 1) & 1)) {
             ok = false;
-            leave();
+            leave(s + 1);
             break;
           }
           tc_fence_after();
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (ok) {
       ok = (stages < 2 || wait(B_OF + (stages & 1), ((stages - 2) >> 1) & 1)) &&
            wait(B_OF + ((stages - 1) & 1), ((stages - 1) >> 1) & 1);
-      if (!ok) leave();
+      if (!ok) leave(stages);
     }
     float l1;
     if (ok && meet(stages, l, l1)) {

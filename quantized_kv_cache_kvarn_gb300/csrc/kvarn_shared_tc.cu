@@ -86,12 +86,13 @@ static_assert(kM * kQRow <= kOffMeta, "query rows are staged in the operand ring
 static_assert(kOffRaw % 16 == 0 && kOffMeta % 1024 == 0, "layout");
 enum { B_KF = 0, B_KE = 2, B_VF = 4, B_VE = 6, B_SF = 8, B_PF = 10, B_OF = 12, B_FIN = 14, B_RF = 15, B_RE = B_RF + kPages,
        B_META = B_RE + kPages, kBars = B_META + kMetaSlots };
-static_assert(kBars * 8 + 8 + 2 * 8 * 4 <= kBarBytes, "barriers, tensor-memory address, abort flag, the pairs' views of it");
+static_assert(kBars * 8 + 8 <= kBarBytes, "barriers");
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256, kColL = 384;  // tensor-memory columns
 constexpr uint32_t kIdQK = tc_idesc_f16(kM, kStage, false, false), kIdPV = tc_idesc_f16(kM, kD, false, false);
 constexpr int kSmemMax = 232448;
 static_assert(kOffRaw + 2 * 8 * DensePage(kD, 128, 8, 8, 4).bytes() + 1024 <= kSmemMax, "two tiles of the widest pages");
 constexpr long long kWait = 2000000000LL;
+constexpr uint32_t kGone = 0x7f800badu;
 constexpr float kRaise = 8.f;  // log2 of how far a share may pass the running maximum
 // Exponents of a tile's values: 2^-60 to 2^60 is beyond what pages of fp16
 // values hold (2^-24 to 2^16 sqrt(128)), and keeps 2^-eV times a sum of
@@ -391,25 +392,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     // warps w and w + 4 share rows and meet once a stage at a named barrier;
     // [stage parity][half][row] for what they exchange. The barrier itself
     // has no time limit, so both act on the same view of the abort flag: what
-    // each saw before the barrier, [stage parity][pair][half], either of which
-    // sends both away. (Behind the barrier each might see another state of
-    // the flag, and one would go and the other wait at the next meeting.) A
-    // warp whose wait runs out says so and arrives at the next meeting, s,
-    // without waiting (leave).
-    float* xch = reinterpret_cast<float*>(sm + kOffMax);
-    volatile int* seen = abort_flag + 1 + 2 * (warp & 3);
+    // either saw before the barrier, told by a word in place of its value
+    // (kGone, a NaN that no arithmetic forms), sends both away. (Behind the
+    // barrier each might see another state of the flag, and one would go and
+    // the other wait at the next meeting.) A warp whose wait runs out says so
+    // and arrives at the next meeting, s, without waiting (leave).
+    uint32_t* xch = reinterpret_cast<uint32_t*>(sm + kOffMax);
     const int pair = 1 + (warp & 3);
-    auto meet = [&](int s, float mine, float& other) -> bool {
-      xch[((s & 1) * 2 + half) * kM + r] = mine;
-      if (lane == 0) seen[(s & 1) * 8 + half] = *abort_flag;
+    auto meet = [&](int s, bool gone, float mine, float& other) -> bool {
+      xch[((s & 1) * 2 + half) * kM + r] = gone ? kGone : __float_as_uint(mine);
       tc_fence_before();
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
       tc_fence_after();
-      other = xch[((s & 1) * 2 + (half ^ 1)) * kM + r];
-      return __all_sync(0xffffffffu, (seen[(s & 1) * 8] | seen[(s & 1) * 8 + 1]) == 0);
+      const uint32_t word = xch[((s & 1) * 2 + (half ^ 1)) * kM + r];
+      other = __uint_as_float(word);
+      return __all_sync(0xffffffffu, !gone && word != kGone);
     };
     auto leave = [&](int s) {
-      if (lane == 0) seen[(s & 1) * 8 + half] = 1;
+      xch[((s & 1) * 2 + half) * kM + r] = kGone;
       __syncwarp();
       asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
     };
@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         break;
       }
       tc_fence_after();
+      const bool gone = __any_sync(0xffffffffu, *abort_flag != 0);
       const float* meta = reinterpret_cast<const float*>(sm + kOffMeta + (tile & (kMetaSlots - 1)) * kMeta);
       const float k = kq * meta[6 * 128];
       const float ev = meta[6 * 128 + 1];
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       }
       const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       float other;
-      if (!meet(s, mine, other)) {  // both have read their scores, too: P may take their place
+      if (!meet(s, gone, mine, other)) {  // both have read their scores, too: P may take their place
         ok = false;
         break;
       }
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       if (!ok) leave(stages);
     }
     float l1;
-    if (ok && meet(stages, l, l1)) {
+    if (ok && meet(stages, __any_sync(0xffffffffu, *abort_flag != 0), l, l1)) {
       tc_fence_after();
       const bool row = r < rows;
       const int pr = kM * blk + (row ? r : 0);

@@ -87,11 +87,10 @@ def text():
 
 def test_the_kernel_meets_as_the_model_does(text):
     body = text[text.index("auto meet = "):text.index("auto leave = ")]
-    steps = ["seen[(s & 1) * 8 + half] = *abort_flag;", "bar.sync", "seen[(s & 1) * 8] | seen[(s & 1) * 8 + 1]"]
-    at = [body.index(s) for s in steps]
-    assert at == sorted(at) and body.count("abort_flag") == 1
+    at = [body.index(s) for s in ("half) * kM + r] = gone ? kGone", "bar.sync", "!gone && word != kGone")]
+    assert at == sorted(at) and "abort_flag" not in body  # the flag is read by the caller, before
     body = text[text.index("auto leave = "):text.index("const float kq")]
-    at = [body.index(s) for s in ("seen[(s & 1) * 8 + half] = 1;", "__syncwarp();", "bar.arrive")]
+    at = [body.index(s) for s in ("half) * kM + r] = kGone;", "__syncwarp();", "bar.arrive")]
     assert at == sorted(at)
 
 

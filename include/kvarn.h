@@ -683,12 +683,13 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
 
 /*
  * kvarn_set_copy_wait_test - diagnostic of the dense decode kernels'
- * (kvarn_decode, _verify, _window, _fp16, _noalloc, _mass, _shared's dense
- * part, kvarn_affine_decode)
- * bounded waits for their page copies, so that a test can drive the time-out
- * path without making a copy fail. `cycles`: how long a wait lasts before the
- * kernel gives up (0 restores the default, 2e9 cycles, about a second; a limit
- * below 1e5 cycles is kept by polling instead of the suspending wait).
+ * (kvarn_decode, _verify, _window, _fp16, _noalloc, _mass, _shared,
+ * kvarn_affine_decode) bounded waits for their page copies, and of all waits
+ * of kvarn_decode_shared's tensor-core kernel, so that a test can drive the
+ * time-out path without making a copy fail. `cycles`: how long a wait lasts
+ * before the kernel gives up (0 restores the default, 2e9 cycles, about a
+ * second; a limit below 1e5 cycles is kept by polling instead of the
+ * suspending wait).
  * `withhold` = 1: every copy is announced 16 bytes larger than it is (or, for
  * copies by the threads themselves, one thread's arrival is withheld), so
  * that no copy's phase ever completes and every wait runs out, while the

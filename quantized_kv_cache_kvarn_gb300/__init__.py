@@ -673,6 +673,7 @@ def decode_shared(q, layout: Layout, cache, prefix_table, prefix_tokens, block_t
 
 def set_copy_wait_test(cycles: int, withhold: bool = False) -> None:
     """Diagnostic: clock cycles the dense decode kernels wait for a page copy
-    before they flag DEVERR_TIMEOUT and return (0: the default), and whether
+    (decode_shared's tensor-core kernel: for any of its roles) before they
+    flag DEVERR_TIMEOUT and return (0: the default), and whether
     every copy is announced larger than it is so that every wait runs out."""
     _check(lib().kvarn_set_copy_wait_test(cycles, 1 if withhold else 0), "set_copy_wait_test")

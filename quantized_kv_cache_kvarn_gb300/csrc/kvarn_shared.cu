@@ -210,6 +210,8 @@ cudaError_t launch_decode_shared(const DecodeParams& p, const SharedPlan& plan, 
     T.tile_bytes = p.N / kPageTokens * pg.bytes();
     T.ws = pre;
     T.slots = plan.prefix.slots;
+    T.wait_limit = A.wait_limit;
+    T.withhold = A.withhold;
     T.err = p.err;
     e = launch_shared_tc(T, plan.tc_units, st);
   } else {

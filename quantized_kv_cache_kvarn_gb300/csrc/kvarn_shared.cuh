@@ -21,6 +21,8 @@ struct SharedTcArgs {
   int32_t ring;           // tiles of pages in shared memory (set by the launch)
   float* ws;              // partials [row][slots]
   int32_t slots;          // splits
+  long long wait_limit;   // clock cycles a wait lasts before the kernel gives up
+  int32_t withhold;       // diagnostic: every copy is announced this many bytes larger (its phase never completes)
   uint32_t* err;
 };
 

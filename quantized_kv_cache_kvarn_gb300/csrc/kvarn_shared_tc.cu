@@ -91,7 +91,7 @@ constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256, kColL = 384;  // tensor-
 constexpr uint32_t kIdQK = tc_idesc_f16(kM, kStage, false, false), kIdPV = tc_idesc_f16(kM, kD, false, false);
 constexpr int kSmemMax = 232448;
 static_assert(kOffRaw + 2 * 8 * DensePage(kD, 128, 8, 8, 4).bytes() + 1024 <= kSmemMax, "two tiles of the widest pages");
-constexpr long long kWait = 2000000000LL;
+constexpr long long kMmaWait = 2000000000LL, kDrainWait = 100000000LL;  // cycles: about a second, 50 ms
 constexpr uint32_t kGone = 0x7f800badu;
 constexpr float kRaise = 8.f;  // log2 of how far a share may pass the running maximum
 // Exponents of a tile's values: 2^-60 to 2^60 is beyond what pages of fp16
@@ -250,6 +250,11 @@ __device__ __forceinline__ void dequant_v(const unsigned char* page, const float
   }
 }
 
+// POLL: a call whose waits are limited to less than kPollWaitBelow, which a
+// probe's own suspension may outlast, keeps the limit by tests that do not
+// suspend. A diagnostic's setting, so a kernel of its own: asked at run time,
+// it cost 32 x 64 heads over 16384 tokens 2.7 us of 87.
+template <bool POLL>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedTcArgs A) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -264,18 +269,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   float* rscale = reinterpret_cast<float*>(sm + kOffScale);
   const uint32_t bar0 = smem_addr(bars);
   // Bounded wait, uniform over the warp; gives up (and tells every role to)
-  // after about a second or once another warp has given up. The clock and the
+  // after the call's limit or once another warp has given up. The clock and the
   // flag are looked at every 32 probes only: a waiting warp takes issue slots
   // from the working ones.
   auto wait = [&](int bar, uint32_t parity) -> bool {
     const uint32_t at = bar0 + 8 * bar;
-    if (__all_sync(0xffffffffu, probe(at, parity))) return true;
+    if (!POLL && __all_sync(0xffffffffu, probe(at, parity))) return true;
     bool ok = false;
     const long long start = clock64();
     do {
+      if (POLL) ok = mbar_test_phase(bars + bar, parity);
 #pragma unroll 1
-      for (int i = 0; i < 32 && !ok; ++i) ok = probe(at, parity);
-    } while (!ok && !*abort_flag && clock64() - start <= kWait);
+      for (int i = 0; !POLL && i < 32 && !ok; ++i) ok = probe(at, parity);
+    } while (!ok && !*abort_flag && clock64() - start <= A.wait_limit);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *abort_flag = 1;
     return ok;
@@ -646,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     }
     if (elect_one()) tc_commit(bars + B_FIN);
     __syncwarp();
-    mbar_wait_bounded(bars + B_FIN, 0, kWait);  // every MMA issued has completed
+    mbar_wait_bounded(bars + B_FIN, 0, kMmaWait);  // every MMA issued has completed
   } else {
     // ------------------------------------------- page copies and scales
     regs_dec<kRegsOther>();
@@ -655,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     auto issue = [&](int tile) {
       const int slot = tile % ring;
       const int32_t* pt = A.table + static_cast<int64_t>(t0 + tile) * ppt;
-      if (lane == 0) mbar_arrive_expect_tx(bars + B_RF + slot, A.tile_bytes);
+      if (lane == 0) mbar_arrive_expect_tx(bars + B_RF + slot, A.tile_bytes + A.withhold);
       __syncwarp();
       if (lane < ppt) {
         int phys = pt[lane];
@@ -736,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     }
     // copies still in flight land before the CTA exits
     for (int tile = max(0, issued - ring); tile < issued; ++tile)
-      mbar_wait_bounded(bars + B_RF + tile % ring, (tile / ring) & 1, kWait);
+      if (!mbar_wait_bounded(bars + B_RF + tile % ring, (tile / ring) & 1, kDrainWait)) break;
   }
 
   tc_fence_before();
@@ -774,7 +780,8 @@ cudaError_t launch_shared_tc(const SharedTcArgs& args, int units, cudaStream_t s
   SharedTcArgs A = args;
   A.ring = std::min(kPages, (kSmemMax - 1024 - kOffRaw) / A.tile_bytes);  // two at least: the largest tile has 35840 bytes
   const int smem = kOffRaw + A.ring * A.tile_bytes + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kern = A.wait_limit < kPollWaitBelow ? shared_tc_kernel<true> : shared_tc_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(A.slots, units);
@@ -786,7 +793,7 @@ cudaError_t launch_shared_tc(const SharedTcArgs& args, int units, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_tc_kernel, A);
+  return cudaLaunchKernelEx(&cfg, kern, A);
 }
 
 }  // namespace kvarn

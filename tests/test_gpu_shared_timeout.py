@@ -87,4 +87,5 @@ def test_waits_that_run_out_anywhere():
         if k % 10 == 0:
             got, flags, _ = call()
             assert flags == 0 and torch.equal(got, want)
-    assert gave_up > 0
+    parity.report(f"shared-prefix waits of 1 to 56,000 cycles: {gave_up} of 120 calls gave up")
+    assert 0 < gave_up < 120

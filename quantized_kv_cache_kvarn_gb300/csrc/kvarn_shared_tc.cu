@@ -781,7 +781,8 @@ cudaError_t launch_shared_tc(const SharedTcArgs& args, int units, cudaStream_t s
   A.ring = std::min(kPages, (kSmemMax - 1024 - kOffRaw) / A.tile_bytes);  // two at least: the largest tile has 35840 bytes
   const int smem = kOffRaw + A.ring * A.tile_bytes + 1024;
   auto kern = A.wait_limit < kPollWaitBelow ? shared_tc_kernel<true> : shared_tc_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the process's, not the call's: one value for calls of every layout, which other threads may be making
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(A.slots, units);

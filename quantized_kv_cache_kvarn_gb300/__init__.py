@@ -439,9 +439,10 @@ def _addr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap):
-    """The checks of the decode calls' common tensors (q: [B, ..., Hq, D]);
-    returns the block table's row stride."""
+def _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap, pages):
+    """The checks of the decode calls' common tensors (q: [B, ..., Hq, D];
+    `pages` entries of a block table row may be read); returns the block
+    table's row stride."""
     kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
     shape = q.shape
     B, Hkv, D = shape[0], layout.num_kv_heads, layout.head_dim
@@ -451,6 +452,8 @@ def _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspac
             or cache.numel() < layout.num_pages * Hkv * page_bytes(layout)):
         _refuse(what, "cache is not contiguous bytes of the layout's pages")
     bt_stride = _row_stride(what, "block_table", block_table, torch.int32, B)
+    if block_table.shape[1] < pages:  # rows further apart than they are long: the C ABI sees the stride alone
+        _refuse(what, f"block_table has fewer columns than max_seq_len has committed pages ({pages})")
     if seq_lens.dtype is not torch.int32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
         _refuse(what, f"seq_lens must be a contiguous int32 vector of {B}")
     if out.dtype is not torch.float32 or out.shape != shape or not out.is_contiguous():
@@ -591,7 +594,7 @@ def decode_mass(q, layout: Layout, cache, block_table, seq_lens, max_seq_len, ou
     B, Hq, _ = q.shape
     dev = _device_of(what, q, cache, block_table, seq_lens, out, mass_in, mass_out, workspace, err, tail_k, tail_v, lse)
     bt_stride = _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse,
-                                layout.tile_tokens)
+                                layout.tile_tokens, max_seq_len // layout.tile_tokens * (layout.tile_tokens // 16))
     stride = _row_stride(what, "mass_in", mass_in, torch.float32, B)
     if _row_stride(what, "mass_out", mass_out, torch.float32, B) != stride or mass_out.shape != mass_in.shape:
         _refuse(what, "mass_in and mass_out differ in shape or stride")
@@ -659,7 +662,9 @@ def decode_shared(q, layout: Layout, cache, prefix_table, prefix_tokens, block_t
     B, Q, Hq, _ = q.shape
     cap = tail_k.shape[2] if tail_k is not None and tail_k.dim() == 4 else max(1, layout.tile_tokens + Q - 2)
     dev = _device_of(what, q, cache, prefix_table, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse)
-    bt_stride = _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap)
+    own = max(0, max_seq_len - Q + 1) // layout.tile_tokens * layout.tile_tokens
+    bt_stride = _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap,
+                                own // 16 if own > prefix_tokens else 0)
     if (prefix_table.dtype is not torch.int32 or prefix_table.dim() != 1 or not prefix_table.is_contiguous()
             or prefix_table.shape[0] * 16 < prefix_tokens):
         _refuse(what, "prefix_table must be a contiguous int32 vector of the prefix's pages")

@@ -652,7 +652,9 @@ int32_t kvarn_decode_shared(const void* q, int32_t num_q_heads, int32_t num_quer
  *                positions (queries and keys, in one launch). Element (b, n,
  *                h, d) is at b*seq_stride + n*token_stride + h*head_stride +
  *                d (elements). in = out (with equal strides) turns in place;
- *                otherwise the two must not overlap
+ *                otherwise the two must not overlap, nor may an output
+ *                overlap another tensor of the call (KVARN_EINVAL where they
+ *                begin at the same address)
  *   dtype        of every tensor: 0 fp16, 1 bf16, 2 fp32
  *   positions    device int32, token n of sequence b at b*pos_stride + n (a
  *                pos_stride of 0: shared by the batch); any value

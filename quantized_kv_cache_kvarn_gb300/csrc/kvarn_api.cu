@@ -779,6 +779,9 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
     if (t.in == t.out && (t.in_seq_stride != t.out_seq_stride || t.in_token_stride != t.out_token_stride ||
                           t.in_head_stride != t.out_head_stride))
       return KVARN_EINVAL;
+    // a tensor is written while the others are read and written
+    for (int32_t j = 0; j < p.num_tensors; ++j)
+      if (t.out == p.t[j].out || t.out == p.t[j].in || t.in == p.t[j].out) return KVARN_EINVAL;
     p.t[p.num_tensors++] = {t.in,            t.out,            t.in_seq_stride,   t.in_token_stride, t.in_head_stride,
                             t.out_seq_stride, t.out_token_stride, t.out_head_stride, t.num_heads,      t.head_dim};
   }

@@ -771,8 +771,12 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
   if (!positions || !inv_freq) return KVARN_EINVAL;
   if (!aligned(positions, 4) || !aligned(inv_freq, 8)) return KVARN_EALIGN;
   for (int32_t k = 0; k < num_tensors; ++k) {
-    const kvarn_rope_tensor& t = tensors[k];
+    kvarn_rope_tensor t = tensors[k];
     if (t.num_heads == 0) continue;
+    // the stride of an axis of length one says nothing
+    if (num_seqs == 1) t.in_seq_stride = t.out_seq_stride = 0;
+    if (num_tokens == 1) t.in_token_stride = t.out_token_stride = 0;
+    if (t.num_heads == 1) t.in_head_stride = t.out_head_stride = 0;
     if (!t.in || !t.out) return KVARN_EINVAL;
     if (!aligned(t.in, size) || !aligned(t.out, size)) return KVARN_EALIGN;
     // in place: every element is written where it was read

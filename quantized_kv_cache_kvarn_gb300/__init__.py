@@ -620,11 +620,13 @@ def evict_tiles(mass_in, block_table, seq_lens, layout: Layout, max_seq_len, kee
     rows = _row_stride(what, "block_table", block_table, torch.int32, B)
     shape, strides = block_table.shape, block_table.stride()
     for name, t in (("block_table_out", block_table_out), ("freed", freed)):
-        if t.dtype is not torch.int32 or t.shape != shape or t.stride() != strides:
+        if t.dtype is not torch.int32 or t.shape != shape or (
+                t.stride() != strides and _row_stride(what, name, t, torch.int32, B) != rows):
             _refuse(what, f"{name} differs from block_table in type, shape or stride")
     masses = _row_stride(what, "mass_in", mass_in, torch.float32, B)
     mshape = mass_in.shape
-    if mass_out.dtype is not torch.float32 or mass_out.shape != mshape or mass_out.stride() != mass_in.stride():
+    if mass_out.dtype is not torch.float32 or mass_out.shape != mshape or (
+            mass_out.stride() != mass_in.stride() and _row_stride(what, "mass_out", mass_out, torch.float32, B) != masses):
         _refuse(what, "mass_out differs from mass_in in type, shape or stride")
     N = layout.tile_tokens
     tiles = max_seq_len // N

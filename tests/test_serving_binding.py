@@ -76,3 +76,33 @@ def test_block_tables_of_a_prefix_and_queries(calls):
     with pytest.raises(kv.KvarnError, match="block_table"):
         decode_shared(table(2, 15, 40), 259, prefix=128, Q=4)
     assert len(calls) == 3
+
+
+def evict(mass_in, mass_out, block_table, table_out, freed):
+    B = mass_in.shape[0]
+    ints = [torch.zeros(B, dtype=torch.int32) for _ in range(3)]
+    kv.evict_tiles(mass_in, block_table, ints[0], kv.dense_layout(128, 128, 1, 8), 256, 1, mass_out, table_out, ints[1], freed,
+                   ints[2], torch.zeros(1, dtype=torch.int32))
+
+
+def mass(rows, columns, stride=None):
+    return table(rows, columns, stride).view(torch.float32)
+
+
+def test_eviction_of_one_row_takes_any_distance_of_rows(calls):
+    evict(mass(1, 2, 9), mass(1, 2, 2), table(1, 16, 99), table(1, 16), table(1, 16, 50))
+    evict(mass(1, 2), mass(1, 2, 7), table(1, 16), table(1, 16, 40), table(1, 16))
+    assert len(calls) == 2
+
+
+@pytest.mark.parametrize("which", ["mass_out", "block_table_out", "freed"])
+def test_eviction_of_several_rows_takes_one_distance(calls, which):
+    made = dict(mass_out=mass(2, 2, 9), block_table_out=table(2, 16, 99), freed=table(2, 16, 99))
+    evict(mass(2, 2, 9), made["mass_out"], table(2, 16, 99), made["block_table_out"], made["freed"])
+    made[which] = mass(2, 2, 8) if which == "mass_out" else table(2, 16, 98)
+    with pytest.raises(kv.KvarnError, match=which):
+        evict(mass(2, 2, 9), made["mass_out"], table(2, 16, 99), made["block_table_out"], made["freed"])
+    made[which] = (mass if which == "mass_out" else table)(2, 16 if which != "mass_out" else 2, 99)[:, ::2]
+    with pytest.raises(kv.KvarnError, match=which):
+        evict(mass(2, 2, 9), made["mass_out"], table(2, 16, 99), made["block_table_out"], made["freed"])
+    assert len(calls) == 1

@@ -587,8 +587,8 @@ int32_t kvarn_decode_mass(const void* q, int32_t num_q_heads, float sm_scale, co
  *                      to entry T * N/P; freed_count[b] of them
  *   seq_lens, seq_lens_out  device int32 [num_seqs]
  *   keep_tiles         >= sink_tiles + recent_tiles
- * The outputs may be the inputs (mass_out = mass_in and so on); freed is a
- * buffer of its own. A length outside [0, max_seq_len] sets
+ * The outputs may be the inputs (mass_out = mass_in and so on); freed and
+ * freed_count are buffers of their own. A length outside [0, max_seq_len] sets
  * KVARN_DEVERR_SEQ_LEN and is clamped. num_seqs is at most 65535.
  */
 int32_t kvarn_evict_tiles(const float* mass_in, float* mass_out, int32_t mass_stride, const int32_t* block_table,

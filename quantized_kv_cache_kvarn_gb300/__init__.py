@@ -612,8 +612,8 @@ def evict_tiles(mass_in, block_table, seq_lens, layout: Layout, max_seq_len, kee
     """Shorten every sequence over `keep_tiles` tiles to that many: its first
     sink_tiles, its newest recent_tiles and the tiles of largest mass between
     them. Tables [B, >= T * N/16] int32 and masses [B, >= T] float32, T =
-    max_seq_len / N; outputs may be the inputs, freed (the dropped page ids,
-    freed_count of them per row) is a tensor of its own."""
+    max_seq_len / N; outputs may be the inputs, freed (the dropped page ids) and
+    freed_count (how many per row) are tensors of their own."""
     what = "evict_tiles"
     B = seq_lens.shape[0]
     dev = _device_of(what, mass_in, block_table, seq_lens, mass_out, block_table_out, seq_lens_out, freed, freed_count, err)

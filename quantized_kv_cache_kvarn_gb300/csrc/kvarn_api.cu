@@ -726,6 +726,7 @@ int32_t kvarn_evict_tiles(const float* mass_in, float* mass_out, int32_t mass_st
       !aligned(freed, 4) || !aligned(seq_lens, 4) || !aligned(seq_lens_out, 4) || !aligned(freed_count, 4) ||
       !aligned(error_flags, 4))
     return KVARN_EALIGN;
+  if (freed_count == seq_lens_out || freed_count == seq_lens) return KVARN_EINVAL;
   EvictParams p{};
   p.mass = mass_in;
   p.mass_out = mass_out;

@@ -41,3 +41,10 @@ def test_rope_outputs_of_a_call_are_tensors_of_their_own(L, pairs):
 
 def test_rope_looks_only_at_tensors_with_heads(L):
     assert rope(L, [(1, 1), (1, 1)], heads=(0, 0)) == OK
+
+
+@pytest.mark.parametrize("lens,lens_out,count", [(A[6], A[7], A[7]), (A[6], A[6], A[6]), (A[6], A[7], A[6])])
+def test_eviction_counts_into_a_buffer_of_its_own(L, lens, lens_out, count):
+    lay = kv.dense_layout(128, 128, 8, 10)
+    assert L.kvarn_evict_tiles(A[0], A[1], 8, A[2], A[3], A[4], 64, lens, lens_out, count, 1024, 2, ctypes.byref(lay), 4, 1, 1, A[8],
+                               None) == EINVAL

@@ -501,6 +501,7 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.
     if yarn is not None:
         f, length, fast, slow = (*yarn, 32.0, 1.0)[:4] if len(yarn) == 2 else yarn
         _need(f >= 1 and length > 0 and fast > slow > 0, "rope_frequencies: yarn factor, length or turns out of range")
+        _need(base > 1, "rope_frequencies: yarn needs a base above 1")
 
         def dim_of(turns):  # the (fractional) i whose frequency turns so often in the trained length
             return rope_dim * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base))

@@ -94,13 +94,13 @@ static_assert(kOffRaw + 2 * 8 * DensePage(kD, 128, 8, 8, 4).bytes() + 1024 <= kS
 constexpr long long kMmaWait = 2000000000LL, kDrainWait = 100000000LL;  // cycles: about a second, 50 ms
 constexpr uint32_t kGone = 0x7f800badu;
 constexpr float kRaise = 8.f;  // log2 of how far a share may pass the running maximum
-// Exponents of a tile's values: 2^-60 to 2^60 is beyond what pages of fp16
-// values hold (2^-24 to 2^16 sqrt(128)), and keeps 2^-eV times a sum of
-// weights in fp32's range. A tile of zeros takes no share: an exponent kZeros
-// below that of the tile before (the first one: of 2^kFirstExp) keeps it from
-// raising the maximum unless its scores are as far above, and its weights,
-// down to 2^-126 of the maximum, in the sum.
-constexpr int kMostExp = 60, kZeros = 40, kFirstExp = -20;
+// Exponents of a tile's values: between them 2^-eV times a sum of weights (at
+// most 2^8 a token) stays in fp32's range, and values to 2^125 in fp16's. A
+// tile of zeros takes no share: an exponent kZeros below that of the tile
+// before (the least where there is none) keeps it from raising the maximum
+// unless its scores are as far above, and its weights, down to 2^-126 of the
+// maximum, in the sum.
+constexpr int kLeastExp = -90, kMostExp = 110, kZeros = 40, kLeastZeros = -100;
 
 // Barriers by shared-memory address: one probe (the hardware may hold the
 // thread a short time; with a time hint it would poll with sleeps between),
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const float ctr = bits == 3 || bits == 5 || bits == 8 ? static_cast<float>(1 << (bits - 1)) : 0.f;
     const float top = static_cast<float>((1 << bits) - 1);
     const int cshift = spt == 1 ? 5 : 4, cmask = (1 << cshift) - 1;  // columns per page: 32 or 16
-    int ev = kFirstExp;
+    int ev = kLeastExp;
     for (int tile = 0; kv < 2 && tile < n; ++tile) {
       if (!wait(B_RF + tile % ring, (tile / ring) & 1)) break;
       const unsigned char* raw = sm + kOffRaw + (tile % ring) * A.tile_bytes + base;
@@ -718,8 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       col_max = warp_max_xor(col_max, 1, 32);
       int e = exponent_of(row_max) + exponent_of(col_max) + 1;
       if (!kv) e = max(-100, min(100, e));
-      else if (row_max * col_max == 0.f) e = ev - kZeros;
-      else e = ev = max(-kMostExp, min(kMostExp, e));
+      else if (row_max * col_max == 0.f) e = max(kLeastZeros, ev - kZeros);
+      else e = ev = max(kLeastExp, min(kMostExp, e));
       const float d0 = pow2i(-(e / 2)), d1 = pow2i(-(e - e / 2));
 #pragma unroll
       for (int j = 0; j < 4; ++j) meta[128 * kv + lane + 32 * j] = cv[j] * d0 * d1;

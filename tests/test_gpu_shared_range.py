@@ -26,6 +26,10 @@ CASES = {
     "fp16_scales_16": (64, 8192, (4, 4, 2), torch.float16, lambda t: -8 if t % 5 == 0 else 8),
     "zeros_first": (128, 8192, (4, 2, 4), torch.float16, lambda t: None if t < 2 else -12),
     "zeros_fifths": (128, 8192, (4, 2, 4), torch.float16, lambda t: None if t % 5 == 0 else 8 if t % 2 else -14),
+    "huge_bf16": (128, 8192, (4, 2, 4), torch.bfloat16, lambda t: 104 if t % 5 == 0 else 90),
+    "tiny_bf16": (64, 4096, (4, 2, 4), torch.bfloat16, lambda t: -86 if t % 5 == 0 else -80),
+    "zeros_tiny_bf16": (128, 8192, (4, 2, 4), torch.bfloat16, lambda t: None if t % 5 == 0 else -80),
+    "zeros_huge_bf16": (128, 8192, (4, 2, 4), torch.bfloat16, lambda t: None if t % 5 == 4 else 100),
     "zeros_only": (128, 8192, (4, 2, 4), torch.float16, lambda t: None),
 }
 B, Q, HQ, D, DIR = 61, 2, 8, 128, 10.6

@@ -106,3 +106,9 @@ def test_eviction_of_several_rows_takes_one_distance(calls, which):
     with pytest.raises(kv.KvarnError, match=which):
         evict(mass(2, 2, 9), made["mass_out"], table(2, 16, 99), made["block_table_out"], made["freed"])
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("base", [1.0, 0.5])
+def test_yarn_needs_frequencies_that_fall(base):
+    with pytest.raises(kv.KvarnError, match="base"):
+        kv.rope_frequencies(64, base, yarn=(2.0, 4096), device="cpu")

@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         break;
       }
       tc_fence_after();
-      const bool gone = __any_sync(0xffffffffu, *abort_flag != 0);
+      const bool gone = *abort_flag != 0;
       const float* meta = reinterpret_cast<const float*>(sm + kOffMeta + (tile & (kMetaSlots - 1)) * kMeta);
       const float k = kq * meta[6 * 128];
       const float ev = meta[6 * 128 + 1];
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       if (!ok) leave(stages);
     }
     float l1;
-    if (ok && meet(stages, __any_sync(0xffffffffu, *abort_flag != 0), l, l1)) {
+    if (ok && meet(stages, *abort_flag != 0, l, l1)) {
       tc_fence_after();
       const bool row = r < rows;
       const int pr = kM * blk + (row ? r : 0);

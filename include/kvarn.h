@@ -549,7 +549,8 @@ int32_t kvarn_affine_decode(const void* q, int32_t num_q_heads, float sm_scale, 
  * 6 or 8; KVARN_EUNSUPPORTED for other widths.
  * Other arguments and results as kvarn_decode; out and lse are bit for bit
  * those of kvarn_decode. The sums are taken in a fixed order: the same call
- * gives the same masses. num_seqs is at most 65535.
+ * gives the same masses. A query with a NaN makes its sequence's masses NaN.
+ * num_seqs is at most 65535.
  */
 int64_t kvarn_decode_mass_workspace_bytes(const kvarn_layout* layout, int32_t num_seqs, int32_t num_q_heads,
                                           int32_t max_seq_len);
@@ -645,8 +646,9 @@ int32_t kvarn_decode_shared(const void* q, int32_t num_q_heads, int32_t num_quer
  * that with respect to y (and, for scale = 1, the inverse). Frequencies
  * scaled for long contexts are the caller's table; scale is the factor that
  * such scalings put on queries and keys. The angle is reduced modulo a turn
- * in 64-bit fixed point, exact for any position; the arithmetic is fp32, the
- * result rounded once to the tensors' type.
+ * in 64-bit fixed point, off by less than 2^-33 turns at any position, and
+ * the signed rest rounded to fp32 (by 2^-24 of itself at most); the arithmetic
+ * is fp32, the result rounded once to the tensors' type.
  *
  *   tensors      host array of 1 .. KVARN_ROPE_MAX_TENSORS tensors that share
  *                positions (queries and keys, in one launch). Element (b, n,

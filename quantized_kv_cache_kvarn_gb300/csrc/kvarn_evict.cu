@@ -18,9 +18,10 @@
 // meeting, so that the outputs may be the inputs. Rows whose ranges do not
 // fit shared memory take one CTA, which reads its keys again in every pass
 // and compacts chunk by chunk.
-// Latency bounds it: five cluster meetings and two trips to memory. 8
-// sequences of up to 16384 tiles take 20 us (one CTA per sequence 50), 32 of
-// up to 128 tiles 11, of which the launch and the host are the most.
+// Latency bounds it: six cluster meetings (four passes, the counts, the one
+// before the fill) and two trips to memory. 8 sequences of up to 16384 tiles
+// take 20 us (one CTA per sequence 50), 32 of up to 128 tiles 11, of which the
+// launch and the host are the most.
 #include <cooperative_groups.h>
 
 #include "kvarn_common.cuh"

@@ -130,7 +130,8 @@ struct SplitPlan {
   int32_t slots;   // nsplit + 1 (the tail)
 };
 
-constexpr int32_t kRawChunk = 128;  // smallest split of the raw (sink and tail) records of the dense decode
+// Smallest split of the raw (sink and tail) records of the dense decode's stream-K plan, largest of its pieces' (down to 32).
+constexpr int32_t kRawChunk = 128;
 
 // Plan of the compressed decode: `ctas` persistent CTAs share the flattened
 // list of compressed tiles (stream-K), each taking at least `min_tiles` of
@@ -141,7 +142,7 @@ struct DensePlan {
   int32_t min_tiles;
   int32_t tile_slots;  // partial slots per row reserved for tiles
   int32_t raw_splits;
-  int32_t raw_chunk;   // raw tokens per raw split (kRawChunk times a power of two)
+  int32_t raw_chunk;   // raw tokens per raw split (kRawChunk times a power of two, over one in the pieces' plan)
   int32_t slots;       // tile_slots + raw_splits
   int32_t piece;       // > 0: pieces of so many tiles within each unit instead of stream-K ranges
   int32_t raw_last;    // raw items from the last CTA down (the grid has CTAs to spare for them)

@@ -11,7 +11,9 @@
 // fp64 frequency, off by less than 2^-64 turns plus the frequency's own
 // rounding), and p F_i modulo 2^64 drops the whole turns exactly, so a
 // position of 2^31 costs no accuracy and no fp64 arithmetic (a GB300 SM has
-// about two fp64 lanes). Cosine and sine are taken of the signed fraction.
+// about two fp64 lanes). Cosine and sine are taken of the signed fraction
+// rounded to fp32, which turns by at most 2^-24 of the angle, itself at most
+// half a turn, more or less: as much as the fp32 arithmetic behind it.
 //
 // A CTA takes `tok` tokens: its threads form the tok x R/2 cosines and sines
 // once in shared memory, each thread keeps those of its token and pair chunk
@@ -237,7 +239,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 }
 
-// Any alignment: one thread per pair or copied channel of a (token, head).
+// Any alignment: one thread per pair or copied channel of a (token, head),
+// which forms its own cosine and sine. That bounds it: 4 x 4096 tokens of 72
+// fp16 heads of 128 take 808 us with 64 channels turned from channel 4 on and
+// 1021 us with 20 turned, 0.6 to 0.75 TB/s; 32 single tokens 9.6 us a call.
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_constant__ RopeParams A) {
   using V = RopeVec<T>;

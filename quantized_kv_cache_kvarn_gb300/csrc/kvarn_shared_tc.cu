@@ -48,7 +48,7 @@
 // the sum of its small products (lo hi + hi lo): the tensor cores truncate the
 // accumulator at every step, so the long sum takes four steps a stage instead
 // of twelve (error against 64 bits at 16384 tokens with one accumulator:
-// 5.4e-6, the fp32 form's is 2.5e-6).
+// 5.4e-6, with two 2.7e-6, of the fp32 form 2.6e-6).
 // A stage costs the tensor pipe 24 MMAs of N = 64 and 12 of N = 128: 1536
 // cycles per 64 tokens and 128 rows. Measured, 256 rows of 8 KV heads over
 // 16384 tokens: 56 us, about 2870 cycles a stage, tensor pipe 43% and issue

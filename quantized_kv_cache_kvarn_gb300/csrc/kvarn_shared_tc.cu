@@ -92,7 +92,7 @@ constexpr uint32_t kIdQK = tc_idesc_f16(kM, kStage, false, false), kIdPV = tc_id
 constexpr int kSmemMax = 232448;
 static_assert(kOffRaw + 2 * 8 * DensePage(kD, 128, 8, 8, 4).bytes() + 1024 <= kSmemMax, "two tiles of the widest pages");
 constexpr long long kMmaWait = 2000000000LL, kDrainWait = 100000000LL;  // cycles: about a second, 50 ms
-constexpr uint32_t kGone = 0x7f800badu;
+constexpr uint32_t kGone = 0x7f800badu;  // in place of a value between a pair's warps: one of them gives up
 constexpr float kRaise = 8.f;  // log2 of how far a share may pass the running maximum
 // Exponents of a tile's values: between them 2^-eV times a sum of weights (at
 // most 2^8 a token) stays in fp32's range, and values to 2^125 in fp16's. A

@@ -22,19 +22,20 @@ def built():
 
 
 class Call:
-    """A call whose prefix goes to the tensor-core kernel (122 rows of eight,
-    4096 tokens); without tiles of its own, so that no other kernel waits for
-    a copy."""
+    """A call whose prefix goes to the tensor-core kernel (61 sequences: 122
+    rows of eight, 4096 tokens), without tiles of its own (own below 64), so
+    that no other kernel waits for a copy; or to the dense kernel (4)."""
 
-    def __init__(self, own=3):
-        x = serving.Batch(128, 64, 8, 1, [4096 + own] * 61, Q=2, prefix=4096, seed=4)
+    def __init__(self, own=3, sequences=61, dim=128):
+        B = sequences
+        x = serving.Batch(dim, 64, 8, 1, [4096 + own] * B, Q=2, prefix=4096, seed=4)
         self.lay, self.n = x.layout_of(), int(x.lens.max())
         self.cache, self.prefix, self.bt, self.lens, self.q, self.tk, self.tv = (
             t.cuda() for t in (torch.from_numpy(x.cache), torch.from_numpy(x.prefix_table), torch.from_numpy(x.bt),
                                torch.from_numpy(x.lens), x.q, x.tail_k, x.tail_v))
         self.sm = x.sm
-        self.out = torch.empty((61, 2, 8, 128), device="cuda")
-        self.ws = torch.empty(kv.decode_shared_workspace_bytes(self.lay, 61, 8, 2, self.n, 4096), dtype=torch.uint8,
+        self.out = torch.empty((B, 2, 8, dim), device="cuda")
+        self.ws = torch.empty(kv.decode_shared_workspace_bytes(self.lay, B, 8, 2, self.n, 4096), dtype=torch.uint8,
                               device="cuda")
         self.err = kv.new_error_word()
 
@@ -50,9 +51,9 @@ class Call:
         return self.out.clone(), kv.read_error_flags(self.err), took
 
 
-@pytest.mark.parametrize("own", [3, 70])
-def test_copies_that_never_complete(own):
-    call = Call(own)
+@pytest.mark.parametrize("own,sequences,dim", [(3, 61, 128), (70, 61, 128), (70, 4, 128), (3, 4, 256), (150, 4, 256)])
+def test_copies_that_never_complete(own, sequences, dim):
+    call = Call(own, sequences, dim)
     want, flags, _ = call()
     assert flags == 0
     for cycles in (1_000_000, 50_000):
@@ -61,7 +62,8 @@ def test_copies_that_never_complete(own):
             _, flags, took = call()
         finally:
             kv.set_copy_wait_test(0, withhold=False)
-        parity.report(f"shared-prefix time-out ({own} own tokens, {cycles} cycles): error word {flags:#x} after {took * 1e3:.0f} ms")
+        parity.report(f"shared-prefix time-out ({sequences} x {own} own tokens, head_dim {dim}, {cycles} cycles): error word "
+                      f"{flags:#x} after {took * 1e3:.0f} ms")
         assert flags == kv.DEVERR_TIMEOUT
         assert took < 1.0  # the limit, 50 ms for the copies under way, launches
         got, flags, _ = call()

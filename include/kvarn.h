@@ -137,6 +137,7 @@ typedef enum {
 #define KVARN_DEVERR_NO_TAIL    0x2u  /* a raw record (tail or sink) is needed but its buffer is NULL */
 #define KVARN_DEVERR_TIMEOUT    0x4u  /* a page copy did not complete in time (see kvarn_set_copy_wait_test) */
 #define KVARN_DEVERR_SEQ_LEN    0x8u  /* seq_len < 0 or above max_seq_len */
+#define KVARN_DEVERR_INDEX      0x10u /* a row index outside the batch (kvarn_fork_sequences) */
 
 typedef struct {
   int32_t head_dim;     /* D: 128, 256 (dense) or 512 (latent) */
@@ -686,9 +687,265 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
                    kvarn_stream_t stream);
 
 /*
+ * The 8-bit block cache: attention over a cache held in 8 bits, with one
+ * scale for each block of tokens and head, and with a sliding window. (The
+ * pages describing the method have no counterpart of these calls.)
+ *
+ * A block is the P = 16 tokens of a page of one KV head. Of its keys, and
+ * likewise of its values: A = the largest magnitude, at least 2^-100; M = 448
+ * (KVARN_Q8_E4M3: codes are e4m3 numbers) or 127 (KVARN_Q8_INT8: whole
+ * numbers); scale = A * (1 / M) and inverse = (1 / A) * M, each quotient and
+ * product rounded to fp32; code = x * inverse, the fp32 product rounded to the
+ * nearest code, ties to even; value = code * scale. A block with an infinity or a NaN reads as NaN throughout. A
+ * block is coded once it is full: the tokens past the last whole block are
+ * raw rows in a tail buffer owned by the caller.
+ *
+ * Layout: head_dim 128 or 256, tile_tokens = page_tokens = 16, k_bits =
+ * v_bits = 8, rope_dim 0; norm_iters and scale_dtype are ignored. `code` of
+ * every call on a cache is the same. Page of one KV head, 32 D + 32 bytes:
+ *   [0, 16D)     K codes, one row of D bytes per token, whose 16-byte units
+ *                sit at unit u XOR 4(token % 2); int8 codes plus 128
+ *   [16D, 32D)   V codes: lane L = 4g + t owns one 32-bit word per 8-channel
+ *                block nc, byte j + 2h of it channel 8nc + g of token 8h + 2t
+ *                + j; the word sits at byte 16(32(nc/4) + L) + 4(nc%4)
+ *   [32D, +4)    K scale fp32    [32D + 4, +4)  V scale    [32D + 8, +24) 0
+ *
+ * kvarn_q8_encode_blocks writes, for every sequence b and u <
+ * chunk_tokens / 16, tokens [16u, 16u + 16) of the chunk as logical block
+ * block_start[b] + u (a negative block_start skips the sequence).
+ * kvarn_q8_read_blocks writes the values of the same blocks to k and v,
+ * rounded once to kv_dtype (for attention of the next prompt chunk, or for
+ * checking), and leaves skipped sequences' rows as they were.
+ *   k, v         device, kv_dtype, element (b, h, i, d) at b*seq_stride +
+ *                h*head_stride + i*token_stride + d; strides multiples of 8
+ *   block_start  device int32 [num_seqs]
+ *   block_table  device int32, rows of bt_stride entries; a block at or past
+ *                bt_stride, or a page outside the cache, sets
+ *                KVARN_DEVERR_PAGE_RANGE and is skipped
+ *
+ * kvarn_q8_append takes the newest token of every sequence, at position
+ * seq_lens[b] - 1: it becomes row (seq_lens[b] - 1) % 16 of the raw tail, or
+ * completes a block, which is coded into its page from the tail's 15 rows and
+ * the token (the tail is then free). A length of 0 skips the sequence. The
+ * decision is taken on the device.
+ *   k, v         device, kv_dtype [num_seqs][Hkv][D]
+ *   tail_k/v     device, kv_dtype [num_seqs][Hkv][tail_capacity][D],
+ *                tail_capacity >= 15
+ */
+#define KVARN_Q8_E4M3 0
+#define KVARN_Q8_INT8 1
+
+int64_t kvarn_q8_page_bytes(const kvarn_layout* layout);
+
+int32_t kvarn_q8_encode_blocks(const void* k, const void* v, int64_t seq_stride, int64_t head_stride,
+                               int64_t token_stride, int32_t num_seqs, int32_t chunk_tokens,
+                               const int32_t* block_start, const int32_t* block_table, int32_t bt_stride,
+                               const kvarn_layout* layout, int32_t code, void* cache, uint32_t* error_flags,
+                               kvarn_stream_t stream);
+
+int32_t kvarn_q8_read_blocks(void* k, void* v, int64_t seq_stride, int64_t head_stride, int64_t token_stride,
+                             int32_t num_seqs, int32_t chunk_tokens, const int32_t* block_start,
+                             const int32_t* block_table, int32_t bt_stride, const kvarn_layout* layout, int32_t code,
+                             const void* cache, uint32_t* error_flags, kvarn_stream_t stream);
+
+int32_t kvarn_q8_append(const void* k, const void* v, const int32_t* seq_lens, int32_t max_seq_len, void* tail_k,
+                        void* tail_v, int32_t tail_capacity, int32_t num_seqs, const int32_t* block_table,
+                        int32_t bt_stride, const kvarn_layout* layout, int32_t code, void* cache,
+                        uint32_t* error_flags, kvarn_stream_t stream);
+
+/*
+ * kvarn_q8_decode - decode or verification over the 8-bit block cache, with a
+ * sliding window whose first tokens stay visible.
+ *
+ * Sequence b holds L = seq_lens[b] tokens, the last Q = num_queries under
+ * verification as in kvarn_decode_verify (Q = 1: plain decode): blocks [0, C),
+ * C = floor((L - Q + 1) / 16), come from the pages and tokens [16C, L) from
+ * rows 0.. of the raw tail. Query j, at position p = L - Q + j, sees the
+ * tokens i <= p with i < sink_tokens or i > p - window (window 0: all of
+ * them, sink_tokens is then not looked at). Time goes with what is seen:
+ * pages outside are not read, their table entries may be anything.
+ *
+ *   q              device, kv_dtype [num_seqs][Q][num_q_heads][D]
+ *   num_queries    1 .. KVARN_MAX_VERIFY_QUERIES
+ *   tail_k/v       device, kv_dtype [num_seqs][Hkv][tail_capacity][D], or
+ *                  NULL when no sequence has tokens past its whole blocks
+ *   tail_capacity  >= Q + 14
+ *   window, sink_tokens  >= 0
+ *   out, lse       as kvarn_decode_verify
+ *   workspace      >= kvarn_q8_decode_workspace_bytes(...)
+ * A query that sees no token gives out = 0 and lse = -inf. Values of hidden
+ * tokens do not matter, whatever they are. At most 8 query heads per KV head;
+ * num_seqs * Q * num_q_heads is at most 2^30. seq_lens outside [0,
+ * max_seq_len] set KVARN_DEVERR_SEQ_LEN and are clamped. The sums are taken in
+ * a fixed order: the same call gives the same bits.
+ */
+int64_t kvarn_q8_decode_workspace_bytes(const kvarn_layout* layout, int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t num_queries, int32_t max_seq_len, int32_t window,
+                                        int32_t sink_tokens);
+
+int32_t kvarn_q8_decode(const void* q, int32_t num_q_heads, int32_t num_queries, float sm_scale, const void* cache,
+                        const kvarn_layout* layout, int32_t code, const int32_t* block_table, int32_t bt_stride,
+                        const int32_t* seq_lens, int32_t max_seq_len, const void* tail_k, const void* tail_v,
+                        int32_t tail_capacity, int32_t window, int32_t sink_tokens, int32_t num_seqs, float* out,
+                        float* lse, void* workspace, int64_t workspace_bytes, uint32_t* error_flags,
+                        kvarn_stream_t stream);
+
+/*
+ * kvarn_norm_rope - norms of queries and keys for each head and their rotary
+ * positions in one pass, and the gradient. (The pages describing the method
+ * leave both to the engine.)
+ *
+ * A head x of D = head_dim channels becomes z_d = x_d r (w_d + weight_offset),
+ * r = (mean of x^2 + eps)^-1/2, and z is turned as by kvarn_rope: channels
+ * rope_offset + [0, rope_dim) by positions[b][n] * inv_freq, times scale; the
+ * other channels are z. weight_offset is 0, or 1 for weights stored as their
+ * distance from one. rope_dim 0: no rotation (positions and inv_freq are not
+ * looked at).
+ *
+ * kvarn_norm_rope_backward takes the same x and the gradient dy of the output
+ * and gives dx and, where dweight is not NULL, the gradient of the weights,
+ * summed over tokens and heads (fp32, overwritten; the sums are taken in a
+ * fixed order, the same call gives the same bits).
+ *
+ *   tensors      host array of 1 .. KVARN_ROPE_MAX_TENSORS tensors that share
+ *                positions and D (queries and keys). Element (b, n, h, d) of
+ *                x is at b*x_seq_stride + n*x_token_stride + h*x_head_stride +
+ *                d (elements), of out (the output, or dx) and of dy likewise.
+ *                out may be x (or dy) where the strides are equal; otherwise
+ *                it may not overlap a tensor of the call (KVARN_EINVAL where
+ *                they begin at the same address). weight: [D] or NULL (ones)
+ *   dtype, weight_dtype  0 fp16, 1 bf16, 2 fp32 (of x, dy, out; of the weights)
+ *   eps          >= 0; with eps 0 a head of zeros gives NaN
+ *   workspace    backward: >= kvarn_norm_rope_backward_workspace_bytes(...),
+ *                16-byte aligned; not looked at where no dweight is wanted
+ * Other arguments and limits as kvarn_rope. Tensors whose addresses and
+ * strides are all multiples of 16 bytes, with D a multiple of 32 bytes' worth
+ * of elements and at most 1024 bytes long, and rope_dim / 2 and rope_offset
+ * multiples of 16 bytes' worth, take the vector path; others one element at a
+ * time.
+ */
+typedef struct {
+  const void* x;
+  const void* dy;
+  void* out;
+  const void* weight;
+  float* dweight;
+  int64_t x_seq_stride, x_token_stride, x_head_stride;
+  int64_t dy_seq_stride, dy_token_stride, dy_head_stride;
+  int64_t out_seq_stride, out_token_stride, out_head_stride;
+  int32_t num_heads;
+  int32_t reserved;
+} kvarn_norm_rope_tensor;
+
+int32_t kvarn_norm_rope(const kvarn_norm_rope_tensor* tensors, int32_t num_tensors, int32_t head_dim, int32_t dtype,
+                        int32_t weight_dtype, int32_t num_seqs, int32_t num_tokens, const int32_t* positions,
+                        int64_t pos_stride, const double* inv_freq, int32_t rope_dim, int32_t rope_offset,
+                        int32_t interleaved, float scale, float eps, float weight_offset, kvarn_stream_t stream);
+
+int64_t kvarn_norm_rope_backward_workspace_bytes(const int32_t* num_heads, int32_t num_tensors, int32_t head_dim,
+                                                 int32_t num_seqs, int32_t num_tokens);
+
+int32_t kvarn_norm_rope_backward(const kvarn_norm_rope_tensor* tensors, int32_t num_tensors, int32_t head_dim,
+                                 int32_t dtype, int32_t weight_dtype, int32_t num_seqs, int32_t num_tokens,
+                                 const int32_t* positions, int64_t pos_stride, const double* inv_freq,
+                                 int32_t rope_dim, int32_t rope_offset, int32_t interleaved, float scale, float eps,
+                                 float weight_offset, void* workspace, int64_t workspace_bytes,
+                                 kvarn_stream_t stream);
+
+/*
+ * kvarn_fork_sequences - a batch's next rows: sequences that go on, fork (one
+ * row becomes several, as in beam search), end, or leave pages behind a
+ * sliding window. (The pages describing the method have no counterpart of
+ * this call.) For any cache of this library: whole tiles are never written
+ * again, so rows that fork share pages, counted in page_refs; a raw tail is
+ * copied.
+ *
+ * New row b continues old row a = parents[b] (negative: an empty row, length
+ * 0; an index >= num_in sets KVARN_DEVERR_INDEX and counts as negative):
+ * seq_lens_out[b] = seq_lens[a]; the row's table entries below those of the
+ * floor((L - recent_tokens) / N) whole tiles of its L tokens are copied, the
+ * others up to entry T * N/P, T = max_seq_len / N, are -1. Negative entries
+ * are places without a page and stay -1; a page outside the cache sets
+ * KVARN_DEVERR_PAGE_RANGE and becomes -1. With window > 0, tiles that the next
+ * token (at position L) does not see, those that neither hold one of the first
+ * sink_tokens tokens nor one after position L - window, become -1 too.
+ *
+ * page_refs_out[p] = page_refs[p] - the times that old rows name p + the times
+ * that new rows do: references of others than these rows stay. freed: the
+ * pages whose count fell from above 0 to 0, ascending, then -1 up to entry
+ * num_pages; freed_count[0] of them.
+ *
+ *   parents        device int32 [num_out]; num_in, num_out at most 32768
+ *   seq_lens       device int32 [num_in]; outside [0, max_seq_len]: sets
+ *                  KVARN_DEVERR_SEQ_LEN, clamped
+ *   block_table    device int32, rows of both tables bt_stride apart, >= T * N/P
+ *   page_refs, page_refs_out, freed  device int32 [layout->num_pages], at most
+ *                  2^23; page_refs_out may be page_refs
+ *   tails          host array of num_tails <= KVARN_FORK_MAX_TAILS buffers
+ *                  [row][num_heads][capacity][row_bytes] (keys, values, a
+ *                  latent's rope part): row b of out gets the first L -
+ *                  (tokens in whole tiles) rows of every head of row a of in,
+ *                  at most capacity, or all of them (whole = 1: raw sinks); its
+ *                  other rows stay as they are. Addresses and row_bytes
+ *                  multiples of 16.
+ *   layout         tile_tokens, page_tokens and num_pages are looked at
+ * Outputs other than page_refs_out are buffers of their own.
+ */
+#define KVARN_FORK_MAX_TAILS 4
+
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t row_bytes;
+  int32_t num_heads;
+  int32_t capacity;
+  int32_t whole;
+  int32_t reserved;
+} kvarn_fork_tail;
+
+int32_t kvarn_fork_sequences(const int32_t* parents, int32_t num_in, int32_t num_out, const int32_t* seq_lens,
+                             int32_t* seq_lens_out, int32_t max_seq_len, const int32_t* block_table,
+                             int32_t* block_table_out, int32_t bt_stride, const int32_t* page_refs,
+                             int32_t* page_refs_out, int32_t* freed, int32_t* freed_count,
+                             const kvarn_fork_tail* tails, int32_t num_tails, const kvarn_layout* layout,
+                             int32_t recent_tokens, int32_t window, int32_t sink_tokens, uint32_t* error_flags,
+                             kvarn_stream_t stream);
+
+/*
+ * kvarn_compact_pages - move the n pages in use to ids 0 .. n - 1, so that the
+ * rest of the cache is free in one piece. (The pages describing the method
+ * have no counterpart of this call.) For any cache of this library.
+ *
+ * A page is in use where page_refs[p] > 0. Pages in use below n stay; the k-th
+ * free id below n receives the k-th page in use from n on. remap[p] is the new
+ * id of page p, -1 of a free one; live_count[0] = n; page_refs_out[p] is the
+ * count of the page now at p, 0 from n on; block_table_out holds the new ids
+ * of block_table's entries (negative ones become -1; one outside the cache or
+ * of a free page sets KVARN_DEVERR_PAGE_RANGE and becomes -1). The bytes of
+ * ids from n on stay as they are.
+ *
+ *   cache        [num_pages][page_stride] bytes; page_stride = Hkv * the page
+ *                bytes of one head (of the latent cache: its page bytes), a
+ *                multiple of 16
+ *   num_pages    at most 2^30
+ *   block_table  device int32 [num_rows][entries], rows of both tables
+ *                bt_stride apart; num_rows may be 0 (tables NULL). Tables of
+ *                another batch on the same cache: renumber them with remap
+ *   page_refs_out, block_table_out  may be page_refs, block_table
+ *   workspace    >= kvarn_compact_workspace_bytes(num_pages), 16-byte aligned
+ */
+int64_t kvarn_compact_workspace_bytes(int64_t num_pages);
+
+int32_t kvarn_compact_pages(void* cache, int64_t page_stride, int64_t num_pages, const int32_t* page_refs,
+                            int32_t* page_refs_out, const int32_t* block_table, int32_t* block_table_out,
+                            int32_t num_rows, int32_t entries, int32_t bt_stride, int32_t* remap,
+                            int32_t* live_count, void* workspace, int64_t workspace_bytes, uint32_t* error_flags,
+                            kvarn_stream_t stream);
+
+/*
  * kvarn_set_copy_wait_test - diagnostic of the dense decode kernels'
  * (kvarn_decode, _verify, _window, _fp16, _noalloc, _mass, _shared,
- * kvarn_affine_decode) bounded waits for their page copies, and of all waits
+ * kvarn_affine_decode, kvarn_q8_decode) bounded waits for their page copies, and of all waits
  * of kvarn_decode_shared's tensor-core kernel, so that a test can drive the
  * time-out path without making a copy fail. `cycles`: how long a wait lasts
  * before the kernel gives up (0 restores the default, 2e9 cycles, about a

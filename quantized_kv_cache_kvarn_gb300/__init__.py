@@ -20,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libkvarn.so")
 
 FP16, BF16 = 0, 1
-DEVERR_PAGE_RANGE, DEVERR_NO_TAIL, DEVERR_TIMEOUT, DEVERR_SEQ_LEN = 0x1, 0x2, 0x4, 0x8
+DEVERR_PAGE_RANGE, DEVERR_NO_TAIL, DEVERR_TIMEOUT, DEVERR_SEQ_LEN, DEVERR_INDEX = 0x1, 0x2, 0x4, 0x8, 0x10
 
 
 class KvarnError(RuntimeError):
@@ -53,6 +53,21 @@ class RopeTensor(ctypes.Structure):
                 + [(f"{side}_{axis}_stride", ctypes.c_int64) for side in ("in", "out")
                    for axis in ("seq", "token", "head")]
                 + [("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)])
+
+
+class NormRopeTensor(ctypes.Structure):
+    """Mirror of kvarn_norm_rope_tensor."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "dy", "out", "weight", "dweight")]
+                + [(f"{side}_{axis}_stride", ctypes.c_int64) for side in ("x", "dy", "out")
+                   for axis in ("seq", "token", "head")]
+                + [("num_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)])
+
+
+class ForkTail(ctypes.Structure):
+    """Mirror of kvarn_fork_tail."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
+                ("num_heads", ctypes.c_int32), ("capacity", ctypes.c_int32), ("whole", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -102,6 +117,22 @@ _SIGS = {
                              _P, _I64, _P, _P], _I32),
     "kvarn_rope": ([ctypes.POINTER(RopeTensor), _I32, _I32, _I32, _I32, _P, _I64, _P, _I32, _I32, _I32, _F32, _I32,
                     _P], _I32),
+    "kvarn_norm_rope": ([ctypes.POINTER(NormRopeTensor), _I32, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _I32, _I32, _I32,
+                         _F32, _F32, _F32, _P], _I32),
+    "kvarn_norm_rope_backward_workspace_bytes": ([ctypes.POINTER(_I32), _I32, _I32, _I32, _I32], _I64),
+    "kvarn_norm_rope_backward": ([ctypes.POINTER(NormRopeTensor), _I32, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _I32,
+                                  _I32, _I32, _F32, _F32, _F32, _P, _I64, _P], _I32),
+    "kvarn_fork_sequences": ([_P, _I32, _I32, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _P, ctypes.POINTER(ForkTail), _I32,
+                              _LP, _I32, _I32, _I32, _P, _P], _I32),
+    "kvarn_compact_workspace_bytes": ([_I64], _I64),
+    "kvarn_compact_pages": ([_P, _I64, _I64, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _P], _I32),
+    "kvarn_q8_page_bytes": ([_LP], _I64),
+    "kvarn_q8_encode_blocks": ([_P, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _I32, _LP, _I32, _P, _P, _P], _I32),
+    "kvarn_q8_read_blocks": ([_P, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _I32, _LP, _I32, _P, _P, _P], _I32),
+    "kvarn_q8_append": ([_P, _P, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _LP, _I32, _P, _P, _P], _I32),
+    "kvarn_q8_decode_workspace_bytes": ([_LP, _I32, _I32, _I32, _I32, _I32, _I32], _I64),
+    "kvarn_q8_decode": ([_P, _I32, _I32, _F32, _P, _LP, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _P,
+                         _P, _I64, _P, _P], _I32),
     "kvarn_decode_noalloc": ([_P, _I32, _F32, _P, _LP, _P, _I32, _P, _I32, _P, _P, _I32, _P, _P, _P, _P],
                              _I32),
 }
@@ -439,17 +470,17 @@ def _addr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap, pages):
+def _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap, pages, page=0):
     """The checks of the decode calls' common tensors (q: [B, ..., Hq, D];
-    `pages` entries of a block table row may be read); returns the block
-    table's row stride."""
+    `pages` entries of a block table row may be read; pages of `page` bytes, 0:
+    the compressed layout's); returns the block table's row stride."""
     kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
     shape = q.shape
     B, Hkv, D = shape[0], layout.num_kv_heads, layout.head_dim
     if q.dtype is not kv_dtype or shape[-1] != D or not q.is_contiguous():
         _refuse(what, f"q must be contiguous {kv_dtype} with head_dim {D}, not {q.dtype} {tuple(shape)}")
     if (cache.dtype is not torch.uint8 or not cache.is_contiguous()
-            or cache.numel() < layout.num_pages * Hkv * page_bytes(layout)):
+            or cache.numel() < layout.num_pages * Hkv * (page or page_bytes(layout))):
         _refuse(what, "cache is not contiguous bytes of the layout's pages")
     bt_stride = _row_stride(what, "block_table", block_table, torch.int32, B)
     if block_table.shape[1] < pages:  # rows further apart than they are long: the C ABI sees the stride alone
@@ -577,6 +608,113 @@ def rope_backward(grads, grad_ins, positions, inv_freq, *, rope_offset=0, interl
     _rope("rope_backward", grads, grad_ins, positions, inv_freq, rope_offset, interleaved, scale, True, stream)
 
 
+_NORM_ROWS = [None] + [(NormRopeTensor * n, struct.Struct("@" + "PPPPPqqqqqqqqqii" * n)) for n in range(1, 5)]
+
+
+def _norm_rope(what, xs, dys, outs, weights, dweights, positions, inv_freq, workspace, eps, weight_offset, rope_offset,
+               interleaved, scale, stream):
+    if isinstance(xs, torch.Tensor):
+        xs, outs, weights = (xs,), (outs,), (weights,)
+        dys = None if dys is None else (dys,)
+        dweights = None if dweights is None else (dweights,)
+    n = len(xs)
+    weights = (None,) * n if weights is None else weights
+    dweights = (None,) * n if dweights is None else dweights
+    if not 1 <= n <= 4 or len(outs) != n or len(weights) != n or len(dweights) != n or (dys is not None and len(dys) != n):
+        _refuse(what, "one to four tensors, each with its output, weight and gradients")
+    x0 = xs[0]
+    dtype = x0.dtype
+    code = ROPE_DTYPES.get(dtype, -1)
+    if x0.dim() != 4 or code < 0:
+        _refuse(what, f"tensors must be float16, bfloat16 or float32 [seqs, tokens, heads, head_dim], not {dtype} "
+                      f"{tuple(x0.shape)}")
+    B, S, _, D = x0.shape
+    dev = _device_of(what, *xs, *outs, *weights, *dweights, *(dys or ()), positions, inv_freq, workspace)
+    wtype = next((w.dtype for w in weights if w is not None), torch.float32)
+    wcode = ROPE_DTYPES.get(wtype, -1)
+    rows = []
+    for x, y, dy, w, dw in zip(xs, outs, dys or (None,) * n, weights, dweights):
+        shape, strides, ostrides = x.shape, x.stride(), y.stride()
+        if len(shape) != 4 or y.shape != shape or x.dtype is not dtype or y.dtype is not dtype:
+            _refuse(what, "tensors must share their type, and each output its tensor's shape")
+        b, t, heads, dim = shape
+        if b != B or t != S or dim != D:
+            _refuse(what, "tensors must share sequences, tokens and head_dim")
+        if D > 1 and (strides[3] != 1 or ostrides[3] != 1):
+            _refuse(what, "the channels of a head must be contiguous")
+        yb, yt, yh, _ = ostrides
+        if (yb == 0 and B > 1) or (yt == 0 and S > 1) or (yh == 0 and heads > 1):
+            _refuse(what, "an output may not be broadcast")
+        gs = (0, 0, 0)
+        if dy is not None:
+            if dy.shape != shape or dy.dtype is not dtype:
+                _refuse(what, "each gradient must have its tensor's type and shape")
+            gs = dy.stride()
+            if D > 1 and gs[3] != 1:
+                _refuse(what, "the channels of a head must be contiguous")
+        if w is not None and (w.dtype is not wtype or wcode < 0 or w.shape != (D,) or not w.is_contiguous()):
+            _refuse(what, f"weights must be contiguous vectors of {D}, float16, bfloat16 or float32, of one type")
+        if dw is not None and (dw.dtype is not torch.float32 or dw.shape != (D,) or not dw.is_contiguous()):
+            _refuse(what, f"gradients of weights must be contiguous float32 vectors of {D}")
+        rows += (x.data_ptr(), _addr(dy), y.data_ptr(), _addr(w), _addr(dw), strides[0], strides[1], strides[2], gs[0], gs[1],
+                 gs[2], yb, yt, yh, heads, 0)
+    pos, pos_stride, freq, rope_dim = 0, 0, 0, 0
+    if inv_freq is not None:
+        shape = positions.shape
+        pb, ps = positions.stride() if positions.dim() == 2 else (0, 0)
+        if positions.dtype is not torch.int32 or not (shape == (B, S) or shape == (1, S)) or (ps != 1 and S > 1):
+            _refuse(what, "positions must be int32 [seqs or 1, tokens], rows contiguous")
+        if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            _refuse(what, "inv_freq must be a contiguous float64 vector")
+        pos, pos_stride, freq, rope_dim = positions.data_ptr(), pb if shape[0] > 1 else 0, inv_freq.data_ptr(), 2 * inv_freq.numel()
+    array, packer = _NORM_ROWS[n]
+    args = (array.from_buffer_copy(packer.pack(*rows)), n, D, code, wcode, B, S, pos, pos_stride, freq, rope_dim, rope_offset,
+            1 if interleaved else 0, scale, eps, weight_offset)
+    if dys is None:
+        _check(lib().kvarn_norm_rope(*args, _raw_stream(what, stream, dev)), what)
+        return
+    if workspace is not None and not workspace.is_contiguous():
+        _refuse(what, "workspace must be contiguous")
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().kvarn_norm_rope_backward(*args, _addr(workspace), size, _raw_stream(what, stream, dev)), what)
+
+
+def norm_rope(xs, outs, weights, positions, inv_freq, *, eps=1e-6, weight_offset=0.0, rope_offset=0, interleaved=False,
+              scale=1.0, stream=None):
+    """The norm of every head of one to four tensors (queries and keys) and
+    its rotary position in one launch: x / sqrt(mean(x^2) + eps) * (weight +
+    weight_offset), turned as by rope. xs: [B, S, heads, D] (any strides,
+    contiguous heads; fp16, bf16 or fp32), outs the same shapes (outs = xs
+    works in place); weights [D] or None (ones), of one type; inv_freq None:
+    no rotation."""
+    _norm_rope("norm_rope", xs, None, outs, weights, None, positions, inv_freq, None, eps, weight_offset, rope_offset,
+               interleaved, scale, stream)
+
+
+def norm_rope_backward_workspace_bytes(xs) -> int:
+    """Workspace of norm_rope_backward for these tensors (or one)."""
+    xs = (xs,) if isinstance(xs, torch.Tensor) else xs
+    n = -1
+    if 1 <= len(xs) <= 4 and xs[0].dim() == 4:
+        heads = (ctypes.c_int32 * len(xs))(*[x.shape[2] for x in xs])
+        B, S, _, D = xs[0].shape
+        n = lib().kvarn_norm_rope_backward_workspace_bytes(heads, len(xs), D, B, S)
+    if n < 0:
+        raise KvarnError("invalid arguments for kvarn_norm_rope_backward_workspace_bytes")
+    return n
+
+
+def norm_rope_backward(xs, grads, grad_ins, weights, grad_weights, positions, inv_freq, workspace, *, eps=1e-6,
+                       weight_offset=0.0, rope_offset=0, interleaved=False, scale=1.0, stream=None):
+    """The gradient of norm_rope: grads with respect to its outputs, grad_ins
+    with respect to xs (may be grads or xs), grad_weights float32 [D] each, or
+    None where it is not wanted (no workspace is needed without any)."""
+    if grads is None:
+        _refuse("norm_rope_backward", "grads are missing")
+    _norm_rope("norm_rope_backward", xs, grads, grad_ins, weights, grad_weights, positions, inv_freq, workspace, eps,
+               weight_offset, rope_offset, interleaved, scale, stream)
+
+
 def decode_mass_workspace_bytes(layout: Layout, num_seqs: int, num_q_heads: int, max_seq_len: int) -> int:
     n = lib().kvarn_decode_mass_workspace_bytes(ctypes.byref(layout), num_seqs, num_q_heads, max_seq_len)
     if n < 0:
@@ -675,6 +813,228 @@ def decode_shared(q, layout: Layout, cache, prefix_table, prefix_tokens, block_t
                                      prefix_table.data_ptr(), prefix_tokens, block_table.data_ptr(), bt_stride,
                                      seq_lens.data_ptr(), max_seq_len, _addr(tail_k), _addr(tail_v), cap, B,
                                      out.data_ptr(), _addr(lse), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), err.data_ptr(),
+                                     _raw_stream(what, stream, dev)), what)
+
+
+# ------------------------------------------------------ 8-bit block cache
+# Codes of 8 bits with one scale per block (the 16 tokens of a page) and head,
+# attended over with a sliding window and sinks.
+
+Q8_E4M3, Q8_INT8 = 0, 1
+
+
+def q8_layout(head_dim, num_kv_heads, num_pages, kv_dtype=FP16) -> Layout:
+    """head_dim 128 or 256; blocks of 16 tokens, one page each."""
+    return Layout(head_dim, 16, 16, num_kv_heads, 8, 8, 1, 0, kv_dtype, 0, num_pages)
+
+
+def q8_page_bytes(layout: Layout) -> int:
+    n = lib().kvarn_q8_page_bytes(ctypes.byref(layout))
+    if n < 0:
+        raise KvarnError("invalid 8-bit layout")
+    return n
+
+
+def alloc_q8_cache(layout: Layout, device=None) -> torch.Tensor:
+    return torch.zeros((layout.num_pages, layout.num_kv_heads, q8_page_bytes(layout)), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def _err_word(what, err):
+    if err.dtype is not torch.int32 or err.numel() != 1:
+        _refuse(what, "err must be one int32")
+
+
+def _cache_bytes(what, cache, layout, page):
+    if (cache.dtype is not torch.uint8 or not cache.is_contiguous()
+            or cache.numel() < layout.num_pages * layout.num_kv_heads * page):
+        _refuse(what, "cache is not contiguous bytes of the layout's pages")
+
+
+def _int_vector(what, name, t, n):
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        _refuse(what, f"{name} must be a contiguous int32 vector of {n}")
+
+
+def _q8_blocks(what, call, k, v, layout, code, block_start, block_table, cache, err, stream):
+    kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
+    if k.dim() != 4 or k.shape != v.shape or k.dtype is not kv_dtype or v.dtype is not kv_dtype:
+        _refuse(what, f"k and v must be {kv_dtype} [seqs, kv heads, tokens, head_dim] of one shape")
+    B, H, C, D = k.shape
+    if H != layout.num_kv_heads or D != layout.head_dim:
+        _refuse(what, f"k and v must have {layout.num_kv_heads} heads of {layout.head_dim}, not {tuple(k.shape)}")
+    sb, sh, st, se = (s if n > 1 else 0 for n, s in zip(k.shape, k.stride()))
+    if tuple(s if n > 1 else 0 for n, s in zip(v.shape, v.stride())) != (sb, sh, st, se) or se != 1:
+        _refuse(what, "k and v must have the same strides and contiguous channels")
+    if call is lib().kvarn_q8_read_blocks and 0 in ((1 if n <= 1 else s) for n, s in zip(k.shape, (sb, sh, st, se))):
+        _refuse(what, "an output may not be broadcast")
+    dev = _device_of(what, k, v, block_start, block_table, cache, err)
+    _cache_bytes(what, cache, layout, q8_page_bytes(layout))
+    bt_stride = _row_stride(what, "block_table", block_table, torch.int32, B)
+    if block_table.shape[1] != bt_stride:  # entries between the rows are nobody's
+        _refuse(what, "the rows of block_table must be contiguous to each other")
+    _int_vector(what, "block_start", block_start, B)
+    _err_word(what, err)
+    _check(call(k.data_ptr(), v.data_ptr(), sb, sh, st, B, C, block_start.data_ptr(), block_table.data_ptr(), bt_stride,
+                ctypes.byref(layout), code, cache.data_ptr(), err.data_ptr(), _raw_stream(what, stream, dev)), what)
+
+
+def q8_encode_blocks(k, v, layout: Layout, code, block_start, block_table, cache, err, stream=None):
+    """Tokens of k, v ([B, Hkv, C, D], any strides with contiguous channels, C
+    whole blocks) into logical blocks block_start[b].. (int32 [B]; negative:
+    skip the sequence)."""
+    _q8_blocks("q8_encode_blocks", lib().kvarn_q8_encode_blocks, k, v, layout, code, block_start, block_table, cache, err,
+               stream)
+
+
+def q8_read_blocks(k, v, layout: Layout, code, block_start, block_table, cache, err, stream=None):
+    """The values of the same blocks, written to k and v."""
+    _q8_blocks("q8_read_blocks", lib().kvarn_q8_read_blocks, k, v, layout, code, block_start, block_table, cache, err,
+               stream)
+
+
+def q8_append(k, v, layout: Layout, code, seq_lens, max_seq_len, tail_k, tail_v, block_table, cache, err, stream=None):
+    """k, v: [B, Hkv, D] newest tokens (seq_lens counts them); tail_k/v:
+    [B, Hkv, capacity, D], capacity at least 15."""
+    what = "q8_append"
+    kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
+    B, H, D = seq_lens.shape[0], layout.num_kv_heads, layout.head_dim
+    for t in (k, v):
+        if t.dtype is not kv_dtype or t.shape != (B, H, D) or not t.is_contiguous():
+            _refuse(what, f"k and v must be contiguous {kv_dtype} of shape {(B, H, D)}")
+    cap = tail_k.shape[2] if tail_k.dim() == 4 else 0
+    for t in (tail_k, tail_v):
+        if t.dtype is not kv_dtype or t.shape != (B, H, cap, D) or not t.is_contiguous():
+            _refuse(what, f"tail_k and tail_v must be contiguous {kv_dtype} of shape {(B, H, 'capacity', D)}")
+    dev = _device_of(what, k, v, seq_lens, tail_k, tail_v, block_table, cache, err)
+    _cache_bytes(what, cache, layout, q8_page_bytes(layout))
+    bt_stride = _row_stride(what, "block_table", block_table, torch.int32, B)
+    if block_table.shape[1] < max_seq_len // 16:
+        _refuse(what, "block_table has fewer columns than max_seq_len has blocks")
+    _int_vector(what, "seq_lens", seq_lens, B)
+    _err_word(what, err)
+    _check(lib().kvarn_q8_append(k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), max_seq_len, tail_k.data_ptr(),
+                                 tail_v.data_ptr(), cap, B, block_table.data_ptr(), bt_stride, ctypes.byref(layout), code,
+                                 cache.data_ptr(), err.data_ptr(), _raw_stream(what, stream, dev)), what)
+
+
+def q8_decode_workspace_bytes(layout: Layout, num_seqs: int, num_q_heads: int, num_queries: int, max_seq_len: int,
+                              window: int = 0, sink_tokens: int = 0) -> int:
+    n = lib().kvarn_q8_decode_workspace_bytes(ctypes.byref(layout), num_seqs, num_q_heads, num_queries, max_seq_len, window,
+                                              sink_tokens)
+    if n < 0:
+        raise KvarnError("invalid arguments for kvarn_q8_decode_workspace_bytes")
+    return n
+
+
+def q8_decode(q, layout: Layout, code, cache, block_table, seq_lens, max_seq_len, out, workspace, err, sm_scale,
+              tail_k=None, tail_v=None, lse=None, window=0, sink_tokens=0, stream=None):
+    """Decode or verification over the 8-bit block cache. q: [B, Q, Hq, D];
+    tail_k/v: [B, Hkv, capacity, D], capacity at least Q + 14; out: [B, Q, Hq,
+    D]. Query j, at position p = seq_lens - Q + j, sees tokens i <= p with
+    i < sink_tokens or i > p - window (window = 0: all)."""
+    what = "q8_decode"
+    if q.dim() != 4:
+        _refuse(what, "q must be [seqs, queries, heads, head_dim]")
+    B, Q, Hq, _ = q.shape
+    cap = tail_k.shape[2] if tail_k is not None and tail_k.dim() == 4 else Q + 14
+    dev = _device_of(what, q, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse)
+    bt_stride = _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap,
+                                max(0, max_seq_len - Q + 1) // 16, q8_page_bytes(layout))
+    _check(lib().kvarn_q8_decode(q.data_ptr(), Hq, Q, sm_scale, cache.data_ptr(), ctypes.byref(layout), code,
+                                 block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), max_seq_len, _addr(tail_k),
+                                 _addr(tail_v), cap, window, sink_tokens, B, out.data_ptr(), _addr(lse),
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), err.data_ptr(),
+                                 _raw_stream(what, stream, dev)), what)
+
+
+# ------------------------------------------------------ pages of a cache
+# Sequences that fork, end and leave their windows; compaction.
+
+def fork_sequences(parents, seq_lens, block_table, page_refs, layout: Layout, max_seq_len, seq_lens_out, block_table_out,
+                   page_refs_out, freed, freed_count, err, *, tails=(), sinks=(), recent_tokens=0, window=0, sink_tokens=0,
+                   stream=None):
+    """A batch's next rows: row b continues row parents[b] (negative: an empty
+    row). Rows that fork share pages, counted in page_refs (int32
+    [num_pages]); freed lists the pages whose count fell to 0, ascending, then
+    -1, freed_count[0] of them. tails: up to four (old, new) pairs of raw tail
+    buffers [rows, heads, capacity, channels], of which the rows in use are
+    copied; sinks: pairs that are copied whole. window: entries of tiles that
+    the next token and the first sink_tokens tokens do not need become -1 and
+    their references are given back. page_refs_out may be page_refs."""
+    what = "fork_sequences"
+    n_in, n_out = seq_lens.shape[0], parents.shape[0]
+    pairs = [(*p, 0) for p in tails] + [(*p, 1) for p in sinks]
+    if len(pairs) > 4:
+        _refuse(what, "at most four tails and sinks")
+    dev = _device_of(what, parents, seq_lens, block_table, page_refs, seq_lens_out, block_table_out, page_refs_out, freed,
+                     freed_count, err, *(t for p in pairs for t in p[:2]))
+    entries = max_seq_len // layout.tile_tokens * (layout.tile_tokens // 16)
+    rows = _row_stride(what, "block_table", block_table, torch.int32, n_in)
+    out_rows = _row_stride(what, "block_table_out", block_table_out, torch.int32, n_out)
+    if block_table.shape[1] < entries or block_table_out.shape[1] < entries:
+        _refuse(what, "a block table has fewer columns than max_seq_len has pages")
+    if n_in > 1 and n_out > 1 and rows != out_rows:
+        _refuse(what, "block_table and block_table_out differ in row stride")
+    for name, t, n in (("parents", parents, n_out), ("seq_lens", seq_lens, n_in), ("seq_lens_out", seq_lens_out, n_out),
+                       ("page_refs", page_refs, layout.num_pages), ("page_refs_out", page_refs_out, layout.num_pages),
+                       ("freed", freed, layout.num_pages), ("freed_count", freed_count, 1)):
+        _int_vector(what, name, t, n)
+    _err_word(what, err)
+    array = (ForkTail * max(1, len(pairs)))()
+    for k, (old, new, whole) in enumerate(pairs):
+        if (old.dim() != 4 or new.dim() != 4 or old.dtype is not new.dtype or old.shape[1:] != new.shape[1:]
+                or old.shape[0] != n_in or new.shape[0] != n_out or not old.is_contiguous() or not new.is_contiguous()):
+            _refuse(what, "tails must be contiguous [rows, heads, capacity, channels], old and new of one type and shape")
+        array[k] = ForkTail(old.data_ptr(), new.data_ptr(), old.shape[3] * old.element_size(), old.shape[1], old.shape[2],
+                            whole, 0)
+    _check(lib().kvarn_fork_sequences(parents.data_ptr(), n_in, n_out, seq_lens.data_ptr(), seq_lens_out.data_ptr(),
+                                      max_seq_len, block_table.data_ptr(), block_table_out.data_ptr(),
+                                      rows if n_in > 1 else out_rows if n_out > 1 else entries, page_refs.data_ptr(),
+                                      page_refs_out.data_ptr(), freed.data_ptr(), freed_count.data_ptr(), array, len(pairs),
+                                      ctypes.byref(layout), recent_tokens, window, sink_tokens, err.data_ptr(),
+                                      _raw_stream(what, stream, dev)), what)
+
+
+def compact_pages_workspace_bytes(num_pages: int) -> int:
+    n = lib().kvarn_compact_workspace_bytes(num_pages)
+    if n < 0:
+        raise KvarnError("invalid number of pages for kvarn_compact_workspace_bytes")
+    return n
+
+
+def compact_pages(cache, page_refs, block_table, page_refs_out, block_table_out, remap, live_count, workspace, err, *,
+                  stream=None):
+    """Move the pages in use (page_refs > 0) of a cache (uint8 [num_pages,
+    ...], as the alloc functions make it) to ids 0 .. live_count[0] - 1.
+    block_table: int32 [rows, entries], all of whose entries are renumbered
+    into block_table_out, or None for both; remap: the new id of every page,
+    -1 of a free one. page_refs_out and block_table_out may be page_refs and
+    block_table."""
+    what = "compact_pages"
+    dev = _device_of(what, cache, page_refs, block_table, page_refs_out, block_table_out, remap, live_count, workspace, err)
+    if cache.dtype is not torch.uint8 or cache.dim() < 2 or not cache.is_contiguous():
+        _refuse(what, "cache must be contiguous bytes [num_pages, ...]")
+    n = cache.shape[0]
+    for name, t, m in (("page_refs", page_refs, n), ("page_refs_out", page_refs_out, n), ("remap", remap, n),
+                       ("live_count", live_count, 1)):
+        _int_vector(what, name, t, m)
+    rows, entries, stride = 0, 0, 0
+    if block_table is not None or block_table_out is not None:
+        if block_table is None or block_table_out is None or block_table.dim() != 2:
+            _refuse(what, "block_table and block_table_out must be int32 matrices, or both None")
+        rows, entries = block_table.shape
+        stride = _row_stride(what, "block_table", block_table, torch.int32, rows)
+        if _row_stride(what, "block_table_out", block_table_out, torch.int32, rows) != stride or \
+                block_table_out.shape != block_table.shape:
+            _refuse(what, "block_table_out differs from block_table in shape or stride")
+    if not workspace.is_contiguous():
+        _refuse(what, "workspace must be contiguous")
+    _err_word(what, err)
+    _check(lib().kvarn_compact_pages(cache.data_ptr(), cache.numel() // n if n else 16, n, page_refs.data_ptr(),
+                                     page_refs_out.data_ptr(), _addr(block_table), _addr(block_table_out), rows, entries,
+                                     stride, remap.data_ptr(), live_count.data_ptr(), workspace.data_ptr(),
                                      workspace.numel() * workspace.element_size(), err.data_ptr(),
                                      _raw_stream(what, stream, dev)), what)
 

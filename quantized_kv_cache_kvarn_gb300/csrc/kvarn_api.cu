@@ -57,6 +57,23 @@ int32_t check_affine(const kvarn_layout* L) {
   return KVARN_OK;
 }
 
+// Layout of the 8-bit block cache: blocks of one page.
+int32_t check_q8(const kvarn_layout* L) {
+  if (!L) return KVARN_EINVAL;
+  if (L->page_tokens != kPageTokens || L->tile_tokens != kPageTokens || L->k_bits != 8 || L->v_bits != 8 ||
+      (L->head_dim != 128 && L->head_dim != 256) || L->rope_dim != 0)
+    return KVARN_EUNSUPPORTED;
+  if (L->kv_dtype != 0 && L->kv_dtype != 1) return KVARN_EUNSUPPORTED;
+  if (L->num_kv_heads < 1 || L->num_pages < 0) return KVARN_EINVAL;
+  return KVARN_OK;
+}
+
+int32_t check_q8(const kvarn_layout* L, int32_t code) {
+  const int32_t s = check_q8(L);
+  if (s != KVARN_OK) return s;
+  return code == KVARN_Q8_E4M3 || code == KVARN_Q8_INT8 ? KVARN_OK : KVARN_EUNSUPPORTED;
+}
+
 }  // namespace
 
 extern "C" {
@@ -803,6 +820,405 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
   p.scale = scale;
   p.inverse = inverse;
   return from_cuda(launch_rope(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int32_t kvarn_fork_sequences(const int32_t* parents, int32_t num_in, int32_t num_out, const int32_t* seq_lens,
+                             int32_t* seq_lens_out, int32_t max_seq_len, const int32_t* block_table,
+                             int32_t* block_table_out, int32_t bt_stride, const int32_t* page_refs,
+                             int32_t* page_refs_out, int32_t* freed, int32_t* freed_count,
+                             const kvarn_fork_tail* tails, int32_t num_tails, const kvarn_layout* L,
+                             int32_t recent_tokens, int32_t window, int32_t sink_tokens, uint32_t* error_flags,
+                             kvarn_stream_t stream) {
+  if (!L) return KVARN_EINVAL;
+  if (L->page_tokens != kPageTokens || L->tile_tokens < kPageTokens || L->tile_tokens % kPageTokens ||
+      L->tile_tokens > 1024)
+    return KVARN_EUNSUPPORTED;
+  if (num_in < 0 || num_out < 0 || max_seq_len < 0 || num_tails < 0 || recent_tokens < 0 || window < 0 ||
+      sink_tokens < 0 || L->num_pages < 0)
+    return KVARN_EINVAL;
+  if (num_in > kForkMaxRows || num_out > kForkMaxRows || num_tails > kForkMaxTails || L->num_pages > kForkMaxPages)
+    return KVARN_EUNSUPPORTED;
+  const int32_t entries = max_seq_len / L->tile_tokens * (L->tile_tokens / kPageTokens);
+  if ((num_out > 0 && (!parents || !seq_lens_out)) || (num_in > 0 && !seq_lens) || !freed_count || !error_flags)
+    return KVARN_EINVAL;
+  if (entries > 0 && ((num_in > 0 && !block_table) || (num_out > 0 && !block_table_out) || bt_stride < entries))
+    return KVARN_EINVAL;
+  if (L->num_pages > 0 && (!page_refs || !page_refs_out || !freed)) return KVARN_EINVAL;
+  const void* ints[] = {parents,   seq_lens, seq_lens_out, block_table, block_table_out, page_refs, page_refs_out,
+                        freed,     freed_count, error_flags};
+  for (const void* p : ints)
+    if (!aligned(p, 4)) return KVARN_EALIGN;
+  // outputs are buffers of their own
+  const void* outs[] = {seq_lens_out, block_table_out, freed, freed_count, error_flags};
+  for (const void* o : outs) {
+    int n = 0;
+    for (const void* p : ints) n += o && p == o;
+    if (n > 1) return KVARN_EINVAL;
+  }
+  if (page_refs_out && (page_refs_out == parents || page_refs_out == seq_lens || page_refs_out == block_table))
+    return KVARN_EINVAL;
+  ForkParams p{};
+  for (int32_t k = 0; k < num_tails; ++k) {
+    if (!tails) return KVARN_EINVAL;
+    const kvarn_fork_tail& t = tails[k];
+    if (t.num_heads < 0 || t.capacity < 0 || t.row_bytes < 0 || (t.whole != 0 && t.whole != 1)) return KVARN_EINVAL;
+    if (t.num_heads > (1 << 20) || t.row_bytes > (1 << 20)) return KVARN_EUNSUPPORTED;
+    if (t.num_heads == 0 || t.capacity == 0 || t.row_bytes == 0) continue;
+    if ((!t.in && num_in > 0) || (!t.out && num_out > 0) || (t.in && t.in == t.out)) return KVARN_EINVAL;
+    if (t.row_bytes % 16 || !aligned(t.in, 16) || !aligned(t.out, 16)) return KVARN_EALIGN;
+    for (int32_t j = 0; j < p.num_rows; ++j)
+      if ((t.out && (t.out == p.rows[j].out || t.out == p.rows[j].in)) || (t.in && t.in == p.rows[j].out)) return KVARN_EINVAL;
+    p.rows[p.num_rows++] = {t.in, t.out, t.num_heads, t.capacity, t.row_bytes, t.whole, 0};
+  }
+  p.parents = parents;
+  p.num_in = num_in;
+  p.num_out = num_out;
+  p.seq_lens = seq_lens;
+  p.lens_out = seq_lens_out;
+  p.max_seq_len = max_seq_len;
+  p.table = block_table;
+  p.table_out = block_table_out;
+  p.bt_stride = bt_stride;
+  p.entries = entries;
+  p.refs = page_refs;
+  p.refs_out = page_refs_out;
+  p.num_pages = static_cast<int32_t>(L->num_pages);
+  p.freed = freed;
+  p.freed_count = freed_count;
+  p.N = L->tile_tokens;
+  p.pages_per_tile = L->tile_tokens / kPageTokens;
+  p.recent = recent_tokens;
+  p.window = window;
+  p.sinks = sink_tokens;
+  p.err = error_flags;
+  return from_cuda(launch_fork(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t kvarn_compact_workspace_bytes(int64_t num_pages) {
+  return num_pages < 0 || num_pages > (1 << 30) ? -1 : compact_workspace_bytes(num_pages);
+}
+
+int32_t kvarn_compact_pages(void* cache, int64_t page_stride, int64_t num_pages, const int32_t* page_refs,
+                            int32_t* page_refs_out, const int32_t* block_table, int32_t* block_table_out,
+                            int32_t num_rows, int32_t entries, int32_t bt_stride, int32_t* remap,
+                            int32_t* live_count, void* workspace, int64_t workspace_bytes, uint32_t* error_flags,
+                            kvarn_stream_t stream) {
+  if (num_pages < 0 || page_stride < 1 || num_rows < 0 || entries < 0) return KVARN_EINVAL;
+  if (num_pages > (1 << 30) || page_stride > (1LL << 30)) return KVARN_EUNSUPPORTED;
+  if (!live_count || !workspace || !error_flags) return KVARN_EINVAL;
+  if (num_pages > 0 && (!cache || !page_refs || !page_refs_out || !remap)) return KVARN_EINVAL;
+  const bool tables = num_rows > 0 && entries > 0;
+  if (tables && (!block_table || !block_table_out || (num_rows > 1 && bt_stride < entries))) return KVARN_EINVAL;
+  if (!aligned(cache, 16) || page_stride % 16 || !aligned(workspace, 16)) return KVARN_EALIGN;
+  const void* ints[] = {page_refs, page_refs_out, block_table, block_table_out, remap, live_count, error_flags};
+  for (const void* p : ints)
+    if (!aligned(p, 4)) return KVARN_EALIGN;
+  for (const void* o : {static_cast<const void*>(remap), static_cast<const void*>(live_count)}) {
+    int n = 0;
+    for (const void* p : ints) n += o && p == o;
+    if (n > 1) return KVARN_EINVAL;
+  }
+  if (tables && (block_table_out == page_refs || block_table_out == page_refs_out || page_refs_out == block_table))
+    return KVARN_EINVAL;
+  if (workspace_bytes < compact_workspace_bytes(num_pages)) return KVARN_EWORKSPACE;
+  CompactParams p{};
+  p.cache = static_cast<uint8_t*>(cache);
+  p.page_bytes = page_stride;
+  p.num_pages = static_cast<int32_t>(num_pages);
+  p.refs = page_refs;
+  p.refs_out = page_refs_out;
+  p.table = block_table;
+  p.table_out = block_table_out;
+  p.rows = tables ? num_rows : 0;
+  p.entries = tables ? entries : 1;
+  p.bt_stride = bt_stride;
+  p.remap = remap;
+  p.live = live_count;
+  p.err = error_flags;
+  return from_cuda(launch_compact(p, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static bool norm_sizes_ok(int32_t num_tensors, int32_t head_dim, int32_t num_seqs, int32_t num_tokens) {
+  return num_tensors >= 1 && num_tensors <= KVARN_ROPE_MAX_TENSORS && head_dim >= 1 && num_seqs >= 0 && num_tokens >= 0;
+}
+
+int64_t kvarn_norm_rope_backward_workspace_bytes(const int32_t* num_heads, int32_t num_tensors, int32_t head_dim,
+                                                 int32_t num_seqs, int32_t num_tokens) {
+  if (!num_heads || !norm_sizes_ok(num_tensors, head_dim, num_seqs, num_tokens) || head_dim > KVARN_ROPE_MAX_DIM ||
+      static_cast<int64_t>(num_seqs) * num_tokens > (1 << 30))
+    return -1;
+  int64_t heads = 0;
+  for (int32_t k = 0; k < num_tensors; ++k) {
+    if (num_heads[k] < 0) return -1;
+    heads += num_heads[k];
+  }
+  if (heads > (1 << 20)) return -1;
+  return norm_rope_workspace_bytes(num_tensors, num_heads, head_dim, static_cast<int64_t>(num_seqs) * num_tokens);
+}
+
+static int32_t norm_rope(const kvarn_norm_rope_tensor* tensors, int32_t num_tensors, int32_t head_dim, int32_t dtype,
+                         int32_t weight_dtype, int32_t num_seqs, int32_t num_tokens, const int32_t* positions,
+                         int64_t pos_stride, const double* inv_freq, int32_t rope_dim, int32_t rope_offset,
+                         int32_t interleaved, float scale, float eps, float weight_offset, bool backward,
+                         void* workspace, int64_t workspace_bytes, kvarn_stream_t stream) {
+  if (!tensors || !norm_sizes_ok(num_tensors, head_dim, num_seqs, num_tokens)) return KVARN_EINVAL;
+  if (dtype < 0 || dtype > 2 || weight_dtype < 0 || weight_dtype > 2) return KVARN_EUNSUPPORTED;
+  if (rope_dim < 0 || rope_dim % 2 || rope_offset < 0 || pos_stride < 0 || (interleaved != 0 && interleaved != 1) ||
+      !(eps >= 0.f) || static_cast<int64_t>(rope_offset) + rope_dim > head_dim)
+    return KVARN_EINVAL;
+  if (head_dim > KVARN_ROPE_MAX_DIM) return KVARN_EUNSUPPORTED;
+  const uintptr_t size = dtype == 2 ? 4 : 2, wsize = weight_dtype == 2 ? 4 : 2;
+  NormParams p{};
+  int64_t heads = 0;
+  int32_t every[KVARN_ROPE_MAX_TENSORS];
+  bool sums = false;
+  for (int32_t k = 0; k < num_tensors; ++k) {
+    if (tensors[k].num_heads < 0) return KVARN_EINVAL;
+    every[k] = tensors[k].num_heads;
+    heads += tensors[k].num_heads;
+    sums = sums || (backward && tensors[k].dweight);
+  }
+  const int64_t tokens = static_cast<int64_t>(num_seqs) * num_tokens;
+  if (heads > (1 << 20) || tokens > (1 << 30)) return KVARN_EUNSUPPORTED;
+  // the gradient of the weights over no tokens or heads is still written
+  if ((tokens == 0 || heads == 0) && !sums) return KVARN_OK;
+  if (rope_dim > 0 && tokens > 0 && (!positions || !inv_freq)) return KVARN_EINVAL;
+  if (!aligned(positions, 4) || !aligned(inv_freq, 8)) return KVARN_EALIGN;
+  for (int32_t k = 0; k < num_tensors; ++k) {
+    kvarn_norm_rope_tensor t = tensors[k];
+    if (!backward) t.dweight = nullptr, t.dy = nullptr;
+    if (!aligned(t.weight, wsize) || !aligned(t.dweight, 4)) return KVARN_EALIGN;
+    if (t.num_heads == 0 || tokens == 0) {
+      t.num_heads = 0;
+    } else {
+      // the stride of an axis of length one says nothing
+      if (num_seqs == 1) t.x_seq_stride = t.dy_seq_stride = t.out_seq_stride = 0;
+      if (num_tokens == 1) t.x_token_stride = t.dy_token_stride = t.out_token_stride = 0;
+      if (t.num_heads == 1) t.x_head_stride = t.dy_head_stride = t.out_head_stride = 0;
+      if (!backward) t.dy_seq_stride = t.dy_token_stride = t.dy_head_stride = 0;
+      if (!t.x || !t.out || (backward && !t.dy)) return KVARN_EINVAL;
+      if (!aligned(t.x, size) || !aligned(t.dy, size) || !aligned(t.out, size)) return KVARN_EALIGN;
+      // in place: every element is written where it was read
+      if (t.x == t.out && (t.x_seq_stride != t.out_seq_stride || t.x_token_stride != t.out_token_stride ||
+                           t.x_head_stride != t.out_head_stride))
+        return KVARN_EINVAL;
+      if (backward && t.dy == t.out && (t.dy_seq_stride != t.out_seq_stride || t.dy_token_stride != t.out_token_stride ||
+                                        t.dy_head_stride != t.out_head_stride))
+        return KVARN_EINVAL;
+    }
+    if ((t.dweight && (t.dweight == t.weight || t.dweight == t.out)) || (t.weight && t.weight == t.out)) return KVARN_EINVAL;
+    // a tensor is written while the others are read and written
+    for (int32_t j = 0; j < p.num_tensors; ++j) {
+      const NormTensor& o = p.t[j];
+      if (t.num_heads && o.heads && (t.out == o.out || t.out == o.x || t.x == o.out)) return KVARN_EINVAL;
+      if (t.num_heads && o.heads && backward && (t.out == o.dy || t.dy == o.out)) return KVARN_EINVAL;
+      if (t.dweight && (t.dweight == o.dw || t.dweight == o.w)) return KVARN_EINVAL;
+      if (o.dw && o.dw == t.weight) return KVARN_EINVAL;
+    }
+    p.t[p.num_tensors++] = {t.x,           t.dy,            t.out,          t.weight,        t.dweight,
+                            t.x_seq_stride, t.x_token_stride, t.x_head_stride, t.dy_seq_stride, t.dy_token_stride,
+                            t.dy_head_stride, t.out_seq_stride, t.out_token_stride, t.out_head_stride, t.num_heads};
+  }
+  if (sums) {
+    if (!workspace && tokens > 0 && heads > 0) return KVARN_EINVAL;
+    if (!aligned(workspace, 16)) return KVARN_EALIGN;
+    if (workspace_bytes < norm_rope_workspace_bytes(num_tensors, every, head_dim, tokens)) return KVARN_EWORKSPACE;
+  }
+  p.dim = head_dim;
+  p.dtype = dtype;
+  p.wdtype = weight_dtype;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.positions = positions;
+  p.pos_stride = pos_stride;
+  p.inv_freq = inv_freq;
+  p.rope_dim = rope_dim;
+  p.offset = rope_offset;
+  p.interleaved = interleaved;
+  p.scale = scale;
+  p.eps = eps;
+  p.weight_offset = weight_offset;
+  p.backward = backward;
+  p.parts = static_cast<float*>(workspace);
+  return from_cuda(launch_norm_rope(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int32_t kvarn_norm_rope(const kvarn_norm_rope_tensor* tensors, int32_t num_tensors, int32_t head_dim, int32_t dtype,
+                        int32_t weight_dtype, int32_t num_seqs, int32_t num_tokens, const int32_t* positions,
+                        int64_t pos_stride, const double* inv_freq, int32_t rope_dim, int32_t rope_offset,
+                        int32_t interleaved, float scale, float eps, float weight_offset, kvarn_stream_t stream) {
+  return norm_rope(tensors, num_tensors, head_dim, dtype, weight_dtype, num_seqs, num_tokens, positions, pos_stride,
+                   inv_freq, rope_dim, rope_offset, interleaved, scale, eps, weight_offset, false, nullptr, 0, stream);
+}
+
+int32_t kvarn_norm_rope_backward(const kvarn_norm_rope_tensor* tensors, int32_t num_tensors, int32_t head_dim,
+                                 int32_t dtype, int32_t weight_dtype, int32_t num_seqs, int32_t num_tokens,
+                                 const int32_t* positions, int64_t pos_stride, const double* inv_freq,
+                                 int32_t rope_dim, int32_t rope_offset, int32_t interleaved, float scale, float eps,
+                                 float weight_offset, void* workspace, int64_t workspace_bytes,
+                                 kvarn_stream_t stream) {
+  return norm_rope(tensors, num_tensors, head_dim, dtype, weight_dtype, num_seqs, num_tokens, positions, pos_stride,
+                   inv_freq, rope_dim, rope_offset, interleaved, scale, eps, weight_offset, true, workspace,
+                   workspace_bytes, stream);
+}
+
+int64_t kvarn_q8_page_bytes(const kvarn_layout* L) { return check_q8(L) == KVARN_OK ? 32 * L->head_dim + 32 : -1; }
+
+static Q8BlockParams q8_params(const kvarn_layout* L, int32_t code, const void* cache, uint32_t* error_flags) {
+  Q8BlockParams p{};
+  p.cache = const_cast<void*>(cache);
+  p.num_pages = L->num_pages;
+  p.num_kv_heads = L->num_kv_heads;
+  p.D = L->head_dim;
+  p.bf16 = L->kv_dtype == 1;
+  p.code = code;
+  p.err = error_flags;
+  return p;
+}
+
+static int32_t q8_blocks(const void* k, const void* v, int64_t seq_stride, int64_t head_stride, int64_t token_stride,
+                         int32_t num_seqs, int32_t chunk_tokens, const int32_t* block_start,
+                         const int32_t* block_table, int32_t bt_stride, const kvarn_layout* L, int32_t code,
+                         const void* cache, uint32_t* error_flags, kvarn_stream_t stream, bool read) {
+  const int32_t s = check_q8(L, code);
+  if (s != KVARN_OK) return s;
+  if (num_seqs < 0 || chunk_tokens < 0 || chunk_tokens % kPageTokens) return KVARN_EINVAL;
+  if (num_seqs == 0 || chunk_tokens == 0) return KVARN_OK;
+  if (!k || !v || !block_start || !block_table || !cache || !error_flags) return KVARN_EINVAL;
+  if (seq_stride < 0 || head_stride < 0 || token_stride < 0 || bt_stride < 1) return KVARN_EINVAL;
+  if (read && k == v) return KVARN_EINVAL;
+  if (!aligned(k, 16) || !aligned(v, 16) || seq_stride % 8 || head_stride % 8 || token_stride % 8) return KVARN_EALIGN;
+  if (!aligned(cache, 128) || !aligned(error_flags, 4) || !aligned(block_start, 4) || !aligned(block_table, 4))
+    return KVARN_EALIGN;
+  // two items a block and head, four to a CTA
+  if (static_cast<int64_t>(num_seqs) * L->num_kv_heads > (1LL << 31) / (chunk_tokens / kPageTokens))
+    return KVARN_EUNSUPPORTED;
+  Q8BlockParams p = q8_params(L, code, cache, error_flags);
+  p.k = k;
+  p.v = v;
+  p.seq_stride = seq_stride;
+  p.head_stride = head_stride;
+  p.token_stride = token_stride;
+  p.num_seqs = num_seqs;
+  p.blocks = chunk_tokens / kPageTokens;
+  p.block_start = block_start;
+  p.block_table = block_table;
+  p.bt_stride = bt_stride;
+  return from_cuda(launch_q8_blocks(p, read, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int32_t kvarn_q8_encode_blocks(const void* k, const void* v, int64_t seq_stride, int64_t head_stride,
+                               int64_t token_stride, int32_t num_seqs, int32_t chunk_tokens,
+                               const int32_t* block_start, const int32_t* block_table, int32_t bt_stride,
+                               const kvarn_layout* L, int32_t code, void* cache, uint32_t* error_flags,
+                               kvarn_stream_t stream) {
+  return q8_blocks(k, v, seq_stride, head_stride, token_stride, num_seqs, chunk_tokens, block_start, block_table,
+                   bt_stride, L, code, cache, error_flags, stream, false);
+}
+
+int32_t kvarn_q8_read_blocks(void* k, void* v, int64_t seq_stride, int64_t head_stride, int64_t token_stride,
+                             int32_t num_seqs, int32_t chunk_tokens, const int32_t* block_start,
+                             const int32_t* block_table, int32_t bt_stride, const kvarn_layout* L, int32_t code,
+                             const void* cache, uint32_t* error_flags, kvarn_stream_t stream) {
+  return q8_blocks(k, v, seq_stride, head_stride, token_stride, num_seqs, chunk_tokens, block_start, block_table,
+                   bt_stride, L, code, cache, error_flags, stream, true);
+}
+
+int32_t kvarn_q8_append(const void* k, const void* v, const int32_t* seq_lens, int32_t max_seq_len, void* tail_k,
+                        void* tail_v, int32_t tail_capacity, int32_t num_seqs, const int32_t* block_table,
+                        int32_t bt_stride, const kvarn_layout* L, int32_t code, void* cache, uint32_t* error_flags,
+                        kvarn_stream_t stream) {
+  const int32_t s = check_q8(L, code);
+  if (s != KVARN_OK) return s;
+  if (num_seqs < 0 || max_seq_len < 0) return KVARN_EINVAL;
+  if (num_seqs == 0) return KVARN_OK;
+  if (!k || !v || !seq_lens || !tail_k || !tail_v || !block_table || !cache || !error_flags || bt_stride < 1)
+    return KVARN_EINVAL;
+  if (tail_k == tail_v || tail_capacity < kPageTokens - 1 || bt_stride < max_seq_len / kPageTokens) return KVARN_EINVAL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(tail_k, 16) || !aligned(tail_v, 16)) return KVARN_EALIGN;
+  if (!aligned(cache, 128) || !aligned(error_flags, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4))
+    return KVARN_EALIGN;
+  if (static_cast<int64_t>(num_seqs) * L->num_kv_heads > (1LL << 31)) return KVARN_EUNSUPPORTED;
+  Q8BlockParams p = q8_params(L, code, cache, error_flags);
+  p.k = k;
+  p.v = v;
+  p.num_seqs = num_seqs;
+  p.seq_lens = seq_lens;
+  p.max_seq_len = max_seq_len;
+  p.tail_k = tail_k;
+  p.tail_v = tail_v;
+  p.tail_cap = tail_capacity;
+  p.block_table = block_table;
+  p.bt_stride = bt_stride;
+  return from_cuda(launch_q8_append(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static bool q8_decode_sizes_ok(const kvarn_layout* L, int32_t num_seqs, int32_t num_q_heads, int32_t num_queries,
+                               int32_t max_seq_len, int32_t window, int32_t sink_tokens) {
+  return num_seqs >= 0 && num_q_heads >= 1 && num_q_heads % L->num_kv_heads == 0 && num_queries >= 1 &&
+         num_queries <= KVARN_MAX_VERIFY_QUERIES && max_seq_len >= 0 && window >= 0 && sink_tokens >= 0;
+}
+
+int64_t kvarn_q8_decode_workspace_bytes(const kvarn_layout* L, int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t num_queries, int32_t max_seq_len, int32_t window,
+                                        int32_t sink_tokens) {
+  if (check_q8(L) != KVARN_OK ||
+      !q8_decode_sizes_ok(L, num_seqs, num_q_heads, num_queries, max_seq_len, window, sink_tokens))
+    return -1;
+  return q8_decode_workspace_bytes(num_seqs, num_q_heads / L->num_kv_heads * num_queries, L->head_dim);
+}
+
+int32_t kvarn_q8_decode(const void* q, int32_t num_q_heads, int32_t num_queries, float sm_scale, const void* cache,
+                        const kvarn_layout* L, int32_t code, const int32_t* block_table, int32_t bt_stride,
+                        const int32_t* seq_lens, int32_t max_seq_len, const void* tail_k, const void* tail_v,
+                        int32_t tail_capacity, int32_t window, int32_t sink_tokens, int32_t num_seqs, float* out,
+                        float* lse, void* workspace, int64_t workspace_bytes, uint32_t* error_flags,
+                        kvarn_stream_t stream) {
+  int32_t s = check_q8(L, code);
+  if (s != KVARN_OK) return s;
+  if (!q8_decode_sizes_ok(L, num_seqs, num_q_heads, num_queries, max_seq_len, window, sink_tokens))
+    return KVARN_EINVAL;
+  s = check_decode_common(L, num_q_heads, block_table, bt_stride, seq_lens, max_seq_len, num_seqs, out, workspace,
+                          error_flags);
+  if (s != KVARN_OK || num_seqs == 0) return s;
+  if (num_q_heads / L->num_kv_heads > 8 || static_cast<int64_t>(num_seqs) * num_queries * num_q_heads > (1 << 30))
+    return KVARN_EUNSUPPORTED;
+  if (!q || !cache || tail_capacity < num_queries + kPageTokens - 2) return KVARN_EINVAL;
+  const int32_t blocks = std::max(0, max_seq_len - num_queries + 1) / kPageTokens;
+  if (bt_stride < blocks || (blocks > 0 && L->num_pages < 1)) return KVARN_EINVAL;
+  if (!aligned(q, 16) || !aligned(cache, 128) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(lse, 4) || !aligned(error_flags, 4))
+    return KVARN_EALIGN;
+  if ((tail_k && !aligned(tail_k, 16)) || (tail_v && !aligned(tail_v, 16))) return KVARN_EALIGN;
+  if (workspace_bytes <
+      q8_decode_workspace_bytes(num_seqs, num_q_heads / L->num_kv_heads * num_queries, L->head_dim))
+    return KVARN_EWORKSPACE;
+  Q8DecodeParams p{};
+  p.q = q;
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.block_table = block_table;
+  p.bt_stride = bt_stride;
+  p.seq_lens = seq_lens;
+  p.max_seq_len = max_seq_len;
+  p.num_seqs = num_seqs;
+  p.num_queries = num_queries;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = L->num_kv_heads;
+  p.D = L->head_dim;
+  p.num_pages = L->num_pages;
+  p.tail_k = tail_k;
+  p.tail_v = tail_v;
+  p.tail_cap = tail_capacity;
+  p.window = window;
+  p.sinks = sink_tokens;
+  p.sm_scale = sm_scale;
+  p.bf16 = L->kv_dtype == 1;
+  p.code = code;
+  p.out = out;
+  p.lse = lse;
+  p.workspace = workspace;
+  p.err = error_flags;
+  return from_cuda(launch_q8_decode(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int32_t kvarn_set_copy_wait_test(int64_t cycles, int32_t withhold) {

@@ -22,6 +22,12 @@ void set_copy_wait_test(long long cycles, int withhold) {
   g_copy_withhold.store(withhold, std::memory_order_relaxed);
 }
 
+long long copy_wait_limit() {
+  const long long w = g_copy_wait_limit.load(std::memory_order_relaxed);
+  return w > 0 ? w : kDefaultCopyWait;
+}
+int copy_withhold() { return g_copy_withhold.load(std::memory_order_relaxed); }
+
 // ------------------------------------------------------------- planning
 int device_sm_count() {
   int dev = 0, n = 0;
@@ -249,11 +255,8 @@ cudaError_t dense_args(const DecodeParams& p, const DensePlan& plan, DecArgs& A)
   A.err = p.err;
   A.bf16 = p.bf16 ? 1 : 0;
   A.partial_tiles = p.codec == 2;
-  {
-    const long long w = g_copy_wait_limit.load(std::memory_order_relaxed);
-    A.wait_limit = w > 0 ? w : kDefaultCopyWait;
-    A.withhold = g_copy_withhold.load(std::memory_order_relaxed);
-  }
+  A.wait_limit = copy_wait_limit();
+  A.withhold = copy_withhold();
   return cudaSuccess;
 }
 

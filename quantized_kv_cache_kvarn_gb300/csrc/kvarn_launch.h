@@ -224,6 +224,32 @@ struct RopeParams {
 };
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t st);
 
+// Norms of queries and keys with their rotation (kvarn_norm_rope.cu).
+struct NormTensor {
+  const void* x;
+  const void* dy;   // gradient of the output (backward)
+  void* out;        // the output, or the gradient of x
+  const void* w;    // [dim] or null: ones
+  float* dw;        // gradient of w (backward; null: not wanted)
+  int64_t x_seq, x_tok, x_head, g_seq, g_tok, g_head, o_seq, o_tok, o_head;  // elements
+  int32_t heads;
+};
+struct NormParams {
+  NormTensor t[kRopeMaxTensors];
+  int32_t num_tensors;
+  int32_t dim, dtype, wdtype;  // 0 fp16, 1 bf16, 2 fp32
+  int32_t num_seqs, num_tokens;
+  const int32_t* positions;
+  int64_t pos_stride;
+  const double* inv_freq;
+  int32_t rope_dim, offset, interleaved;
+  float scale, eps, weight_offset;
+  int32_t backward;
+  float* parts;  // backward: sums of the CTAs
+};
+int64_t norm_rope_workspace_bytes(int32_t num_tensors, const int32_t* heads, int32_t dim, int64_t tokens);
+cudaError_t launch_norm_rope(const NormParams& p, cudaStream_t st);
+
 // Eviction of tiles (kvarn_evict.cu).
 struct EvictParams {
   const float* mass;
@@ -262,10 +288,114 @@ SplitPlan plan_mla(int32_t num_seqs, int32_t max_seq_len);
 int64_t mla_workspace_bytes(int32_t num_seqs, int32_t num_heads, const SplitPlan& plan);
 cudaError_t launch_decode_mla(const DecodeParams& p, const SplitPlan& plan, cudaStream_t st);
 
+// Pages of a cache (kvarn_pages.cu): sequences that fork, end and leave their
+// windows; compaction.
+constexpr int kForkMaxTails = 4, kForkMaxRows = 32768, kForkMaxPages = 1 << 23;
+struct ForkRows {
+  const void* in;  // [num_in][heads][capacity][row_bytes]
+  void* out;       // [num_out]...
+  int32_t heads, capacity;
+  int64_t row_bytes;
+  int32_t whole;   // all rows, not the live ones alone
+  int64_t pieces;  // set by the launch
+};
+struct ForkParams {
+  const int32_t* parents;
+  int32_t num_in, num_out;
+  const int32_t* seq_lens;
+  int32_t* lens_out;
+  int32_t max_seq_len;
+  const int32_t* table;
+  int32_t* table_out;
+  int32_t bt_stride, entries;  // entries: of max_seq_len's whole tiles
+  const int32_t* refs;
+  int32_t* refs_out;
+  int32_t num_pages;
+  int32_t* freed;
+  int32_t* freed_count;
+  int32_t N, pages_per_tile, recent, window, sinks;
+  ForkRows rows[kForkMaxTails];
+  int32_t num_rows;
+  int64_t tail_pieces;  // set by the launch
+  uint32_t* err;
+};
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t st);
+
+struct CompactParams {
+  uint8_t* cache;
+  int64_t page_bytes;
+  int32_t num_pages;
+  const int32_t* refs;
+  int32_t* refs_out;
+  const int32_t* table;
+  int32_t* table_out;
+  int32_t rows, entries, bt_stride;
+  int32_t* remap;
+  int32_t* live;
+  uint32_t* err;
+  int32_t* block_live;  // in the workspace, set by the launch, as the rest
+  int32_t* moves;
+  int2* movers;         // page, count
+  int32_t* holes;
+};
+int64_t compact_workspace_bytes(int64_t num_pages);
+cudaError_t launch_compact(const CompactParams& p, void* workspace, cudaStream_t st);
+
+// The 8-bit block cache (kvarn_q8.cu): blocks of 16 tokens written, read back
+// or completed by an appended token.
+struct Q8BlockParams {
+  const void* k;  // tokens (written by the read)
+  const void* v;
+  int64_t seq_stride, head_stride, token_stride;  // elements
+  int32_t num_seqs, blocks;
+  const int32_t* block_start;
+  const int32_t* seq_lens;  // append
+  int32_t max_seq_len;
+  void* tail_k;  // [B][Hkv][tail_cap][D]
+  void* tail_v;
+  int32_t tail_cap;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  void* cache;
+  int64_t num_pages;
+  int32_t num_kv_heads, D;
+  bool bf16;
+  int32_t code;  // 0 e4m3, 1 int8
+  uint32_t* err;
+};
+cudaError_t launch_q8_blocks(const Q8BlockParams& p, bool read, cudaStream_t st);
+cudaError_t launch_q8_append(const Q8BlockParams& p, cudaStream_t st);
+
+// Decode over the 8-bit block cache, with a sliding window (kvarn_q8_decode.cu).
+struct Q8DecodeParams {
+  const void* q;  // [B][Q][Hq][D]
+  const uint8_t* cache;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  const int32_t* seq_lens;
+  int32_t max_seq_len, num_seqs, num_queries, num_q_heads, num_kv_heads, D;
+  int64_t num_pages;
+  const void* tail_k;
+  const void* tail_v;
+  int32_t tail_cap;
+  int32_t window, sinks;  // window 0: none
+  float sm_scale;
+  bool bf16;
+  int32_t code;
+  float* out;
+  float* lse;
+  void* workspace;
+  uint32_t* err;
+};
+int64_t q8_decode_workspace_bytes(int32_t num_seqs, int32_t rows, int32_t D);
+cudaError_t launch_q8_decode(const Q8DecodeParams& p, cudaStream_t st);
+
 int device_sm_count();
 // Diagnostic: clock cycles the dense decode kernels wait for a page copy (0:
 // default) and whether each copy is announced larger than it is (so that its
 // phase never completes and every wait runs out).
 void set_copy_wait_test(long long cycles, int withhold);
+long long copy_wait_limit();  // cycles, the default where none is set
+int copy_withhold();
 
 }  // namespace kvarn

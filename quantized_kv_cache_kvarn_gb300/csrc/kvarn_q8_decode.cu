@@ -1,0 +1,840 @@
+// Decode attention over the 8-bit block cache, with a sliding window and
+// sinks, sm_103a.
+//
+// Query j of sequence b sits at position p = L - Q + j and sees the tokens
+// i <= p with i < S or i > p - W (W = 0: all). Its output is
+//   sum_i 2^(s_i) v_i / sum_i 2^(s_i),  s_i = sm_scale log2(e) q . k_i,
+// k_i = K scale of i's block times codes, v_i likewise.
+//
+// Work. The visible blocks of a sequence (those of the sinks, those from the
+// window's start on) form one list, taken two at a time as items; up to
+// sixteen raw tail tokens are an item too. The items of all units (sequence,
+// KV head, group of R query rows) are one list, and every warp of the grid
+// takes an equal contiguous range of it, so that neither a long sequence nor
+// a short window leaves SMs idle and no page outside a window is touched. A
+// unit that lies in one range is written out by its warp; the parts of others
+// go to the workspace (two slots per range: of its first and its last unit)
+// and a second kernel joins them.
+//
+// A warp works alone: a ring of kStages items in shared memory, filled by one
+// bulk copy per page (lane 0, bounded waits on the stage's mbarrier), and the
+// tensor cores' m16n8k16 with fp16 operands. Codes of both kinds are exact in
+// fp16, and so is a row of queries scaled by a power of two, so that Q K needs
+// one product. The weights go in as fp16 hi + lo: with up to eight rows (R =
+// 8) they fill the two halves of the m16 tile, with more (R = 16) they are two
+// products into one accumulator.
+//
+// Two running maxima per row, both whole numbers (so that rescaling is exact):
+// m of s for the sum of the weights, and mt of s + e, 2^e the power of two in
+// the block's V scale, for the output, so that blocks of any scales add up
+// without leaving fp16's range: the operand is 2^(s + e - mt + 12) times the
+// scale's mantissa, and a weight counts down to 2^-36 of the largest share.
+//
+// At head_dim 256 two warps share an item, 128 channels each (one warp's output
+// alone would take 128 registers a thread): they add each other's scores by way
+// of shared memory, meeting once an item at a named barrier, and do the softmax
+// twice. That barrier has no time limit, so a warp whose wait ran out says so
+// beside its scores and both leave behind the same meeting.
+//
+// The raw tail (at most Q + 14 tokens a sequence) is done in fp32 without the
+// tensor cores: hidden tokens' values are never multiplied, whatever they are.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kvarn_launch.h"
+#include "kvarn_merge.cuh"
+#include "kvarn_q8.cuh"
+
+namespace kvarn {
+
+namespace {
+
+constexpr int kStages = 3;
+constexpr float kOff = 12.f;  // exponent of the weights' operands over mt
+
+struct Q8Args {
+  const void* q;
+  const uint8_t* cache;
+  const int32_t* table;
+  int32_t bt_stride;
+  const int32_t* lens;
+  int32_t max_len, B, Q, Hq, Hkv, G, groups;
+  int64_t num_pages;
+  const void* tail_k;
+  const void* tail_v;
+  int32_t tail_cap;
+  int32_t window, sinks;
+  float scale_log2;
+  int32_t bf16;
+  float* out;
+  float* lse;
+  int64_t* offs;  // [B + 1]: items before each sequence
+  float* part;    // [teams][2][R][D + 4]
+  uint32_t* err;
+  long long wait_limit;
+  int32_t withhold;
+};
+
+constexpr int kWarps = 8, kDW = 128;  // channels of a warp
+
+template <int D, int R> struct Shape {
+  static constexpr int HV = D / kDW, TEAMS = kWarps / HV;
+  static constexpr int PB = q8_page(D), STAGE = 2 * PB;
+  static constexpr int XLANE = R;  // floats that a lane exchanges: 32 tokens' scores of its rows over four lanes
+  static constexpr int XBUF = HV == 2 ? 2 * 2 * XLANE * 32 * 4 : 0;  // [parity][half][value][lane], per team
+  static constexpr int XCHG = TEAMS * kStages * STAGE;
+  static constexpr int FLAGS = XCHG + TEAMS * XBUF;  // [team][parity][half]
+  static constexpr int BARS = FLAGS + (HV == 2 ? TEAMS * 16 : 0);
+  static constexpr int SMEM = BARS + TEAMS * kStages * 8;
+  static_assert(SMEM + 512 <= 227 * 1024, "shared memory of a CTA");
+};
+// Floats of a partial row: m, l, mt, pad, output.
+__host__ __device__ constexpr int part_row(int D) { return D + 4; }
+
+// What a sequence's queries see: blocks [0, sp) and [wp, C) of C whole ones,
+// then `tail` raw tokens.
+struct Seq {
+  int L, C, sp, wp, np, tail, page_items, items;
+  __device__ __forceinline__ void load(const Q8Args& A, int b) {
+    L = min(max(A.lens[b], 0), A.max_len);
+    C = max(0, L - A.Q + 1) / kPageTokens;
+    sp = C;
+    wp = C;
+    if (A.window > 0) {
+      wp = min(C, max(0, L - A.Q + 1 - A.window) / kPageTokens);
+      sp = min(C, (A.sinks + kPageTokens - 1) / kPageTokens);
+      if (sp >= wp) sp = wp = C;
+    }
+    np = sp + C - wp;
+    tail = L - C * kPageTokens;
+    page_items = (np + 1) >> 1;
+    items = page_items + (tail + 15) / 16;
+  }
+  __device__ __forceinline__ int block(int i) const { return i < sp ? i : wp + i - sp; }
+};
+
+// A place in the item list.
+struct Place {
+  int b, u, i;
+  Seq s;
+  __device__ __forceinline__ void next(const Q8Args& A, int units) {
+    if (++i < s.items) return;
+    i = 0;
+    if (++u < units) return;
+    u = 0;
+    do {
+      if (++b >= A.B) return;
+      s.load(A, b);
+    } while (s.items == 0);
+  }
+};
+
+// d = A B: the accumulators need not be cleared before.
+__device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ float ex2(float x) { return fast_exp2(x); }
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
+
+// Four consecutive 16-bit elements as floats.
+__device__ __forceinline__ void raw4(uint32_t a, uint32_t b, bool bf16, float* f) {
+  if (bf16) {
+    f[0] = __uint_as_float(a << 16);
+    f[1] = __uint_as_float(a & 0xffff0000u);
+    f[2] = __uint_as_float(b << 16);
+    f[3] = __uint_as_float(b & 0xffff0000u);
+  } else {
+    const float2 x = __half22float2(u32_as_h2(a)), y = __half22float2(u32_as_h2(b));
+    f[0] = x.x;
+    f[1] = x.y;
+    f[2] = y.x;
+    f[3] = y.y;
+  }
+}
+
+// Sixteen consecutive 16-bit elements (32 bytes, aligned to 16) as floats.
+__device__ __forceinline__ void raw16(const uint16_t* p, bool bf16, float* f) {
+  const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8);
+  raw4(x.x, x.y, bf16, f);
+  raw4(x.z, x.w, bf16, f + 4);
+  raw4(y.x, y.y, bf16, f + 8);
+  raw4(y.z, y.w, bf16, f + 12);
+}
+
+// The rows of a unit that a lane holds: row lane / 4, and row 8 + lane / 4
+// where R is 16; of D channels those from c0 on.
+template <int D, int R>
+struct Rows {
+  static constexpr int NR = R / 8;
+  uint32_t q[kDW / 16][2 * NR];  // k-step: (a0, a2) of the first row, then (a1, a3) of the second
+  float qs[NR];                  // what a row's products are times, per unit K scale
+  int pos[NR];                   // position of the row's query
+  float m[NR], mt[NR], l[NR];
+  float o[kDW / 8][4];
+
+  // q channels c0 + 16 (t + 4 c) + 4 s .. + 3 are k-step 4 c + s of lane column t.
+  __device__ __forceinline__ void load(const Q8Args& A, int b, int u, const Seq& s, int c0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int h = u / A.groups, grp = u % A.groups;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int rr = grp * R + 8 * r + g;
+      const bool real = rr < A.G * A.Q;
+      const int j = real ? rr / A.G : 0, hg = real ? rr % A.G : 0;
+      pos[r] = real ? s.L - A.Q + j : -1;
+      const uint16_t* src = static_cast<const uint16_t*>(A.q) +
+                            ((static_cast<int64_t>(b) * A.Q + j) * A.Hq + h * A.G + hg) * D + c0;
+      float top = 0.f;
+      bool finite = true;
+#pragma unroll
+      for (int c = 0; c < kDW / 64; ++c) {
+        float f[16];
+        raw16(src + 16 * (t + 4 * c), A.bf16, f);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          top = fmaxf(top, fabsf(f[k]));
+          finite = finite && fabsf(f[k]) < INFINITY;
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t votes = __ballot_sync(0xffffffffu, finite);
+      finite = ((votes >> (lane & 28)) & 15u) == 15u;
+      // the largest element to [2^14, 2^15); smaller ones stay normal fp16
+      // numbers down to 2^-28 of it
+      const int e = finite && top > 0.f ? 141 - static_cast<int>(__float_as_uint(top) >> 23) : 0;
+      const int e1 = e >> 1, e2 = e - e1;  // 2^e may not be a float (bf16 subnormals)
+      const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+      const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+      const float i1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
+      const float i2 = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+      qs[r] = finite ? A.scale_log2 * i1 * i2 : nan_f();
+#pragma unroll
+      for (int c = 0; c < kDW / 64; ++c) {
+        float f[16];
+        raw16(src + 16 * (t + 4 * c), A.bf16, f);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) f[k] = finite && real ? f[k] * f1 * f2 : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          q[4 * c + k][2 * r] = h2_as_u32(__floats2half2_rn(f[4 * k], f[4 * k + 1]));
+          q[4 * c + k][2 * r + 1] = h2_as_u32(__floats2half2_rn(f[4 * k + 2], f[4 * k + 3]));
+        }
+      }
+      m[r] = mt[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < kDW / 8; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
+  }
+
+  __device__ __forceinline__ bool sees(const Q8Args& A, int r, int token) const {
+    return token <= pos[r] && (A.window == 0 || token < A.sinks || token > pos[r] - A.window);
+  }
+
+  // New maxima over this lane's scores' maxima; rescales what was added up.
+  __device__ __forceinline__ void raise(const float (&ms)[NR], const float (&mts)[NR]) {
+    float a[NR];
+    bool moved = false;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float x = ms[r], y = mts[r];
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+      x = fmaxf(m[r], ceilf(x));
+      y = fmaxf(mt[r], ceilf(y));
+      l[r] *= x == m[r] ? 1.f : ex2(m[r] - x);
+      a[r] = y == mt[r] ? 1.f : ex2(mt[r] - y);
+      moved = moved || y != mt[r];
+      m[r] = x;
+      mt[r] = y;
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int n = 0; n < kDW / 8; ++n) {
+        o[n][0] *= a[0];
+        o[n][1] *= a[0];
+        o[n][2] *= a[NR - 1];
+        o[n][3] *= a[NR - 1];
+      }
+    }
+  }
+
+  // Weight of a score for the sum, and its operand with 2^ev vm the V scale.
+  __device__ __forceinline__ void weigh(int r, float s, float ev, float vm, float& sum, float& w) const {
+    const bool none = m[r] == -INFINITY;
+    const float p = ex2(s - (none ? 0.f : m[r]));
+    sum += p;
+    // at most 2^13: fp32 rounds s + ev - mt of scores beyond 2^24
+    const float x = ex2(fminf(s + (ev - (none ? 0.f : mt[r]) + kOff), kOff + 1.f)) * vm;
+    w = s == -INFINITY ? 0.f : x;
+  }
+
+  // This warp's part of the scores of an item's two pages, the second one the
+  // first again where the list ends (n = 1): token 8 e + 2 t + j of page p for
+  // row r at s[8 r + 4 p + 2 e + j].
+  template <int CODE>
+  __device__ __forceinline__ void page_scores(const unsigned char* pg0, const unsigned char* pg1, int half,
+                                              float (&s)[R]) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float acc[2][2][4];
+#pragma unroll
+    for (int c = 0; c < kDW / 64; ++c) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 v = *reinterpret_cast<const uint4*>((p ? pg1 : pg0) + (8 * e + g) * D + half * kDW +
+                                                          16 * ((t + 4 * c) ^ (4 * (g & 1))));
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t b0, b1;
+            q8_pairs<CODE>(x[k], b0, b1);
+            const uint32_t* a = q[4 * c + k];
+            if (c == 0 && k == 0)
+              mma_first(acc[p][e], a[0], NR == 2 ? a[2 * NR - 2] : 0u, a[1], NR == 2 ? a[2 * NR - 1] : 0u, b0, b1);
+            else
+              mma_f16(acc[p][e], a[0], NR == 2 ? a[2 * NR - 2] : 0u, a[1], NR == 2 ? a[2 * NR - 1] : 0u, b0, b1);
+          }
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float ks = *reinterpret_cast<const float*>((p ? pg1 : pg0) + q8_scales(D));
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 0; x < 2 * NR; ++x) s[8 * (x >> 1) + 4 * p + 2 * e + (x & 1)] = acc[p][e][x] * (ks * qs[x >> 1]);
+    }
+  }
+
+  template <int CODE>
+  __device__ __forceinline__ void add_pages(const Q8Args& A, const unsigned char* pg0, const unsigned char* pg1, int half,
+                                            const Seq& sq, int i0, int n, float (&s)[R]) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    float ev[2], vm[2];
+    int first[2];
+    bool edge = n < 2;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint32_t bits = *reinterpret_cast<const uint32_t*>((p ? pg1 : pg0) + q8_scales(D) + 4);
+      ev[p] = static_cast<float>(static_cast<int>(bits >> 23 & 0xff) - 127);
+      vm[p] = (bits >> 23 & 0xff) == 0xff ? nan_f() : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+      first[p] = p < n ? sq.block(i0 + p) * kPageTokens : 0;
+      if (A.window > 0 && first[p] + kPageTokens > A.sinks && first[p] <= sq.L - 1 - A.window) edge = true;
+    }
+    if (edge) {
+#pragma unroll
+      for (int x = 0; x < R; ++x) {
+        const int p = x >> 2 & 1;
+        if (p >= n || !sees(A, x >> 3, first[p] + 8 * (x >> 1 & 1) + 2 * t + (x & 1))) s[x] = -INFINITY;
+      }
+    }
+    float ms[NR], mts[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float top[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        top[p] = fmaxf(fmaxf(s[8 * r + 4 * p], s[8 * r + 4 * p + 1]), fmaxf(s[8 * r + 4 * p + 2], s[8 * r + 4 * p + 3]));
+      ms[r] = fmaxf(top[0], top[1]);
+      mts[r] = fmaxf(top[0] + ev[0], top[1] + ev[1]);
+    }
+    raise(ms, mts);
+    uint32_t hi[2][2][NR], lo[2][2][NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float sum = 0.f;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float w0, w1;
+          weigh(r, s[8 * r + 4 * p + 2 * e], ev[p], vm[p], sum, w0);
+          weigh(r, s[8 * r + 4 * p + 2 * e + 1], ev[p], vm[p], sum, w1);
+          split_hi_lo(w0, w1, hi[p][e][r], lo[p][e][r]);
+        }
+      l[r] += sum;
+    }
+    // The products of the two pages start from zero and join the output by
+    // rounded additions: the tensor cores truncate what they accumulate, which
+    // over thousands of tokens adds up to 4e-6 where this leaves 6e-7.
+#pragma unroll
+    for (int w = 0; w < kDW / 32; ++w) {
+      uint32_t x[2][4];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint4 v = *reinterpret_cast<const uint4*>((p ? pg1 : pg0) + 16 * D + 16 * (32 * (4 * half + w) + lane));
+        x[p][0] = v.x;
+        x[p][1] = v.y;
+        x[p][2] = v.z;
+        x[p][3] = v.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float* to = o[4 * w + k];
+        uint32_t b[2][2];
+        q8_pairs<CODE>(x[0][k], b[0][0], b[0][1]);
+        q8_pairs<CODE>(x[1][k], b[1][0], b[1][1]);
+        float d[4];
+        if constexpr (NR == 1) {
+          mma_first(d, hi[0][0][0], lo[0][0][0], hi[0][1][0], lo[0][1][0], b[0][0], b[0][1]);
+          mma_f16(d, hi[1][0][0], lo[1][0][0], hi[1][1][0], lo[1][1][0], b[1][0], b[1][1]);
+        } else {
+          mma_first(d, lo[0][0][0], lo[0][0][NR - 1], lo[0][1][0], lo[0][1][NR - 1], b[0][0], b[0][1]);
+          mma_f16(d, lo[1][0][0], lo[1][0][NR - 1], lo[1][1][0], lo[1][1][NR - 1], b[1][0], b[1][1]);
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            mma_f16(d, hi[p][0][0], hi[p][0][NR - 1], hi[p][1][0], hi[p][1][NR - 1], b[p][0], b[p][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float2 v = f2add(make_float2(to[i], to[i + 1]), make_float2(d[i], d[i + 1]));
+          to[i] = v.x;
+          to[i + 1] = v.y;
+        }
+      }
+    }
+  }
+
+  // Raw tokens of the tail in fp32, n <= 16 rows from K on: token 8 e + 2 t + j
+  // for row r at s[8 r + 2 e + j].
+  __device__ __forceinline__ void raw_scores(const Q8Args& A, const uint16_t* K, int n, float (&s)[R]) const {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int x = 0; x < R; ++x) s[x] = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      float d[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) d[r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kDW / 64; ++c) {
+        float f[16];
+        raw16(K + static_cast<int64_t>(i) * D + 16 * (t + 4 * c), A.bf16, f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float2 a = __half22float2(u32_as_h2(q[4 * c + k][2 * r]));
+            const float2 b = __half22float2(u32_as_h2(q[4 * c + k][2 * r + 1]));
+            d[r] = fmaf(a.x, f[4 * k], d[r]);
+            d[r] = fmaf(a.y, f[4 * k + 1], d[r]);
+            d[r] = fmaf(b.x, f[4 * k + 2], d[r]);
+            d[r] = fmaf(b.y, f[4 * k + 3], d[r]);
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        d[r] += __shfl_xor_sync(0xffffffffu, d[r], 1);
+        d[r] += __shfl_xor_sync(0xffffffffu, d[r], 2);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (i == 8 * (x >> 1) + 2 * t + (x & 1)) s[8 * r + x] = d[r] * qs[r];
+      }
+    }
+  }
+
+  __device__ __forceinline__ void add_raw(const Q8Args& A, const uint16_t* V, int token0, int n, const float (&s)[R]) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    float w[NR][4], ms[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      ms[r] = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int i = 8 * (x >> 1) + 2 * t + (x & 1);
+        w[r][x] = i < n && sees(A, r, token0 + i) ? s[8 * r + x] : -INFINITY;
+        ms[r] = fmaxf(ms[r], w[r][x]);
+      }
+    }
+    raise(ms, ms);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) weigh(r, w[r][x], 0.f, 1.f, sum, w[r][x]);
+      l[r] += sum;
+    }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int x = 2 * (i >> 3) + (i & 1), from = (lane & 28) | (i & 7) >> 1;
+      float wi[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float v = x == 0 ? w[r][0] : x == 1 ? w[r][1] : x == 2 ? w[r][2] : w[r][3];
+        wi[r] = __shfl_sync(0xffffffffu, v, from);
+      }
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(V + static_cast<int64_t>(i) * D) + t;
+#pragma unroll
+      for (int c = 0; c < kDW / 8; ++c) {
+        float f[4];
+        raw4(src[4 * c], 0u, A.bf16, f);
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          if (wi[r] != 0.f) {  // a hidden token's value may be anything
+            o[c][2 * r] = fmaf(wi[r], f[0], o[c][2 * r]);
+            o[c][2 * r + 1] = fmaf(wi[r], f[1], o[c][2 * r + 1]);
+          }
+      }
+    }
+  }
+};
+
+// out and lse of a row from its sums: O 2^(mt - kOff) / (l 2^m).
+__device__ __forceinline__ float out_factor(float m, float mt, float l) {
+  return l == 0.f ? 0.f : exp2f(mt - m - kOff) / l;
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
+template <int D, int R, int CODE>
+__global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_constant__ Q8Args A) {
+  using S = Shape<D, R>;
+  constexpr int W = kWarps, HV = S::HV, TEAMS = S::TEAMS, ROW = part_row(D);
+  extern __shared__ __align__(128) unsigned char smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
+  __shared__ int64_t sum_of[W], start_at[TEAMS], total_sh;
+  __shared__ int start_b[TEAMS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < TEAMS * kStages) mbar_init(bars + tid, 1);
+  fence_mbar_init();
+  pdl_wait_primary();
+  pdl_launch_dependents();
+
+  // Items before each sequence: thread i counts those of an equal share of
+  // the sequences.
+  const int units = A.Hkv * A.groups;
+  const int per = (A.B + 32 * W - 1) / (32 * W), b0 = min(A.B, tid * per), b1 = min(A.B, b0 + per);
+  int64_t mine = 0;
+  Place at;
+  for (int b = b0; b < b1; ++b) {
+    at.s.load(A, b);
+    mine += static_cast<int64_t>(at.s.items) * units;
+    if (blockIdx.x == 0) {
+      if (A.lens[b] != at.s.L) set_error(A.err, KVARN_DEVERR_SEQ_LEN);
+      if (at.s.tail > 0 && (!A.tail_k || !A.tail_v)) set_error(A.err, KVARN_DEVERR_NO_TAIL);
+    }
+  }
+  int64_t before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += x;
+  }
+  if (lane == 31) sum_of[warp] = before;
+  before -= mine;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before += sum_of[w];
+  if (tid == 32 * W - 1) total_sh = before + mine;
+  __syncthreads();
+  // Range e of as many as there are teams (warps, or pairs of them), at most
+  // one per item, is that of team e / grid of CTA e % grid: few items spread
+  // over the SMs.
+  const int64_t total = total_sh, teams = min(total, static_cast<int64_t>(gridDim.x) * TEAMS);
+  auto range_of = [&](int w) { return static_cast<int64_t>(w) * gridDim.x + blockIdx.x; };
+  for (int b = b0; b < b1; ++b) {
+    if (blockIdx.x == 0) A.offs[b] = before;
+    at.s.load(A, b);
+    const int64_t n = static_cast<int64_t>(at.s.items) * units;
+    for (int w = 0; w < TEAMS; ++w) {
+      const int64_t e = range_of(w), x = e < teams ? e * total / teams : -1;
+      if (x >= before && x < before + n) {
+        start_b[w] = b;
+        start_at[w] = x - before;
+      }
+    }
+    before += n;
+  }
+  if (blockIdx.x == 0 && tid == 0) A.offs[A.B] = total;
+  __syncthreads();
+  const int team = warp / HV, half = warp % HV;
+  const int64_t range = range_of(team);
+  if (range >= teams) return;
+  const int64_t x0 = range * total / teams, x1 = (range + 1) * total / teams;
+
+  at.b = start_b[team];
+  at.s.load(A, at.b);
+  at.u = static_cast<int>(start_at[team] / at.s.items);
+  at.i = static_cast<int>(start_at[team] % at.s.items);
+  Place ahead = at;
+  const int count = static_cast<int>(x1 - x0);  // items of this team
+  unsigned char* ring = smem + team * kStages * S::STAGE;
+  uint64_t* bar = bars + team * kStages;
+
+  // Copies of the next item that none has been asked for into its stage. ids:
+  // 32 entries of the block list of sequence ids_b from ids_at on.
+  int ids = 0, ids_b = -1, ids_at = 0, issued = 0;
+  auto issue = [&]() {
+    const int st = issued % kStages;
+    if (ahead.i < ahead.s.page_items) {
+      const int i = 2 * ahead.i, n = min(2, ahead.s.np - i);
+      if (ids_b != ahead.b || ids_at != (i & ~31)) {
+        ids_b = ahead.b;
+        ids_at = i & ~31;
+        const int k = ids_at + lane;
+        ids = 0;
+        if (k < ahead.s.np) {
+          ids = A.table[static_cast<int64_t>(ahead.b) * A.bt_stride + ahead.s.block(k)];
+          if (ids < 0 || ids >= A.num_pages) {
+            set_error(A.err, KVARN_DEVERR_PAGE_RANGE);
+            ids = 0;
+          }
+        }
+      }
+      const int p0 = __shfl_sync(0xffffffffu, ids, i & 31), p1 = __shfl_sync(0xffffffffu, ids, (i + 1) & 31);
+      if (lane == 0) {
+        const int h = ahead.u / A.groups;
+        unsigned char* dst = ring + st * S::STAGE;
+        mbar_arrive_expect_tx(bar + st, n * S::PB + A.withhold);
+        bulk_g2s(dst, A.cache + (static_cast<int64_t>(p0) * A.Hkv + h) * S::PB, S::PB, bar + st);
+        if (n == 2) bulk_g2s(dst + S::PB, A.cache + (static_cast<int64_t>(p1) * A.Hkv + h) * S::PB, S::PB, bar + st);
+      }
+    } else if (lane == 0) {
+      mbar_arrive_expect_tx(bar + st, 0);  // raw tokens: nothing to copy
+    }
+    ++issued;
+    if (issued < count) ahead.next(A, units);
+  };
+  if (half == 0)
+    for (int k = 0; k < min(kStages, count); ++k) issue();
+
+  Rows<D, R> rows;
+  bool fresh = true, whole = false;  // whole: the unit's first item was this team's
+  int seg_item = 0;                  // the range's item that the segment began with
+  for (int k = 0; k < count; ++k) {
+    if (fresh) {
+      rows.load(A, at.b, at.u, at.s, half * kDW);
+      fresh = false;
+      whole = at.i == 0;
+      seg_item = k;
+    }
+    const int st = k % kStages;
+    const bool came = __all_sync(0xffffffffu, mbar_wait_bounded(bar + st, (k / kStages) & 1, A.wait_limit));
+    const bool paged = at.i < at.s.page_items;
+    const int i0 = 2 * at.i, n = min(2, at.s.np - i0);
+    const unsigned char* pg0 = ring + st * S::STAGE;
+    const unsigned char* pg1 = n == 2 ? pg0 + S::PB : pg0;
+    const int r0 = 16 * (at.i - at.s.page_items), nraw = min(16, at.s.tail - r0);
+    const int64_t raw_at = ((static_cast<int64_t>(at.b) * A.Hkv + at.u / A.groups) * A.tail_cap + r0) * D + half * kDW;
+    const bool raw = !paged && A.tail_k && A.tail_v;
+    float s[R];
+    if (paged)
+      rows.template page_scores<CODE>(pg0, pg1, half, s);
+    else if (raw)
+      rows.raw_scores(A, static_cast<const uint16_t*>(A.tail_k) + raw_at, nraw, s);
+    bool dead = !came;
+    if constexpr (HV == 2) {
+      float* mine = reinterpret_cast<float*>(smem + S::XCHG + team * S::XBUF) + ((k & 1) * 2 + half) * S::XLANE * 32;
+      const float* other = mine + (half ? -1 : 1) * S::XLANE * 32;
+      volatile int* flag = reinterpret_cast<volatile int*>(smem + S::FLAGS) + (team * 2 + (k & 1)) * 2;
+#pragma unroll
+      for (int x = 0; x < R; ++x) mine[x * 32 + lane] = s[x];
+      if (lane == 0) flag[half] = dead;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + team) : "memory");
+#pragma unroll
+      for (int x = 0; x < R; ++x) s[x] += other[x * 32 + lane];
+      dead = dead || flag[half ^ 1];
+      // both warps have left the item before this one
+      if (half == 0 && !dead && k > 0 && issued < count) issue();
+    }
+    if (dead) {
+      // give up: the copies under way have to land before the CTA leaves
+      if (!came) set_error(A.err, KVARN_DEVERR_TIMEOUT);
+      for (int j = k; j < min(count, k + kStages); ++j)
+        if (half != 0 || j < issued) mbar_wait_bounded(bar + j % kStages, (j / kStages) & 1, 100000000LL);
+      return;
+    }
+    if (paged)
+      rows.template add_pages<CODE>(A, pg0, pg1, half, at.s, i0, n, s);
+    else if (raw)
+      rows.add_raw(A, static_cast<const uint16_t*>(A.tail_v) + raw_at, at.s.C * kPageTokens + r0, nraw, s);
+    __syncwarp();
+    if (HV == 1 && issued < count) issue();
+    const bool last = at.i + 1 == at.s.items;
+    if (last || k + 1 == count) {
+      const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+      for (int r = 0; r < rows.NR; ++r) {
+        float l = rows.l[r];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const int rr = (at.u % A.groups) * R + 8 * r + g;
+        float f = 1.f;
+        float* dst = nullptr;
+        if (last && whole) {
+          if (rr < A.G * A.Q) {
+            const int64_t row = (static_cast<int64_t>(at.b) * A.Q + rr / A.G) * A.Hq + at.u / A.groups * A.G + rr % A.G;
+            f = out_factor(rows.m[r], rows.mt[r], l);
+            dst = A.out + row * D;
+            if (A.lse && t == 0 && half == 0) A.lse[row] = lse_of(rows.m[r], l);
+          }
+        } else {
+          dst = A.part + ((2 * range + (seg_item == 0 ? 0 : 1)) * R + 8 * r + g) * ROW;
+          if (t == 0 && half == 0) *reinterpret_cast<float4*>(dst) = make_float4(rows.m[r], l, rows.mt[r], 0.f);
+          dst += 4;
+        }
+        if (dst) {
+          dst += half * kDW + 2 * t;
+#pragma unroll
+          for (int c = 0; c < kDW / 8; ++c) {
+            const float a = rows.NR == 2 ? rows.o[c][2 * r] : rows.o[c][0] + rows.o[c][2];
+            const float b = rows.NR == 2 ? rows.o[c][2 * r + 1] : rows.o[c][1] + rows.o[c][3];
+            *reinterpret_cast<float2*>(dst + 8 * c) = make_float2(a * f, b * f);
+          }
+        }
+      }
+      fresh = true;
+    }
+    if (k + 1 < count) at.next(A, units);
+  }
+}
+
+// One warp per output row: joins the parts of units that several warps took,
+// writes the rows of empty sequences.
+template <int D, int R>
+__global__ void __launch_bounds__(128) q8_merge_kernel(const __grid_constant__ Q8Args A, int64_t grid_teams) {
+  constexpr int E = D / 32, ROW = part_row(D);
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t b = row / (static_cast<int64_t>(A.Q) * A.Hq);
+  if (b >= A.B) return;
+  const int j = static_cast<int>(row / A.Hq % A.Q), hq = static_cast<int>(row % A.Hq);
+  const int h = hq / A.G, rr = j * A.G + hq % A.G, units = A.Hkv * A.groups;
+  const int64_t o0 = A.offs[b], o1 = A.offs[b + 1], total = A.offs[A.B];
+  const int64_t items = (o1 - o0) / units, teams = min(total, grid_teams);
+  float* dst = A.out + row * D + lane * E;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  float M = -INFINITY, L = 0.f, f = 0.f;
+  if (items > 0) {
+    const int64_t p0 = o0 + (static_cast<int64_t>(h) * A.groups + rr / R) * items, p1 = p0 + items;
+    // the range of item x is the last that begins at or before it
+    const int64_t w0 = ((p0 + 1) * teams - 1) / total, w1 = (p1 * teams - 1) / total;
+    if (w0 == w1) return;
+    const bool inside = w0 * total / teams < p0;  // the first range begins before the unit
+    const int n = static_cast<int>(w1 - w0 + 1);
+    const float* part = A.part + (2 * w0 * R + rr % R) * ROW;
+    auto slot = [&](int i) { return part + static_cast<int64_t>(2 * i + (i == 0 && inside ? 1 : 0)) * R * ROW; };
+    float MT = -INFINITY;
+    for (int i = lane; i < n; i += 32) {
+      const float* p = slot(i);
+      M = fmaxf(M, p[0]);
+      MT = fmaxf(MT, p[2]);
+    }
+    M = warp_max_xor(M, 1, 32);
+    MT = warp_max_xor(MT, 1, 32);
+    const float mu = M == -INFINITY ? 0.f : M, mtu = MT == -INFINITY ? 0.f : MT;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* p = slot(i);
+      const float4 head = *reinterpret_cast<const float4*>(p);
+      L = fmaf(head.y, exp2f(head.x - mu), L);
+      const float w = exp2f(head.z - mtu);
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + 4 + lane * E + e);
+        acc[e] = fmaf(v.x, w, acc[e]);
+        acc[e + 1] = fmaf(v.y, w, acc[e + 1]);
+        acc[e + 2] = fmaf(v.z, w, acc[e + 2]);
+        acc[e + 3] = fmaf(v.w, w, acc[e + 3]);
+      }
+    }
+    f = out_factor(mu, mtu, L);
+    M = mu;
+  }
+#pragma unroll
+  for (int e = 0; e < E; e += 4)
+    *reinterpret_cast<float4*>(dst + e) = make_float4(acc[e] * f, acc[e + 1] * f, acc[e + 2] * f, acc[e + 3] * f);
+  if (A.lse && lane == 0) A.lse[row] = lse_of(M, L);
+}
+
+int rows_per_group(int rows) { return rows > 8 ? 16 : 8; }
+
+template <int D, int R, int CODE>
+cudaError_t run(const Q8Args& A, int ctas, cudaStream_t st) {
+  using S = Shape<D, R>;
+  auto* kernel = q8_decode_kernel<D, R, CODE>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, A);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(A.B) * A.Q * A.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, q8_merge_kernel<D, R>, A, static_cast<int64_t>(ctas) * S::TEAMS);
+}
+
+}  // namespace
+
+// Offsets, then two partial slots per team.
+int64_t q8_decode_workspace_bytes(int32_t num_seqs, int32_t rows, int32_t D) {
+  const int64_t teams = static_cast<int64_t>(device_sm_count()) * (kWarps * kDW / D);
+  return (8LL * (num_seqs + 1) + 127) / 128 * 128 + teams * 2 * rows_per_group(rows) * part_row(D) * 4;
+}
+
+cudaError_t launch_q8_decode(const Q8DecodeParams& p, cudaStream_t st) {
+  Q8Args A{};
+  A.q = p.q;
+  A.cache = p.cache;
+  A.table = p.block_table;
+  A.bt_stride = p.bt_stride;
+  A.lens = p.seq_lens;
+  A.max_len = p.max_seq_len;
+  A.B = p.num_seqs;
+  A.Q = p.num_queries;
+  A.Hq = p.num_q_heads;
+  A.Hkv = p.num_kv_heads;
+  A.G = p.num_q_heads / p.num_kv_heads;
+  const int R = rows_per_group(A.G * A.Q);
+  A.groups = (A.G * A.Q + R - 1) / R;
+  A.num_pages = p.num_pages;
+  A.tail_k = p.tail_k;
+  A.tail_v = p.tail_v;
+  A.tail_cap = p.tail_cap;
+  // every query sees at most the whole sequence
+  A.window = p.window >= p.max_seq_len ? 0 : p.window;
+  A.sinks = std::min(p.sinks, p.max_seq_len);
+  A.scale_log2 = p.sm_scale * 1.4426950408889634f;
+  A.bf16 = p.bf16;
+  A.out = p.out;
+  A.lse = p.lse;
+  A.offs = static_cast<int64_t*>(p.workspace);
+  A.part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + (8LL * (p.num_seqs + 1) + 127) / 128 * 128);
+  A.err = p.err;
+  A.wait_limit = copy_wait_limit();
+  A.withhold = copy_withhold();
+  const int ctas = device_sm_count();
+  const bool i8 = p.code == kQ8Int8;
+  if (p.D == 128) {
+    if (R == 8) return i8 ? run<128, 8, kQ8Int8>(A, ctas, st) : run<128, 8, kQ8E4M3>(A, ctas, st);
+    return i8 ? run<128, 16, kQ8Int8>(A, ctas, st) : run<128, 16, kQ8E4M3>(A, ctas, st);
+  }
+  if (R == 8) return i8 ? run<256, 8, kQ8Int8>(A, ctas, st) : run<256, 8, kQ8E4M3>(A, ctas, st);
+  return i8 ? run<256, 16, kQ8Int8>(A, ctas, st) : run<256, 16, kQ8E4M3>(A, ctas, st);
+}
+
+}  // namespace kvarn

@@ -50,7 +50,6 @@ namespace kvarn {
 
 namespace {
 
-constexpr int kStages = 3;
 constexpr float kOff = 12.f;  // exponent of the weights' operands over mt
 
 struct Q8Args {
@@ -76,7 +75,12 @@ struct Q8Args {
   int32_t withhold;
 };
 
-constexpr int kWarps = 8, kDW = 128;  // channels of a warp
+constexpr int kDW = 128;  // channels of a warp
+
+// One CTA of eight warps per SM, each with a ring of three items. Twelve warps
+// of 168 registers with two items each spill and take 192 us where eight take
+// 180 (32 x 16384 tokens, 64/8 heads), ten 222.
+constexpr int kWarps = 8, kStages = 3;
 
 template <int D, int R> struct Shape {
   static constexpr int HV = D / kDW, TEAMS = kWarps / HV;
@@ -114,15 +118,17 @@ struct Seq {
   __device__ __forceinline__ int block(int i) const { return i < sp ? i : wp + i - sp; }
 };
 
-// A place in the item list.
+// A place in the item list: item i of row group grp of KV head h of sequence b.
 struct Place {
-  int b, u, i;
+  int b, h, grp, i;
   Seq s;
-  __device__ __forceinline__ void next(const Q8Args& A, int units) {
+  __device__ __forceinline__ void next(const Q8Args& A) {
     if (++i < s.items) return;
     i = 0;
-    if (++u < units) return;
-    u = 0;
+    if (++grp < A.groups) return;
+    grp = 0;
+    if (++h < A.Hkv) return;
+    h = 0;
     do {
       if (++b >= A.B) return;
       s.load(A, b);
@@ -179,9 +185,8 @@ struct Rows {
   float o[kDW / 8][4];
 
   // q channels c0 + 16 (t + 4 c) + 4 s .. + 3 are k-step 4 c + s of lane column t.
-  __device__ __forceinline__ void load(const Q8Args& A, int b, int u, const Seq& s, int c0) {
+  __device__ __forceinline__ void load(const Q8Args& A, int b, int h, int grp, const Seq& s, int c0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int h = u / A.groups, grp = u % A.groups;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const int rr = grp * R + 8 * r + g;
@@ -270,15 +275,17 @@ struct Rows {
     }
   }
 
-  // Weight of a score for the sum, and its operand with 2^ev vm the V scale.
-  __device__ __forceinline__ void weigh(int r, float s, float ev, float vm, float& sum, float& w) const {
-    const bool none = m[r] == -INFINITY;
-    const float p = ex2(s - (none ? 0.f : m[r]));
-    sum += p;
-    // at most 2^13: fp32 rounds s + ev - mt of scores beyond 2^24
-    const float x = ex2(fminf(s + (ev - (none ? 0.f : mt[r]) + kOff), kOff + 1.f)) * vm;
-    w = s == -INFINITY ? 0.f : x;
+  // Two scores of a row to their weights for the sum, 2^(s - m), and for the
+  // output, 2^(s + ev - mt + kOff) vm with 2^ev vm the V scale; cm = -m and ct =
+  // ev - mt + kOff of the row. The output's are at most 2^(kOff + 1) (fp32
+  // rounds s + ct of scores beyond 2^24).
+  static __device__ __forceinline__ float2 weigh(float2 s, float cm, float ct, float vm, float2& sum) {
+    const float2 x = f2add(s, f2(cm)), y = f2add(s, f2(ct));
+    sum = f2add(sum, make_float2(ex2(x.x), ex2(x.y)));
+    return f2mul(make_float2(ex2(fminf(y.x, kOff + 1.f)), ex2(fminf(y.y, kOff + 1.f))), f2(vm));
   }
+  // m and mt with 0 for a row that has seen nothing.
+  __device__ __forceinline__ float base(float x) const { return x == -INFINITY ? 0.f : x; }
 
   // This warp's part of the scores of an item's two pages, the second one the
   // first again where the list ends (n = 1): token 8 e + 2 t + j of page p for
@@ -313,9 +320,15 @@ struct Rows {
     for (int p = 0; p < 2; ++p) {
       const float ks = *reinterpret_cast<const float*>((p ? pg1 : pg0) + q8_scales(D));
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int r = 0; r < NR; ++r) {
+        const float k = ks * qs[r];
 #pragma unroll
-        for (int x = 0; x < 2 * NR; ++x) s[8 * (x >> 1) + 4 * p + 2 * e + (x & 1)] = acc[p][e][x] * (ks * qs[x >> 1]);
+        for (int e = 0; e < 2; ++e) {
+          const float2 v = f2mul(make_float2(acc[p][e][2 * r], acc[p][e][2 * r + 1]), f2(k));
+          s[8 * r + 4 * p + 2 * e] = v.x;
+          s[8 * r + 4 * p + 2 * e + 1] = v.y;
+        }
+      }
     }
   }
 
@@ -325,12 +338,13 @@ struct Rows {
     const int lane = threadIdx.x & 31, t = lane & 3;
     float ev[2], vm[2];
     int first[2];
-    bool edge = n < 2;
+    bool edge = n < 2, bad = false;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const uint32_t bits = *reinterpret_cast<const uint32_t*>((p ? pg1 : pg0) + q8_scales(D) + 4);
-      ev[p] = static_cast<float>(static_cast<int>(bits >> 23 & 0xff) - 127);
-      vm[p] = (bits >> 23 & 0xff) == 0xff ? nan_f() : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+      ev[p] = static_cast<float>(static_cast<int>(bits >> 23) - 127);
+      vm[p] = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+      bad = bad || bits >= 0x7f800000u;  // not a scale: the block holds no numbers
       first[p] = p < n ? sq.block(i0 + p) * kPageTokens : 0;
       if (A.window > 0 && first[p] + kPageTokens > A.sinks && first[p] <= sq.L - 1 - A.window) edge = true;
     }
@@ -355,17 +369,22 @@ struct Rows {
     uint32_t hi[2][2][NR], lo[2][2][NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float sum = 0.f;
+      float2 sum = f2(0.f);
+      const float cm = -base(m[r]), ct = kOff - base(mt[r]);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float w0, w1;
-          weigh(r, s[8 * r + 4 * p + 2 * e], ev[p], vm[p], sum, w0);
-          weigh(r, s[8 * r + 4 * p + 2 * e + 1], ev[p], vm[p], sum, w1);
-          split_hi_lo(w0, w1, hi[p][e][r], lo[p][e][r]);
+          const int x = 8 * r + 4 * p + 2 * e;
+          float2 w = weigh(make_float2(s[x], s[x + 1]), cm, ct + ev[p], vm[p], sum);
+          if (bad) {
+            const uint32_t bits = *reinterpret_cast<const uint32_t*>((p ? pg1 : pg0) + q8_scales(D) + 4);
+            if (bits >= 0x7f800000u)  // NaN where it is seen
+              w = make_float2(s[x] == -INFINITY ? 0.f : nan_f(), s[x + 1] == -INFINITY ? 0.f : nan_f());
+          }
+          split_hi_lo2(w, hi[p][e][r], lo[p][e][r]);
         }
-      l[r] += sum;
+      l[r] += sum.x + sum.y;
     }
     // The products of the two pages start from zero and join the output by
     // rounded additions: the tensor cores truncate what they accumulate, which
@@ -462,10 +481,15 @@ struct Rows {
     raise(ms, ms);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float sum = 0.f;
+      float2 sum = f2(0.f);
+      const float cm = -base(m[r]), ct = kOff - base(mt[r]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) weigh(r, w[r][x], 0.f, 1.f, sum, w[r][x]);
-      l[r] += sum;
+      for (int x = 0; x < 4; x += 2) {
+        const float2 v = weigh(make_float2(w[r][x], w[r][x + 1]), cm, ct, 1.f, sum);
+        w[r][x] = v.x;
+        w[r][x + 1] = v.y;
+      }
+      l[r] += sum.x + sum.y;
     }
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
@@ -565,8 +589,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
 
   at.b = start_b[team];
   at.s.load(A, at.b);
-  at.u = static_cast<int>(start_at[team] / at.s.items);
   at.i = static_cast<int>(start_at[team] % at.s.items);
+  at.h = static_cast<int>(start_at[team] / at.s.items) / A.groups;
+  at.grp = static_cast<int>(start_at[team] / at.s.items) % A.groups;
   Place ahead = at;
   const int count = static_cast<int>(x1 - x0);  // items of this team
   unsigned char* ring = smem + team * kStages * S::STAGE;
@@ -574,9 +599,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
 
   // Copies of the next item that none has been asked for into its stage. ids:
   // 32 entries of the block list of sequence ids_b from ids_at on.
-  int ids = 0, ids_b = -1, ids_at = 0, issued = 0;
+  int ids = 0, ids_b = -1, ids_at = 0, issued = 0, issue_st = 0;
   auto issue = [&]() {
-    const int st = issued % kStages;
     if (ahead.i < ahead.s.page_items) {
       const int i = 2 * ahead.i, n = min(2, ahead.s.np - i);
       if (ids_b != ahead.b || ids_at != (i & ~31)) {
@@ -594,17 +618,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
       }
       const int p0 = __shfl_sync(0xffffffffu, ids, i & 31), p1 = __shfl_sync(0xffffffffu, ids, (i + 1) & 31);
       if (lane == 0) {
-        const int h = ahead.u / A.groups;
-        unsigned char* dst = ring + st * S::STAGE;
-        mbar_arrive_expect_tx(bar + st, n * S::PB + A.withhold);
-        bulk_g2s(dst, A.cache + (static_cast<int64_t>(p0) * A.Hkv + h) * S::PB, S::PB, bar + st);
-        if (n == 2) bulk_g2s(dst + S::PB, A.cache + (static_cast<int64_t>(p1) * A.Hkv + h) * S::PB, S::PB, bar + st);
+        unsigned char* dst = ring + issue_st * S::STAGE;
+        mbar_arrive_expect_tx(bar + issue_st, n * S::PB + A.withhold);
+        bulk_g2s(dst, A.cache + (static_cast<int64_t>(p0) * A.Hkv + ahead.h) * S::PB, S::PB, bar + issue_st);
+        if (n == 2)
+          bulk_g2s(dst + S::PB, A.cache + (static_cast<int64_t>(p1) * A.Hkv + ahead.h) * S::PB, S::PB, bar + issue_st);
       }
     } else if (lane == 0) {
-      mbar_arrive_expect_tx(bar + st, 0);  // raw tokens: nothing to copy
+      mbar_arrive_expect_tx(bar + issue_st, 0);  // raw tokens: nothing to copy
     }
-    ++issued;
-    if (issued < count) ahead.next(A, units);
+    if (++issue_st == kStages) issue_st = 0;
+    if (++issued < count) ahead.next(A);
   };
   if (half == 0)
     for (int k = 0; k < min(kStages, count); ++k) issue();
@@ -612,22 +636,30 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
   Rows<D, R> rows;
   bool fresh = true, whole = false;  // whole: the unit's first item was this team's
   int seg_item = 0;                  // the range's item that the segment began with
+  int st = 0;
+  uint32_t parity = 0;
   for (int k = 0; k < count; ++k) {
     if (fresh) {
-      rows.load(A, at.b, at.u, at.s, half * kDW);
+      rows.load(A, at.b, at.h, at.grp, at.s, half * kDW);
       fresh = false;
       whole = at.i == 0;
       seg_item = k;
     }
-    const int st = k % kStages;
-    const bool came = __all_sync(0xffffffffu, mbar_wait_bounded(bar + st, (k / kStages) & 1, A.wait_limit));
+    bool came = mbar_test_phase(bar + st, parity);
+    if (!__all_sync(0xffffffffu, came))
+      came = __all_sync(0xffffffffu, mbar_wait_bounded(bar + st, parity, A.wait_limit));
     const bool paged = at.i < at.s.page_items;
     const int i0 = 2 * at.i, n = min(2, at.s.np - i0);
     const unsigned char* pg0 = ring + st * S::STAGE;
     const unsigned char* pg1 = n == 2 ? pg0 + S::PB : pg0;
-    const int r0 = 16 * (at.i - at.s.page_items), nraw = min(16, at.s.tail - r0);
-    const int64_t raw_at = ((static_cast<int64_t>(at.b) * A.Hkv + at.u / A.groups) * A.tail_cap + r0) * D + half * kDW;
     const bool raw = !paged && A.tail_k && A.tail_v;
+    int r0 = 0, nraw = 0;
+    int64_t raw_at = 0;
+    if (!paged) {
+      r0 = 16 * (at.i - at.s.page_items);
+      nraw = min(16, at.s.tail - r0);
+      raw_at = ((static_cast<int64_t>(at.b) * A.Hkv + at.h) * A.tail_cap + r0) * D + half * kDW;
+    }
     float s[R];
     if (paged)
       rows.template page_scores<CODE>(pg0, pg1, half, s);
@@ -669,12 +701,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
         float l = rows.l[r];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int rr = (at.u % A.groups) * R + 8 * r + g;
+        const int rr = at.grp * R + 8 * r + g;
         float f = 1.f;
         float* dst = nullptr;
         if (last && whole) {
           if (rr < A.G * A.Q) {
-            const int64_t row = (static_cast<int64_t>(at.b) * A.Q + rr / A.G) * A.Hq + at.u / A.groups * A.G + rr % A.G;
+            const int64_t row = (static_cast<int64_t>(at.b) * A.Q + rr / A.G) * A.Hq + at.h * A.G + rr % A.G;
             f = out_factor(rows.m[r], rows.mt[r], l);
             dst = A.out + row * D;
             if (A.lse && t == 0 && half == 0) A.lse[row] = lse_of(rows.m[r], l);
@@ -696,7 +728,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
       }
       fresh = true;
     }
-    if (k + 1 < count) at.next(A, units);
+    if (++st == kStages) {
+      st = 0;
+      parity ^= 1;
+    }
+    if (k + 1 < count) at.next(A);
   }
 }
 

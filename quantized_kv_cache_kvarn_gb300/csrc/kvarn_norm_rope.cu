@@ -14,7 +14,9 @@
 // of its token and the weights of its channels in registers while it walks
 // the heads. The gradient of the weights stays in registers too, is joined
 // over the CTA's groups in a fixed order and leaves as one row per CTA, which
-// a second kernel sums in fp64: no atomics, the same bits every time.
+// a second kernel sums in fp64: no atomics, the same bits every time. The pass
+// forward is bound by HBM (0.85 of the measured copy bandwidth), the one
+// backward by the latency of its two sums at 16 warps an SM (0.56).
 #include <algorithm>
 
 #include "kvarn_launch.h"
@@ -48,23 +50,57 @@ __device__ __forceinline__ int tensor_of(const NormPlan& P, int n) {
   return k;
 }
 
-template <typename T, bool INTERLEAVED, bool BACK>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormParams A,
-                                                             const __grid_constant__ NormPlan P) {
+// Rounds whose vectors are under way to shared memory (32 bytes a lane and
+// round forward, 64 backward), and CTAs per SM that registers leave room for:
+// 4 x 4096 tokens of 72 bf16 heads of 128 take 106 us with three CTAs (80
+// registers) as with two, 118 with four (spills); backward two CTAs of at most
+// 128 registers, two to four rounds under way make no difference (2 x 4093
+// tokens of 28 heads of 256: 94 to 97 us).
+constexpr int kFwdCtas = 3, kFwdDepth = 4, kBackCtas = 2, kBackDepth = 2;
+
+// 16 bytes to shared memory, zeros where there is nothing to read.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// The vector pair of a lane as its pairs' channels, a[e] and b[e].
+template <int N, bool INTERLEAVED>
+__device__ __forceinline__ void to_pairs(const float (&f)[2 * N], float2 (&a)[N / 2], float2 (&b)[N / 2]) {
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    a[e] = INTERLEAVED ? make_float2(f[4 * e], f[4 * e + 2]) : make_float2(f[2 * e], f[2 * e + 1]);
+    b[e] = INTERLEAVED ? make_float2(f[4 * e + 1], f[4 * e + 3]) : make_float2(f[N + 2 * e], f[N + 2 * e + 1]);
+  }
+}
+template <int N, bool INTERLEAVED>
+__device__ __forceinline__ void from_pairs(const float2 (&a)[N / 2], const float2 (&b)[N / 2], float (&f)[2 * N]) {
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    f[INTERLEAVED ? 4 * e : 2 * e] = a[e].x;
+    f[INTERLEAVED ? 4 * e + 2 : 2 * e + 1] = a[e].y;
+    f[INTERLEAVED ? 4 * e + 1 : N + 2 * e] = b[e].x;
+    f[INTERLEAVED ? 4 * e + 3 : N + 2 * e + 1] = b[e].y;
+  }
+}
+
+template <typename T, int LANES, bool INTERLEAVED, bool BACK>
+__global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
+    norm_rope_kernel(const __grid_constant__ NormParams A, const __grid_constant__ NormPlan P) {
   using V = RopeVec<T>;
-  constexpr int N = V::N;
+  constexpr int N = V::N, M = N / 2;
+  constexpr int VECS = BACK ? 4 : 2, DEPTH = BACK ? kBackDepth : kFwdDepth;
   extern __shared__ __align__(16) unsigned char smem[];
-  const int k = tensor_of(P, A.num_tensors), tok = P.tok[k], lanes = P.lanes;
+  const int k = tensor_of(P, A.num_tensors), tok = P.tok[k];
   const NormTensor& t = A.t[k];
   const int pairs = A.rope_dim / 2, chunks = pairs / N, columns = A.dim / (2 * N);
-  uint64_t* frac = reinterpret_cast<uint64_t*>(smem);                     // [pairs]
-  float2* cs = reinterpret_cast<float2*>(smem + 8 * ((pairs + 1) & ~1));  // [tok][pairs]
+  uint4* ring = reinterpret_cast<uint4*>(smem);  // [depth][vector][thread]
+  unsigned char* rest = smem + DEPTH * VECS * kThreads * 16;
+  uint64_t* frac = reinterpret_cast<uint64_t*>(rest);                     // [pairs]
+  float2* cs = reinterpret_cast<float2*>(rest + 8 * ((pairs + 1) & ~1));  // [tok][pairs]
   const int tokens = A.num_seqs * A.num_tokens;  // fits 32 bits
-  const int tid = threadIdx.x, lane = tid & 31;
-  for (int i = tid; i < pairs; i += kThreads) frac[i] = turn_fraction(A.inv_freq[i]);
+  const int tid = threadIdx.x;
 
-  const int c = tid % lanes, tt = tid / lanes % tok, hs = tid / (lanes * tok), slots = kThreads / (lanes * tok);
-  const uint32_t group = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (lane & ~(lanes - 1));
+  const int c = tid % LANES, tt = tid / LANES % tok, hs = tid / (LANES * tok), slots = kThreads / (LANES * tok);
   const bool on = c < columns, turn = c < chunks;
   int first = 0, second = 0;
   if (turn) {
@@ -75,19 +111,88 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     first = j < A.offset ? j : j + A.rope_dim;
     second = j + N < A.offset ? j + N : j + N + A.rope_dim;
   }
-  float w[2 * N], dw[BACK ? 2 * N : 1];
+  // A round is one head of every group's token; the rounds of all the CTA's
+  // tiles are asked for in one sequence, DEPTH ahead, each lane its own
+  // vectors into its own slots: no barrier, and nothing held in registers.
+  const int per = BACK ? P.per[k] : 1;  // forward: one tile
+  const int tile0 = (static_cast<int>(blockIdx.x) - P.cta0[k]) * per;
+  const int rounds = (t.heads + slots - 1) / slots;  // of a tile
+  int ahead_tile = tile0, ahead_left = rounds, ahead_mine = 0, slot = 0;
+  const T* ahead_x = nullptr;
+  const T* ahead_g = nullptr;
+  auto at_tile = [&](int tile) {
+    const int n = tile * tok + tt;
+    ahead_mine = 0;  // rounds in which this lane has a head
+    ahead_x = static_cast<const T*>(t.x);
+    ahead_g = static_cast<const T*>(t.dy);
+    if (tile < tile0 + per && n < tokens && on) {
+      const int seq = n / A.num_tokens, pos_in = n % A.num_tokens;
+      ahead_x += seq * t.x_seq + pos_in * t.x_tok + hs * t.x_head + first;
+      if (BACK) ahead_g += seq * t.g_seq + pos_in * t.g_tok + hs * t.g_head + first;
+      ahead_mine = (t.heads - hs + slots - 1) / slots;
+    }
+  };
+  at_tile(tile0);
+  const int64_t x_step = slots * t.x_head, g_step = slots * t.g_head;
+  const int apart = second - first;
+  auto ask = [&]() {
+    const bool there = ahead_mine > 0;
+    const uint32_t dst = smem_addr(ring + slot * VECS * kThreads + tid);
+    cp_async16_or_zero(dst, ahead_x, there);
+    cp_async16_or_zero(dst + kThreads * 16, there ? ahead_x + apart : ahead_x, there);
+    if constexpr (BACK) {
+      cp_async16_or_zero(dst + 2 * kThreads * 16, ahead_g, there);
+      cp_async16_or_zero(dst + 3 * kThreads * 16, there ? ahead_g + apart : ahead_g, there);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (--ahead_mine > 0) {
+      ahead_x += x_step;
+      if (BACK) ahead_g += g_step;
+    }
+    if (BACK && --ahead_left == 0) {
+      ahead_left = rounds;
+      at_tile(++ahead_tile);
+    }
+  };
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    w[e] = on ? weight_at(t.w, A.wdtype, first + e) + A.weight_offset : 0.f;
-    w[N + e] = on ? weight_at(t.w, A.wdtype, second + e) + A.weight_offset : 0.f;
+  for (int i = 0; i < DEPTH; ++i) {
+    slot = i;
+    ask();
+  }
+  slot = 0;
+  auto take = [&](uint4 (&v)[VECS]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) v[i] = ring[(slot * VECS + i) * kThreads + tid];
+  };
+  // The slot's next round, once its values have gone into a sum.
+  auto refill = [&]() {
+    ask();
+    if (++slot == DEPTH) slot = 0;
+  };
+
+  for (int i = tid; i < pairs; i += kThreads) frac[i] = turn_fraction(A.inv_freq[i]);
+  float2 wa[M], wb[M], da[BACK ? M : 1], db[BACK ? M : 1];  // weights and their gradients by pair
+  {
+    float w[2 * N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      w[e] = on ? weight_at(t.w, A.wdtype, first + e) + A.weight_offset : 0.f;
+      w[N + e] = on ? weight_at(t.w, A.wdtype, second + e) + A.weight_offset : 0.f;
+    }
+    to_pairs<N, INTERLEAVED>(w, wa, wb);
   }
 #pragma unroll
-  for (int e = 0; e < (BACK ? 2 * N : 1); ++e) dw[e] = 0.f;
+  for (int e = 0; e < (BACK ? M : 1); ++e) da[e] = db[e] = f2(0.f);
   const float inv_dim = 1.f / static_cast<float>(A.dim);
   __syncthreads();
+  auto group_sum = [](float s) {
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s;
+  };
 
-  const int tile0 = (static_cast<int>(blockIdx.x) - P.cta0[k]) * P.per[k];
-  for (int tile = tile0; tile < tile0 + P.per[k]; ++tile) {
+  for (int tile = tile0; tile < tile0 + per; ++tile) {
     const int n0 = tile * tok;
     if (n0 >= tokens) break;
     for (int i = tid; i < tok * pairs; i += kThreads) {
@@ -98,116 +203,123 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       }
     }
     __syncthreads();
-    const int n = n0 + tt;
-    if (n < tokens && hs < slots) {
-      const int seq = n / A.num_tokens, pos_in = n % A.num_tokens;
-      float cv[N], sv[N];
+    const int n = min(n0 + tt, tokens - 1);
+    const bool live = on && n0 + tt < tokens;
+    const int seq = n / A.num_tokens, pos_in = n % A.num_tokens;
+    float2 cv[M], sv[M];
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float2 v = turn ? cs[tt * pairs + c * N + e] : make_float2(1.f, 0.f);
-        cv[e] = v.x;
-        sv[e] = v.y;
+    for (int e = 0; e < M; ++e) {
+      const float4 v = turn && live ? *reinterpret_cast<const float4*>(cs + tt * pairs + c * N + 2 * e) : make_float4(1.f, 0.f, 1.f, 0.f);
+      cv[e] = make_float2(v.x, v.z);
+      sv[e] = make_float2(v.y, v.w);
+    }
+    T* dst = static_cast<T*>(t.out) + seq * t.o_seq + pos_in * t.o_tok + hs * t.o_head + first;
+    const int64_t o_step = slots * t.o_head;
+    // Every lane of the CTA makes every round, so that the sums' exchanges are
+    // those of whole warps.
+    if constexpr (!BACK) {
+      // y_a = r (w_a c x_a - w_b s x_b), y_b = r (w_a s x_a + w_b c x_b): the
+      // weights go into the turn's coefficients once per token
+      float2 aa[M], ab[M], ba[M], bb[M];
+#pragma unroll
+      for (int e = 0; e < M; ++e) {
+        aa[e] = f2mul(wa[e], cv[e]);
+        ab[e] = f2mul(wb[e], make_float2(-sv[e].x, -sv[e].y));
+        ba[e] = f2mul(wa[e], sv[e]);
+        bb[e] = f2mul(wb[e], cv[e]);
       }
-      const T* x0 = static_cast<const T*>(t.x) + seq * t.x_seq + pos_in * t.x_tok;
-      const T* g0 = static_cast<const T*>(t.dy) + (BACK ? seq * t.g_seq + pos_in * t.g_tok : 0);
-      T* o0 = static_cast<T*>(t.out) + seq * t.o_seq + pos_in * t.o_tok;
-      auto rotate = [&](const float* f, float* r) {
+      for (int h = hs; h - hs < t.heads; h += slots) {
+        uint4 v[VECS];
+        take(v);
+        float f[2 * N];
+        V::unpack(v[0], f);
+        V::unpack(v[1], f + N);
+        float2 fa[M], fb[M], s2 = f2(0.f);
+        to_pairs<N, INTERLEAVED>(f, fa, fb);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const int a = INTERLEAVED ? 2 * e : e, b = INTERLEAVED ? 2 * e + 1 : N + e;
-          r[a] = fmaf(f[a], cv[e], -f[b] * sv[e]);
-          r[b] = fmaf(f[a], sv[e], f[b] * cv[e]);
+        for (int e = 0; e < M; ++e) s2 = f2fma(fa[e], fa[e], f2fma(fb[e], fb[e], s2));
+        const float2 rs = f2(rsqrtf(fmaf(group_sum(s2.x + s2.y), inv_dim, A.eps)));
+        refill();
+        if (live && h < t.heads) {
+          float2 ya[M], yb[M];
+#pragma unroll
+          for (int e = 0; e < M; ++e) {
+            ya[e] = f2mul(rs, f2fma(fa[e], aa[e], f2mul(fb[e], ab[e])));
+            yb[e] = f2mul(rs, f2fma(fa[e], ba[e], f2mul(fb[e], bb[e])));
+          }
+          from_pairs<N, INTERLEAVED>(ya, yb, f);
+          *reinterpret_cast<uint4*>(dst) = V::pack(f);
+          *reinterpret_cast<uint4*>(dst + apart) = V::pack(f + N);
         }
-      };
-      auto group_sum = [&](float s) {
-        for (int d = 1; d < lanes; d <<= 1) s += __shfl_xor_sync(group, s, d);
-        return s;
-      };
-      if constexpr (!BACK) {
-        constexpr int kBatch = 2;
-        for (int h = hs; h < t.heads; h += kBatch * slots) {
-          uint4 x[kBatch], y[kBatch];
+        dst += o_step;
+      }
+    } else {
+      for (int h = hs; h - hs < t.heads; h += slots) {
+        uint4 v[VECS];
+        const bool here = live && h < t.heads;
+        take(v);
+        float f[2 * N];
+        float2 xa[M], xb[M], ga[M], gb[M], s2 = f2(0.f), q2 = f2(0.f);
+        V::unpack(v[2], f);
+        V::unpack(v[3], f + N);
+        to_pairs<N, INTERLEAVED>(f, xa, xb);
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            x[u] = y[u] = make_uint4(0, 0, 0, 0);
-            const int hh = h + u * slots;
-            if (on && hh < t.heads) {
-              x[u] = *reinterpret_cast<const uint4*>(x0 + hh * t.x_head + first);
-              y[u] = *reinterpret_cast<const uint4*>(x0 + hh * t.x_head + second);
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const int hh = h + u * slots;
-            if (hh >= t.heads) break;
-            float f[2 * N], r[2 * N];
-            V::unpack(x[u], f);
-            V::unpack(y[u], f + N);
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < 2 * N; ++e) s = fmaf(f[e], f[e], s);
-            const float rs = rsqrtf(fmaf(group_sum(s), inv_dim, A.eps));
-#pragma unroll
-            for (int e = 0; e < 2 * N; ++e) f[e] = f[e] * rs * w[e];
-            if (on) {
-              T* dst = o0 + hh * t.o_head;
-              if (turn) rotate(f, r);
-              *reinterpret_cast<uint4*>(dst + first) = V::pack(turn ? r : f);
-              *reinterpret_cast<uint4*>(dst + second) = V::pack(turn ? r + N : f + N);
-            }
-          }
+        for (int e = 0; e < M; ++e) {  // the turn back: sv has its sign
+          ga[e] = f2fma(xa[e], cv[e], f2mul(xb[e], make_float2(-sv[e].x, -sv[e].y)));
+          gb[e] = f2fma(xa[e], sv[e], f2mul(xb[e], cv[e]));
         }
-      } else {
-        for (int h = hs; h < t.heads; h += slots) {
-          uint4 v[4] = {};
-          if (on) {
-            v[0] = *reinterpret_cast<const uint4*>(x0 + h * t.x_head + first);
-            v[1] = *reinterpret_cast<const uint4*>(x0 + h * t.x_head + second);
-            v[2] = *reinterpret_cast<const uint4*>(g0 + h * t.g_head + first);
-            v[3] = *reinterpret_cast<const uint4*>(g0 + h * t.g_head + second);
-          }
-          float f[2 * N], d[2 * N], g[2 * N];
-          V::unpack(v[0], f);
-          V::unpack(v[1], f + N);
-          V::unpack(v[2], d);
-          V::unpack(v[3], d + N);
-          float s = 0.f, q = 0.f;
-          rotate(d, g);
+        V::unpack(v[0], f);
+        V::unpack(v[1], f + N);
+        to_pairs<N, INTERLEAVED>(f, xa, xb);
 #pragma unroll
-          for (int e = 0; e < 2 * N; ++e) {
-            if (!turn) g[e] = d[e];
-            s = fmaf(f[e], f[e], s);
-            q = fmaf(g[e] * w[e], f[e], q);
-          }
-          s = group_sum(s);
-          q = group_sum(q);
-          const float rs = rsqrtf(fmaf(s, inv_dim, A.eps));
-          const float m = q * rs * inv_dim;  // (u . h) / D
-#pragma unroll
-          for (int e = 0; e < 2 * N; ++e) {
-            const float hd = f[e] * rs;
-            dw[e] = fmaf(g[e], hd, dw[e]);
-            f[e] = rs * fmaf(g[e], w[e], -hd * m);
-          }
-          if (on) {
-            T* dst = o0 + h * t.o_head;
-            *reinterpret_cast<uint4*>(dst + first) = V::pack(f);
-            *reinterpret_cast<uint4*>(dst + second) = V::pack(f + N);
-          }
+        for (int e = 0; e < M; ++e) {
+          s2 = f2fma(xa[e], xa[e], f2fma(xb[e], xb[e], s2));
+          q2 = f2fma(f2mul(ga[e], wa[e]), xa[e], f2fma(f2mul(gb[e], wb[e]), xb[e], q2));
         }
+        float ss = s2.x + s2.y, qs = q2.x + q2.y;
+#pragma unroll
+        for (int d = 1; d < LANES; d <<= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, d);
+          qs += __shfl_xor_sync(0xffffffffu, qs, d);
+        }
+        refill();
+        const float root = rsqrtf(fmaf(ss, inv_dim, A.eps));
+        const float rs1 = n0 + tt < tokens && h < t.heads ? root : 0.f;  // no row: nothing, even with eps 0
+        const float m = qs * rs1 * inv_dim;  // (u . h) / D
+        const float2 rs = f2(rs1), mm = f2(-m);
+#pragma unroll
+        for (int e = 0; e < M; ++e) {
+          xa[e] = f2mul(xa[e], rs);
+          xb[e] = f2mul(xb[e], rs);
+          da[e] = f2fma(ga[e], xa[e], da[e]);
+          db[e] = f2fma(gb[e], xb[e], db[e]);
+          xa[e] = f2mul(rs, f2fma(ga[e], wa[e], f2mul(xa[e], mm)));
+          xb[e] = f2mul(rs, f2fma(gb[e], wb[e], f2mul(xb[e], mm)));
+        }
+        if (here) {
+          from_pairs<N, INTERLEAVED>(xa, xb, f);
+          *reinterpret_cast<uint4*>(dst) = V::pack(f);
+          *reinterpret_cast<uint4*>(dst + apart) = V::pack(f + N);
+        }
+        dst += o_step;
       }
     }
     __syncthreads();
   }
   if constexpr (BACK) {
     if (!t.dw) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
     float* rows = reinterpret_cast<float*>(smem);  // [groups][dim]
-    const int groups = kThreads / lanes, g = tid / lanes;
+    constexpr int groups = kThreads / LANES;
+    const int g = tid / LANES;
     if (on) {
+      float f[2 * N];
+      from_pairs<N, INTERLEAVED>(da, db, f);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        rows[g * A.dim + first + e] = dw[e];
-        rows[g * A.dim + second + e] = dw[N + e];
+        rows[g * A.dim + first + e] = f[e];
+        rows[g * A.dim + second + e] = f[N + e];
       }
     }
     __syncthreads();
@@ -303,50 +415,55 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
 }
 
 // Sums of the CTAs' rows: a CTA takes 32 channels of a tensor, its warps every
-// eighth row, in fp64.
-__global__ void __launch_bounds__(256) norm_weight_sum_kernel(const __grid_constant__ NormParams A,
-                                                              const __grid_constant__ NormPlan P) {
-  __shared__ double part[8][32];
-  const int k = blockIdx.y, d = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+// 32nd row, in fp64.
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const __grid_constant__ NormParams A,
+                                                               const __grid_constant__ NormPlan P) {
+  __shared__ double part[32][32];
+  const int k = blockIdx.y, lane = threadIdx.x & 31, d = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
   pdl_wait_primary();
   if (!A.t[k].dw) return;
   double s = 0.;
   if (d < A.dim) {
 #pragma unroll 8
-    for (int i = P.cta0[k] + w; i < P.cta0[k + 1]; i += 8) s += A.parts[static_cast<int64_t>(i) * A.dim + d];
+    for (int i = P.cta0[k] + w; i < P.cta0[k + 1]; i += 32) s += A.parts[static_cast<int64_t>(i) * A.dim + d];
   }
-  part[w][threadIdx.x & 31] = s;
+  part[w][lane] = s;
   __syncthreads();
   if (w == 0 && d < A.dim) {
-    for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) s += part[i][lane];
     A.t[k].dw[d] = static_cast<float>(s);
   }
 }
 
-// CTAs of tensor k. Backward: rows of the weights' gradient, so a CTA takes
-// up to about 64 tokens' worth of heads, fewer where that leaves SMs idle.
+// Tiles and CTAs of every tensor. Forward a CTA takes one tile (several, with
+// their vectors asked for in one sequence, took 122 to 156 us where one takes
+// 106). Backward the CTAs fill the SMs once, shared out by the tensors' work (a
+// tile's rounds and about one more for its cosines and barriers), but none adds
+// up more than 128 rounds.
 NormPlan plan_norm(int num_tensors, const int32_t* heads, int dim, int64_t tokens, int lanes, bool backward) {
   NormPlan P{};
   P.lanes = lanes;
   const int groups = kThreads / lanes;
   const int64_t sms = device_sm_count();
-  int64_t all = 0;
-  for (int k = 0; k < num_tensors; ++k) all += heads[k];
+  int64_t tiles[kRopeMaxTensors], rounds[kRopeMaxTensors], all = 0;
   for (int k = 0; k < num_tensors; ++k) {
     // tokens of a tile: as many as leave each group a head, halved while
     // fewer than four CTAs per SM remain
     int tok = 1;
     while (tok < 8 && tok * 2 <= groups && (tok * heads[k] < groups || (tokens + 2 * tok - 1) / (2 * tok) >= 4 * sms)) tok *= 2;
-    const int64_t tiles = (tokens + tok - 1) / tok;
-    int64_t per = 1;
-    if (backward) {
-      // CTAs in proportion to the heads, about eight per SM over all tensors
-      const int64_t want = std::max<int64_t>(1, 8 * sms * heads[k] / std::max<int64_t>(1, all));
-      per = std::max<int64_t>(1, std::min<int64_t>((tiles + want - 1) / want, std::max(1, 64 / tok)));
-    }
     P.tok[k] = tok;
+    tiles[k] = heads[k] ? (tokens + tok - 1) / tok : 0;
+    rounds[k] = (static_cast<int64_t>(heads[k]) * tok + groups - 1) / groups;
+    all += tiles[k] * (rounds[k] + 1);
+  }
+  for (int k = 0; k < num_tensors; ++k) {
+    int64_t per = 1;
+    if (backward && tiles[k]) {
+      const int64_t want = std::max<int64_t>(1, 2 * sms * tiles[k] * (rounds[k] + 1) / all);
+      per = std::max<int64_t>(1, std::min<int64_t>((tiles[k] + want - 1) / want, 128 / std::max<int64_t>(1, rounds[k])));
+    }
     P.per[k] = static_cast<int32_t>(per);
-    P.cta0[k + 1] = P.cta0[k] + (heads[k] ? static_cast<int32_t>((tiles + per - 1) / per) : 0);
+    P.cta0[k + 1] = P.cta0[k] + static_cast<int32_t>((tiles[k] + per - 1) / per);
   }
   return P;
 }
@@ -355,6 +472,13 @@ int vector_lanes(int dim, int n) {
   int lanes = 4;
   while (lanes * 2 * n < dim) lanes *= 2;
   return lanes;
+}
+
+using NormKernel = void (*)(const NormParams, const NormPlan);
+template <typename T, int LANES>
+NormKernel vector_kernel(bool interleaved, bool backward) {
+  if (interleaved) return backward ? norm_rope_kernel<T, LANES, true, true> : norm_rope_kernel<T, LANES, true, false>;
+  return backward ? norm_rope_kernel<T, LANES, false, true> : norm_rope_kernel<T, LANES, false, false>;
 }
 
 template <typename T>
@@ -385,10 +509,16 @@ cudaError_t launch(const NormParams& A, cudaStream_t st) {
   } else if (vec) {
     int tok = 1;
     for (int k = 0; k < A.num_tensors; ++k) tok = std::max(tok, P.tok[k]);
-    int smem = 8 * ((pairs + 1) & ~1) + 8 * tok * pairs;
+    const int ring = A.backward ? kBackDepth * 4 * kThreads * 16 : kFwdDepth * 2 * kThreads * 16;
+    int smem = ring + 8 * ((pairs + 1) & ~1) + 8 * tok * pairs;
     if (A.backward) smem = std::max(smem, kThreads / P.lanes * A.dim * 4);
-    auto* kernel = A.interleaved ? (A.backward ? norm_rope_kernel<T, true, true> : norm_rope_kernel<T, true, false>)
-                                 : (A.backward ? norm_rope_kernel<T, false, true> : norm_rope_kernel<T, false, false>);
+    auto* kernel = P.lanes == 4    ? vector_kernel<T, 4>(A.interleaved, A.backward)
+                   : P.lanes == 8  ? vector_kernel<T, 8>(A.interleaved, A.backward)
+                   : P.lanes == 16 ? vector_kernel<T, 16>(A.interleaved, A.backward)
+                                   : vector_kernel<T, 32>(A.interleaved, A.backward);
+    // the most that a call may ask for: the ring, 512 fractions, 8 x 512 cosines and sines
+    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + 8 * 512 + 8 * 8 * 512);
+    if (set != cudaSuccess) return set;
     kernel<<<ctas, kThreads, smem, st>>>(A, P);
   } else {
     const int smem = A.backward ? kThreads / 32 * A.dim * 4 : 0;
@@ -399,8 +529,16 @@ cudaError_t launch(const NormParams& A, cudaStream_t st) {
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !sums) return e;
-  norm_weight_sum_kernel<<<dim3((A.dim + 31) / 32, A.num_tensors), 256, 0, st>>>(A, P);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((A.dim + 31) / 32, A.num_tensors);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_weight_sum_kernel, A, P);
 }
 
 }  // namespace

@@ -213,6 +213,17 @@ def test_values_at_the_ends():
     close(y[:, :, fine], want, off)
 
 
+def test_eps_of_zero():
+    """Heads and tokens that do not fill a CTA, with eps 0: rows that are not there bring nothing into the sums."""
+    xs, dys, ws, pos, inv = make(1, 3, (3,), 128, torch.float32, torch.float32, 128, 0, False, 6)
+    dx, dw = torch.empty_like(xs[0]), torch.empty(128, device="cuda")
+    space = torch.empty(kv.norm_rope_backward_workspace_bytes(xs), dtype=torch.uint8, device="cuda")
+    kv.norm_rope_backward(xs[0], dys[0], dx, ws[0], dw, pos, inv, space, eps=0.0)
+    want, ex, want_w, ew = gradients(xs[0], dys[0], ws[0], pos, inv, 0, False, 1.0, 0.0, 0.0)
+    close(dx, want, ex)
+    close(dw, want_w, ew)
+
+
 def test_nothing_to_do():
     inv, _ = kv.rope_frequencies(128)
     for B, S, H in ((0, 3, 2), (2, 0, 2), (2, 3, 0)):

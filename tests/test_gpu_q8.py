@@ -126,7 +126,7 @@ def check(x, out=None, lse=None):
     assert (np.abs(got - want) <= off).all(), (np.abs(got - want) / np.maximum(off, 1e-300)).max()
     fine = np.isfinite(want_lse)
     assert np.array_equal(np.isneginf(got_lse), ~fine)
-    assert (np.abs(got_lse - want_lse)[fine] <= off_lse[fine]).all()
+    assert (np.abs(got_lse[fine] - want_lse[fine]) <= off_lse[fine]).all()
     assert (got[~fine] == 0).all()
 
 

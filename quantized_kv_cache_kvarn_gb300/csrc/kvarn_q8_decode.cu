@@ -295,26 +295,34 @@ struct Rows {
                                               float (&s)[R]) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float acc[2][2][4];
+    // products in turn into four accumulators, so that none waits for the one before
 #pragma unroll
     for (int c = 0; c < kDW / 64; ++c) {
+      uint32_t x[4][4];
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int n = 0; n < 4; ++n) {  // half n & 1 of page n >> 1
+        const uint4 v = *reinterpret_cast<const uint4*>((n >> 1 ? pg1 : pg0) + (8 * (n & 1) + g) * D + half * kDW +
+                                                        16 * ((t + 4 * c) ^ (4 * (g & 1))));
+        x[n][0] = v.x;
+        x[n][1] = v.y;
+        x[n][2] = v.z;
+        x[n][3] = v.w;
+      }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint4 v = *reinterpret_cast<const uint4*>((p ? pg1 : pg0) + (8 * e + g) * D + half * kDW +
-                                                          16 * ((t + 4 * c) ^ (4 * (g & 1))));
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t* a = q[4 * c + k];
+        uint32_t b[4][2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t b0, b1;
-            q8_pairs<CODE>(x[k], b0, b1);
-            const uint32_t* a = q[4 * c + k];
-            if (c == 0 && k == 0)
-              mma_first(acc[p][e], a[0], NR == 2 ? a[2 * NR - 2] : 0u, a[1], NR == 2 ? a[2 * NR - 1] : 0u, b0, b1);
-            else
-              mma_f16(acc[p][e], a[0], NR == 2 ? a[2 * NR - 2] : 0u, a[1], NR == 2 ? a[2 * NR - 1] : 0u, b0, b1);
-          }
+        for (int n = 0; n < 4; ++n) q8_pairs<CODE>(x[n][k], b[n][0], b[n][1]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          float* to = acc[n >> 1][n & 1];
+          if (c == 0 && k == 0)
+            mma_first(to, a[0], NR == 2 ? a[2 * NR - 2] : 0u, a[1], NR == 2 ? a[2 * NR - 1] : 0u, b[n][0], b[n][1]);
+          else
+            mma_f16(to, a[0], NR == 2 ? a[2 * NR - 2] : 0u, a[1], NR == 2 ? a[2 * NR - 1] : 0u, b[n][0], b[n][1]);
         }
+      }
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
@@ -400,48 +408,60 @@ struct Rows {
         x[p][2] = v.z;
         x[p][3] = v.w;
       }
+      float d[4][4];
+      uint32_t b[4][2][2];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float* to = o[4 * w + k];
-        uint32_t b[2][2];
-        q8_pairs<CODE>(x[0][k], b[0][0], b[0][1]);
-        q8_pairs<CODE>(x[1][k], b[1][0], b[1][1]);
-        float d[4];
-        if constexpr (NR == 1) {
-          mma_first(d, hi[0][0][0], lo[0][0][0], hi[0][1][0], lo[0][1][0], b[0][0], b[0][1]);
-          mma_f16(d, hi[1][0][0], lo[1][0][0], hi[1][1][0], lo[1][1][0], b[1][0], b[1][1]);
-        } else {
-          mma_first(d, lo[0][0][0], lo[0][0][NR - 1], lo[0][1][0], lo[0][1][NR - 1], b[0][0], b[0][1]);
-          mma_f16(d, lo[1][0][0], lo[1][0][NR - 1], lo[1][1][0], lo[1][1][NR - 1], b[1][0], b[1][1]);
+        q8_pairs<CODE>(x[0][k], b[k][0][0], b[k][0][1]);
+        q8_pairs<CODE>(x[1][k], b[k][1][0], b[k][1][1]);
+      }
+      // four accumulators in turn
+      if constexpr (NR == 1) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-            mma_f16(d, hi[p][0][0], hi[p][0][NR - 1], hi[p][1][0], hi[p][1][NR - 1], b[p][0], b[p][1]);
-        }
+        for (int k = 0; k < 4; ++k) mma_first(d[k], hi[0][0][0], lo[0][0][0], hi[0][1][0], lo[0][1][0], b[k][0][0], b[k][0][1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_f16(d[k], hi[1][0][0], lo[1][0][0], hi[1][1][0], lo[1][1][0], b[k][1][0], b[k][1][1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_first(d[k], lo[0][0][0], lo[0][0][NR - 1], lo[0][1][0], lo[0][1][NR - 1], b[k][0][0], b[k][0][1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f16(d[k], lo[1][0][0], lo[1][0][NR - 1], lo[1][1][0], lo[1][1][NR - 1], b[k][1][0], b[k][1][1]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16(d[k], hi[p][0][0], hi[p][0][NR - 1], hi[p][1][0], hi[p][1][NR - 1], b[k][p][0], b[k][p][1]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float2 v = f2add(make_float2(to[i], to[i + 1]), make_float2(d[i], d[i + 1]));
-          to[i] = v.x;
-          to[i + 1] = v.y;
+          float* to = o[4 * w + k] + i;
+          const float2 v = f2add(make_float2(to[0], to[1]), make_float2(d[k][i], d[k][i + 1]));
+          to[0] = v.x;
+          to[1] = v.y;
         }
-      }
     }
   }
 
-  // Raw tokens of the tail in fp32, n <= 16 rows from K on: token 8 e + 2 t + j
-  // for row r at s[8 r + 2 e + j].
+  // Raw tokens of the tail in fp32, n <= 16 rows of the stage: token 8 e + 2 t +
+  // j for row r at s[8 r + 2 e + j]; four tokens at a time (rows behind the n-th
+  // are hidden afterwards).
   __device__ __forceinline__ void raw_scores(const Q8Args& A, const uint16_t* K, int n, float (&s)[R]) const {
     const int t = threadIdx.x & 3;
 #pragma unroll
     for (int x = 0; x < R; ++x) s[x] = 0.f;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
+#pragma unroll 4
+    for (int i = 0; i < ((n + 3) & ~3); ++i) {
       float d[NR];
 #pragma unroll
       for (int r = 0; r < NR; ++r) d[r] = 0.f;
 #pragma unroll
       for (int c = 0; c < kDW / 64; ++c) {
         float f[16];
-        raw16(K + static_cast<int64_t>(i) * D + 16 * (t + 4 * c), A.bf16, f);
+        raw16(K + i * D + 16 * (t + 4 * c), A.bf16, f);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -491,7 +511,7 @@ struct Rows {
       }
       l[r] += sum.x + sum.y;
     }
-#pragma unroll 1
+#pragma unroll 2
     for (int i = 0; i < n; ++i) {
       const int x = 2 * (i >> 3) + (i & 1), from = (lane & 28) | (i & 7) >> 1;
       float wi[NR];
@@ -500,7 +520,7 @@ struct Rows {
         const float v = x == 0 ? w[r][0] : x == 1 ? w[r][1] : x == 2 ? w[r][2] : w[r][3];
         wi[r] = __shfl_sync(0xffffffffu, v, from);
       }
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(V + static_cast<int64_t>(i) * D) + t;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(V + i * D) + t;
 #pragma unroll
       for (int c = 0; c < kDW / 8; ++c) {
         float f[4];
@@ -599,6 +619,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
 
   // Copies of the next item that none has been asked for into its stage. ids:
   // 32 entries of the block list of sequence ids_b from ids_at on.
+  const bool has_tail = A.tail_k && A.tail_v;
   int ids = 0, ids_b = -1, ids_at = 0, issued = 0, issue_st = 0;
   auto issue = [&]() {
     if (ahead.i < ahead.s.page_items) {
@@ -624,8 +645,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
         if (n == 2)
           bulk_g2s(dst + S::PB, A.cache + (static_cast<int64_t>(p1) * A.Hkv + ahead.h) * S::PB, S::PB, bar + issue_st);
       }
-    } else if (lane == 0) {
-      mbar_arrive_expect_tx(bar + issue_st, 0);  // raw tokens: nothing to copy
+    } else if (lane == 0) {  // raw tokens: their key rows, then at 16 rows their value rows
+      const int r0 = 16 * (ahead.i - ahead.s.page_items), bytes = has_tail ? min(16, ahead.s.tail - r0) * 2 * D : 0;
+      mbar_arrive_expect_tx(bar + issue_st, 2 * bytes + (bytes ? A.withhold : 0));
+      if (bytes) {
+        unsigned char* dst = ring + issue_st * S::STAGE;
+        const int64_t from = ((static_cast<int64_t>(ahead.b) * A.Hkv + ahead.h) * A.tail_cap + r0) * D;
+        bulk_g2s(dst, static_cast<const uint16_t*>(A.tail_k) + from, bytes, bar + issue_st);
+        bulk_g2s(dst + 32 * D, static_cast<const uint16_t*>(A.tail_v) + from, bytes, bar + issue_st);
+      }
     }
     if (++issue_st == kStages) issue_st = 0;
     if (++issued < count) ahead.next(A);
@@ -652,19 +680,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
     const int i0 = 2 * at.i, n = min(2, at.s.np - i0);
     const unsigned char* pg0 = ring + st * S::STAGE;
     const unsigned char* pg1 = n == 2 ? pg0 + S::PB : pg0;
-    const bool raw = !paged && A.tail_k && A.tail_v;
+    const bool raw = !paged && has_tail;
     int r0 = 0, nraw = 0;
-    int64_t raw_at = 0;
     if (!paged) {
       r0 = 16 * (at.i - at.s.page_items);
       nraw = min(16, at.s.tail - r0);
-      raw_at = ((static_cast<int64_t>(at.b) * A.Hkv + at.h) * A.tail_cap + r0) * D + half * kDW;
     }
     float s[R];
     if (paged)
       rows.template page_scores<CODE>(pg0, pg1, half, s);
     else if (raw)
-      rows.raw_scores(A, static_cast<const uint16_t*>(A.tail_k) + raw_at, nraw, s);
+      rows.raw_scores(A, reinterpret_cast<const uint16_t*>(pg0) + half * kDW, nraw, s);
     bool dead = !came;
     if constexpr (HV == 2) {
       float* mine = reinterpret_cast<float*>(smem + S::XCHG + team * S::XBUF) + ((k & 1) * 2 + half) * S::XLANE * 32;
@@ -690,7 +716,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
     if (paged)
       rows.template add_pages<CODE>(A, pg0, pg1, half, at.s, i0, n, s);
     else if (raw)
-      rows.add_raw(A, static_cast<const uint16_t*>(A.tail_v) + raw_at, at.s.C * kPageTokens + r0, nraw, s);
+      rows.add_raw(A, reinterpret_cast<const uint16_t*>(pg0 + 32 * D) + half * kDW, at.s.C * kPageTokens + r0, nraw, s);
     __syncwarp();
     if (HV == 1 && issued < count) issue();
     const bool last = at.i + 1 == at.s.items;

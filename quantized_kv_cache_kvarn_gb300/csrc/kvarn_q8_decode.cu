@@ -96,6 +96,12 @@ template <int D, int R> struct Shape {
 // Floats of a partial row: m, l, mt, pad, output.
 __host__ __device__ constexpr int part_row(int D) { return D + 4; }
 
+// a / b of non-negative numbers, by the short division where both fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // What a sequence's queries see: blocks [0, sp) and [wp, C) of C whole ones,
 // then `tail` raw tokens.
 struct Seq {
@@ -143,6 +149,14 @@ __device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1, ui
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// x as fp16 hi + lo, saturated: fp32 rounds s + ev - mt of scores beyond 2^24,
+// and 2^(kOff + 1) may be passed by more than fp16 holds.
+__device__ __forceinline__ void split_sat(float2 x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %2, %1;" : "=r"(hi) : "f"(x.x), "f"(x.y));
+  const float2 r = f2fma(__half22float2(u32_as_h2(hi)), f2(-1.f), x);
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %2, %1;" : "=r"(lo) : "f"(r.x), "f"(r.y));
 }
 
 __device__ __forceinline__ float ex2(float x) { return fast_exp2(x); }
@@ -277,12 +291,11 @@ struct Rows {
 
   // Two scores of a row to their weights for the sum, 2^(s - m), and for the
   // output, 2^(s + ev - mt + kOff) vm with 2^ev vm the V scale; cm = -m and ct =
-  // ev - mt + kOff of the row. The output's are at most 2^(kOff + 1) (fp32
-  // rounds s + ct of scores beyond 2^24).
+  // ev - mt + kOff of the row. The output's are below 2^(kOff + 1).
   static __device__ __forceinline__ float2 weigh(float2 s, float cm, float ct, float vm, float2& sum) {
     const float2 x = f2add(s, f2(cm)), y = f2add(s, f2(ct));
     sum = f2add(sum, make_float2(ex2(x.x), ex2(x.y)));
-    return f2mul(make_float2(ex2(fminf(y.x, kOff + 1.f)), ex2(fminf(y.y, kOff + 1.f))), f2(vm));
+    return f2mul(make_float2(ex2(y.x), ex2(y.y)), f2(vm));
   }
   // m and mt with 0 for a row that has seen nothing.
   __device__ __forceinline__ float base(float x) const { return x == -INFINITY ? 0.f : x; }
@@ -346,13 +359,13 @@ struct Rows {
     const int lane = threadIdx.x & 31, t = lane & 3;
     float ev[2], vm[2];
     int first[2];
-    bool edge = n < 2, bad = false;
+    bool edge = n < 2, bad[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const uint32_t bits = *reinterpret_cast<const uint32_t*>((p ? pg1 : pg0) + q8_scales(D) + 4);
       ev[p] = static_cast<float>(static_cast<int>(bits >> 23) - 127);
-      vm[p] = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-      bad = bad || bits >= 0x7f800000u;  // not a scale: the block holds no numbers
+      bad[p] = bits >= 0x7f800000u;  // not a scale: the block reads as NaN
+      vm[p] = bad[p] ? nan_f() : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
       first[p] = p < n ? sq.block(i0 + p) * kPageTokens : 0;
       if (A.window > 0 && first[p] + kPageTokens > A.sinks && first[p] <= sq.L - 1 - A.window) edge = true;
     }
@@ -374,7 +387,7 @@ struct Rows {
       mts[r] = fmaxf(top[0] + ev[0], top[1] + ev[1]);
     }
     raise(ms, mts);
-    uint32_t hi[2][2][NR], lo[2][2][NR];
+    float2 w[NR][2][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       float2 sum = f2(0.f);
@@ -384,16 +397,24 @@ struct Rows {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int x = 8 * r + 4 * p + 2 * e;
-          float2 w = weigh(make_float2(s[x], s[x + 1]), cm, ct + ev[p], vm[p], sum);
-          if (bad) {
-            const uint32_t bits = *reinterpret_cast<const uint32_t*>((p ? pg1 : pg0) + q8_scales(D) + 4);
-            if (bits >= 0x7f800000u)  // NaN where it is seen
-              w = make_float2(s[x] == -INFINITY ? 0.f : nan_f(), s[x + 1] == -INFINITY ? 0.f : nan_f());
-          }
-          split_hi_lo2(w, hi[p][e][r], lo[p][e][r]);
+          w[r][p][e] = weigh(make_float2(s[x], s[x + 1]), cm, ct + ev[p], vm[p], sum);
         }
       l[r] += sum.x + sum.y;
     }
+    if (edge && (bad[0] || bad[1])) {  // 0 times NaN where a token is hidden
+#pragma unroll
+      for (int x = 0; x < R; x += 2) {
+        float2& v = w[x >> 3][x >> 2 & 1][x >> 1 & 1];
+        v = make_float2(s[x] == -INFINITY ? 0.f : v.x, s[x + 1] == -INFINITY ? 0.f : v.y);
+      }
+    }
+    uint32_t hi[2][2][NR], lo[2][2][NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) split_sat(w[r][p][e], hi[p][e][r], lo[p][e][r]);
     // The products of the two pages start from zero and join the output by
     // rounded additions: the tensor cores truncate what they accumulate, which
     // over thousands of tokens adds up to 4e-6 where this leaves 6e-7.
@@ -548,7 +569,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
   constexpr int W = kWarps, HV = S::HV, TEAMS = S::TEAMS, ROW = part_row(D);
   extern __shared__ __align__(128) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
-  __shared__ int64_t sum_of[W], start_at[TEAMS], total_sh;
+  __shared__ int64_t sum_of[W], range_at[TEAMS], start_at[TEAMS];
   __shared__ int start_b[TEAMS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < TEAMS * kStages) mbar_init(bars + tid, 1);
@@ -579,20 +600,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
   if (lane == 31) sum_of[warp] = before;
   before -= mine;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) before += sum_of[w];
-  if (tid == 32 * W - 1) total_sh = before + mine;
-  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += sum_of[w];
+    total += sum_of[w];
+  }
   // Range e of as many as there are teams (warps, or pairs of them), at most
   // one per item, is that of team e / grid of CTA e % grid: few items spread
   // over the SMs.
-  const int64_t total = total_sh, teams = min(total, static_cast<int64_t>(gridDim.x) * TEAMS);
+  const int64_t teams = min(total, static_cast<int64_t>(gridDim.x) * TEAMS);
   auto range_of = [&](int w) { return static_cast<int64_t>(w) * gridDim.x + blockIdx.x; };
+  if (tid < TEAMS) range_at[tid] = range_of(tid) < teams ? quotient(range_of(tid) * total, teams) : -1;
+  __syncthreads();
   for (int b = b0; b < b1; ++b) {
     if (blockIdx.x == 0) A.offs[b] = before;
     at.s.load(A, b);
     const int64_t n = static_cast<int64_t>(at.s.items) * units;
     for (int w = 0; w < TEAMS; ++w) {
-      const int64_t e = range_of(w), x = e < teams ? e * total / teams : -1;
+      const int64_t x = range_at[w];
       if (x >= before && x < before + n) {
         start_b[w] = b;
         start_at[w] = x - before;
@@ -605,13 +630,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
   const int team = warp / HV, half = warp % HV;
   const int64_t range = range_of(team);
   if (range >= teams) return;
-  const int64_t x0 = range * total / teams, x1 = (range + 1) * total / teams;
+  const int64_t x0 = range_at[team], x1 = quotient((range + 1) * total, teams);
 
   at.b = start_b[team];
   at.s.load(A, at.b);
-  at.i = static_cast<int>(start_at[team] % at.s.items);
-  at.h = static_cast<int>(start_at[team] / at.s.items) / A.groups;
-  at.grp = static_cast<int>(start_at[team] / at.s.items) % A.groups;
+  const int unit = static_cast<int>(quotient(start_at[team], at.s.items));
+  at.i = static_cast<int>(start_at[team] - static_cast<int64_t>(unit) * at.s.items);
+  at.h = unit / A.groups;
+  at.grp = unit % A.groups;
   Place ahead = at;
   const int count = static_cast<int>(x1 - x0);  // items of this team
   unsigned char* ring = smem + team * kStages * S::STAGE;
@@ -770,12 +796,12 @@ __global__ void __launch_bounds__(128) q8_merge_kernel(const __grid_constant__ Q
   pdl_wait_primary();
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t b = row / (static_cast<int64_t>(A.Q) * A.Hq);
-  if (b >= A.B) return;
-  const int j = static_cast<int>(row / A.Hq % A.Q), hq = static_cast<int>(row % A.Hq);
+  if (row >= static_cast<int64_t>(A.B) * A.Q * A.Hq) return;
+  const int at = static_cast<int>(row) / A.Hq, hq = static_cast<int>(row) % A.Hq;  // at most 2^30 rows
+  const int b = at / A.Q, j = at % A.Q;
   const int h = hq / A.G, rr = j * A.G + hq % A.G, units = A.Hkv * A.groups;
   const int64_t o0 = A.offs[b], o1 = A.offs[b + 1], total = A.offs[A.B];
-  const int64_t items = (o1 - o0) / units, teams = min(total, grid_teams);
+  const int64_t items = quotient(o1 - o0, units), teams = min(total, grid_teams);
   float* dst = A.out + row * D + lane * E;
   float acc[E];
 #pragma unroll
@@ -784,9 +810,9 @@ __global__ void __launch_bounds__(128) q8_merge_kernel(const __grid_constant__ Q
   if (items > 0) {
     const int64_t p0 = o0 + (static_cast<int64_t>(h) * A.groups + rr / R) * items, p1 = p0 + items;
     // the range of item x is the last that begins at or before it
-    const int64_t w0 = ((p0 + 1) * teams - 1) / total, w1 = (p1 * teams - 1) / total;
+    const int64_t w0 = quotient((p0 + 1) * teams - 1, total), w1 = quotient(p1 * teams - 1, total);
     if (w0 == w1) return;
-    const bool inside = w0 * total / teams < p0;  // the first range begins before the unit
+    const bool inside = quotient(w0 * total, teams) < p0;  // the first range begins before the unit
     const int n = static_cast<int>(w1 - w0 + 1);
     const float* part = A.part + (2 * w0 * R + rr % R) * ROW;
     auto slot = [&](int i) { return part + static_cast<int64_t>(2 * i + (i == 0 && inside ? 1 : 0)) * R * ROW; };
@@ -823,6 +849,9 @@ __global__ void __launch_bounds__(128) q8_merge_kernel(const __grid_constant__ Q
   if (A.lse && lane == 0) A.lse[row] = lse_of(M, L);
 }
 
+// Sixteen rows to a group wherever there are more than eight: 12 rows at
+// head_dim 256 behind a window take 92 us as one group of sixteen, 125 as two
+// of eight, 18 rows 143 as two and 166 as three, 16 rows at 128 143 and 205.
 int rows_per_group(int rows) { return rows > 8 ? 16 : 8; }
 
 template <int D, int R, int CODE>

@@ -628,40 +628,50 @@ def _norm_rope(what, xs, dys, outs, weights, dweights, positions, inv_freq, work
     if x0.dim() != 4 or code < 0:
         _refuse(what, f"tensors must be float16, bfloat16 or float32 [seqs, tokens, heads, head_dim], not {dtype} "
                       f"{tuple(x0.shape)}")
-    B, S, _, D = x0.shape
+    shape0 = x0.shape
+    B, S, _, D = shape0
     dev = _device_of(what, *xs, *outs, *weights, *dweights, *(dys or ()), positions, inv_freq, workspace)
-    wtype = next((w.dtype for w in weights if w is not None), torch.float32)
-    wcode = ROPE_DTYPES.get(wtype, -1)
+    vector, wtype, wcode = (D,), None, 2
     rows = []
-    for x, y, dy, w, dw in zip(xs, outs, dys or (None,) * n, weights, dweights):
+    for k in range(n):
+        x, y, w, dw = xs[k], outs[k], weights[k], dweights[k]
         shape, strides, ostrides = x.shape, x.stride(), y.stride()
         if len(shape) != 4 or y.shape != shape or x.dtype is not dtype or y.dtype is not dtype:
             _refuse(what, "tensors must share their type, and each output its tensor's shape")
         b, t, heads, dim = shape
         if b != B or t != S or dim != D:
             _refuse(what, "tensors must share sequences, tokens and head_dim")
-        if D > 1 and (strides[3] != 1 or ostrides[3] != 1):
+        xb, xt, xh, xe = strides
+        yb, yt, yh, ye = ostrides
+        if (xe != 1 or ye != 1) and D > 1:
             _refuse(what, "the channels of a head must be contiguous")
-        yb, yt, yh, _ = ostrides
         if (yb == 0 and B > 1) or (yt == 0 and S > 1) or (yh == 0 and heads > 1):
             _refuse(what, "an output may not be broadcast")
-        gs = (0, 0, 0)
-        if dy is not None:
+        gp = gb = gt = gh = wp = dwp = 0
+        if dys is not None:
+            dy = dys[k]
+            gb, gt, gh, ge = dy.stride() if dy.dim() == 4 else (0, 0, 0, 0)
             if dy.shape != shape or dy.dtype is not dtype:
                 _refuse(what, "each gradient must have its tensor's type and shape")
-            gs = dy.stride()
-            if D > 1 and gs[3] != 1:
+            if ge != 1 and D > 1:
                 _refuse(what, "the channels of a head must be contiguous")
-        if w is not None and (w.dtype is not wtype or wcode < 0 or w.shape != (D,) or not w.is_contiguous()):
-            _refuse(what, f"weights must be contiguous vectors of {D}, float16, bfloat16 or float32, of one type")
-        if dw is not None and (dw.dtype is not torch.float32 or dw.shape != (D,) or not dw.is_contiguous()):
-            _refuse(what, f"gradients of weights must be contiguous float32 vectors of {D}")
-        rows += (x.data_ptr(), _addr(dy), y.data_ptr(), _addr(w), _addr(dw), strides[0], strides[1], strides[2], gs[0], gs[1],
-                 gs[2], yb, yt, yh, heads, 0)
-    pos, pos_stride, freq, rope_dim = 0, 0, 0, 0
+            gp = dy.data_ptr()
+        if w is not None:
+            if wtype is None:
+                wtype = w.dtype
+                wcode = ROPE_DTYPES.get(wtype, -1)
+            if w.dtype is not wtype or wcode < 0 or w.shape != vector or not w.is_contiguous():
+                _refuse(what, f"weights must be contiguous vectors of {D}, float16, bfloat16 or float32, of one type")
+            wp = w.data_ptr()
+        if dw is not None:
+            if dw.dtype is not torch.float32 or dw.shape != vector or not dw.is_contiguous():
+                _refuse(what, f"gradients of weights must be contiguous float32 vectors of {D}")
+            dwp = dw.data_ptr()
+        rows += (x.data_ptr(), gp, y.data_ptr(), wp, dwp, xb, xt, xh, gb, gt, gh, yb, yt, yh, heads, 0)
+    pos = pos_stride = freq = rope_dim = 0
     if inv_freq is not None:
         shape = positions.shape
-        pb, ps = positions.stride() if positions.dim() == 2 else (0, 0)
+        pb, ps = positions.stride() if len(shape) == 2 else (0, 0)
         if positions.dtype is not torch.int32 or not (shape == (B, S) or shape == (1, S)) or (ps != 1 and S > 1):
             _refuse(what, "positions must be int32 [seqs or 1, tokens], rows contiguous")
         if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
@@ -836,6 +846,11 @@ def q8_page_bytes(layout: Layout) -> int:
     return n
 
 
+def _q8_page(layout):
+    """q8_page_bytes of a layout that the call itself will check."""
+    return 32 * layout.head_dim + 32
+
+
 def alloc_q8_cache(layout: Layout, device=None) -> torch.Tensor:
     return torch.zeros((layout.num_pages, layout.num_kv_heads, q8_page_bytes(layout)), dtype=torch.uint8,
                        device=device or "cuda")
@@ -870,7 +885,7 @@ def _q8_blocks(what, call, k, v, layout, code, block_start, block_table, cache, 
     if call is lib().kvarn_q8_read_blocks and 0 in ((1 if n <= 1 else s) for n, s in zip(k.shape, (sb, sh, st, se))):
         _refuse(what, "an output may not be broadcast")
     dev = _device_of(what, k, v, block_start, block_table, cache, err)
-    _cache_bytes(what, cache, layout, q8_page_bytes(layout))
+    _cache_bytes(what, cache, layout, _q8_page(layout))
     bt_stride = _row_stride(what, "block_table", block_table, torch.int32, B)
     if block_table.shape[1] != bt_stride:  # entries between the rows are nobody's
         _refuse(what, "the rows of block_table must be contiguous to each other")
@@ -900,15 +915,17 @@ def q8_append(k, v, layout: Layout, code, seq_lens, max_seq_len, tail_k, tail_v,
     what = "q8_append"
     kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
     B, H, D = seq_lens.shape[0], layout.num_kv_heads, layout.head_dim
+    shape = (B, H, D)
     for t in (k, v):
-        if t.dtype is not kv_dtype or t.shape != (B, H, D) or not t.is_contiguous():
-            _refuse(what, f"k and v must be contiguous {kv_dtype} of shape {(B, H, D)}")
+        if t.dtype is not kv_dtype or t.shape != shape or not t.is_contiguous():
+            _refuse(what, f"k and v must be contiguous {kv_dtype} of shape {shape}")
     cap = tail_k.shape[2] if tail_k.dim() == 4 else 0
+    shape = (B, H, cap, D)
     for t in (tail_k, tail_v):
-        if t.dtype is not kv_dtype or t.shape != (B, H, cap, D) or not t.is_contiguous():
+        if t.dtype is not kv_dtype or t.shape != shape or not t.is_contiguous():
             _refuse(what, f"tail_k and tail_v must be contiguous {kv_dtype} of shape {(B, H, 'capacity', D)}")
     dev = _device_of(what, k, v, seq_lens, tail_k, tail_v, block_table, cache, err)
-    _cache_bytes(what, cache, layout, q8_page_bytes(layout))
+    _cache_bytes(what, cache, layout, _q8_page(layout))
     bt_stride = _row_stride(what, "block_table", block_table, torch.int32, B)
     if block_table.shape[1] < max_seq_len // 16:
         _refuse(what, "block_table has fewer columns than max_seq_len has blocks")
@@ -941,7 +958,7 @@ def q8_decode(q, layout: Layout, code, cache, block_table, seq_lens, max_seq_len
     cap = tail_k.shape[2] if tail_k is not None and tail_k.dim() == 4 else Q + 14
     dev = _device_of(what, q, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse)
     bt_stride = _decode_tensors(what, q, layout, cache, block_table, seq_lens, out, workspace, err, tail_k, tail_v, lse, cap,
-                                max(0, max_seq_len - Q + 1) // 16, q8_page_bytes(layout))
+                                max(0, max_seq_len - Q + 1) // 16, _q8_page(layout))
     _check(lib().kvarn_q8_decode(q.data_ptr(), Hq, Q, sm_scale, cache.data_ptr(), ctypes.byref(layout), code,
                                  block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), max_seq_len, _addr(tail_k),
                                  _addr(tail_v), cap, window, sink_tokens, B, out.data_ptr(), _addr(lse),
@@ -951,6 +968,9 @@ def q8_decode(q, layout: Layout, code, cache, block_table, seq_lens, max_seq_len
 
 # ------------------------------------------------------ pages of a cache
 # Sequences that fork, end and leave their windows; compaction.
+
+_FORK_TAILS = [(ForkTail * max(1, n), struct.Struct("@" + "PPqiiii" * n)) for n in range(5)]
+
 
 def fork_sequences(parents, seq_lens, block_table, page_refs, layout: Layout, max_seq_len, seq_lens_out, block_table_out,
                    page_refs_out, freed, freed_count, err, *, tails=(), sinks=(), recent_tokens=0, window=0, sink_tokens=0,
@@ -970,7 +990,8 @@ def fork_sequences(parents, seq_lens, block_table, page_refs, layout: Layout, ma
         _refuse(what, "at most four tails and sinks")
     dev = _device_of(what, parents, seq_lens, block_table, page_refs, seq_lens_out, block_table_out, page_refs_out, freed,
                      freed_count, err, *(t for p in pairs for t in p[:2]))
-    entries = max_seq_len // layout.tile_tokens * (layout.tile_tokens // 16)
+    tile, pages = layout.tile_tokens, layout.num_pages
+    entries = max_seq_len // tile * (tile // 16) if tile > 0 else 0
     rows = _row_stride(what, "block_table", block_table, torch.int32, n_in)
     out_rows = _row_stride(what, "block_table_out", block_table_out, torch.int32, n_out)
     if block_table.shape[1] < entries or block_table_out.shape[1] < entries:
@@ -978,17 +999,19 @@ def fork_sequences(parents, seq_lens, block_table, page_refs, layout: Layout, ma
     if n_in > 1 and n_out > 1 and rows != out_rows:
         _refuse(what, "block_table and block_table_out differ in row stride")
     for name, t, n in (("parents", parents, n_out), ("seq_lens", seq_lens, n_in), ("seq_lens_out", seq_lens_out, n_out),
-                       ("page_refs", page_refs, layout.num_pages), ("page_refs_out", page_refs_out, layout.num_pages),
-                       ("freed", freed, layout.num_pages), ("freed_count", freed_count, 1)):
+                       ("page_refs", page_refs, pages), ("page_refs_out", page_refs_out, pages), ("freed", freed, pages),
+                       ("freed_count", freed_count, 1)):
         _int_vector(what, name, t, n)
     _err_word(what, err)
-    array = (ForkTail * max(1, len(pairs)))()
-    for k, (old, new, whole) in enumerate(pairs):
-        if (old.dim() != 4 or new.dim() != 4 or old.dtype is not new.dtype or old.shape[1:] != new.shape[1:]
-                or old.shape[0] != n_in or new.shape[0] != n_out or not old.is_contiguous() or not new.is_contiguous()):
+    values = []
+    for old, new, whole in pairs:
+        shape, shape2 = old.shape, new.shape
+        if (len(shape) != 4 or old.dtype is not new.dtype or shape[1:] != shape2[1:] or shape[0] != n_in or shape2[0] != n_out
+                or not old.is_contiguous() or not new.is_contiguous()):
             _refuse(what, "tails must be contiguous [rows, heads, capacity, channels], old and new of one type and shape")
-        array[k] = ForkTail(old.data_ptr(), new.data_ptr(), old.shape[3] * old.element_size(), old.shape[1], old.shape[2],
-                            whole, 0)
+        values += (old.data_ptr(), new.data_ptr(), shape[3] * old.element_size(), shape[1], shape[2], whole, 0)
+    array, packer = _FORK_TAILS[len(pairs)]
+    array = array.from_buffer_copy(packer.pack(*values)) if pairs else None
     _check(lib().kvarn_fork_sequences(parents.data_ptr(), n_in, n_out, seq_lens.data_ptr(), seq_lens_out.data_ptr(),
                                       max_seq_len, block_table.data_ptr(), block_table_out.data_ptr(),
                                       rows if n_in > 1 else out_rows if n_out > 1 else entries, page_refs.data_ptr(),

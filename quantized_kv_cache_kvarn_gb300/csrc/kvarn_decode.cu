@@ -30,10 +30,13 @@ int copy_withhold() { return g_copy_withhold.load(std::memory_order_relaxed); }
 
 // ------------------------------------------------------------- planning
 int device_sm_count() {
+  static std::atomic<int> known[64];  // by device; a device's count does not change
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
     return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kvarn {
 
 struct EncodeParams {
@@ -317,6 +319,7 @@ struct ForkParams {
   ForkRows rows[kForkMaxTails];
   int32_t num_rows;
   int64_t tail_pieces;  // set by the launch
+  int32_t vectors;      // the counts' addresses are multiples of 16 (set by the launch)
   uint32_t* err;
 };
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t st);
@@ -391,6 +394,26 @@ int64_t q8_decode_workspace_bytes(int32_t num_seqs, int32_t rows, int32_t D);
 cudaError_t launch_q8_decode(const Q8DecodeParams& p, cudaStream_t st);
 
 int device_sm_count();
+
+// A kernel's limit of dynamic shared memory, raised once per device to one
+// value whatever the call (a static object per kernel).
+class SmemLimit {
+ public:
+  template <typename K>
+  cudaError_t set(K* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
 // Diagnostic: clock cycles the dense decode kernels wait for a page copy (0:
 // default) and whether each copy is announced larger than it is (so that its
 // phase never completes and every wait runs out).

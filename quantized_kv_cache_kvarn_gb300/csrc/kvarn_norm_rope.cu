@@ -474,11 +474,22 @@ int vector_lanes(int dim, int n) {
   return lanes;
 }
 
-using NormKernel = void (*)(const NormParams, const NormPlan);
+template <typename T, int LANES, bool INTERLEAVED, bool BACK>
+cudaError_t run_vector(const NormParams& A, const NormPlan& P, int rest, cudaStream_t st) {
+  constexpr int kRing = (BACK ? kBackDepth * 4 : kFwdDepth * 2) * kThreads * 16;
+  static SmemLimit limit;
+  auto* kernel = norm_rope_kernel<T, LANES, INTERLEAVED, BACK>;
+  // beside the ring at most 512 fractions, 8 x 512 cosines and sines
+  const cudaError_t e = limit.set(kernel, kRing + 8 * 512 + 8 * 8 * 512);
+  if (e != cudaSuccess) return e;
+  kernel<<<P.cta0[A.num_tensors], kThreads, std::max(kRing + rest, BACK ? kThreads / LANES * A.dim * 4 : 0), st>>>(A, P);
+  return cudaGetLastError();
+}
 template <typename T, int LANES>
-NormKernel vector_kernel(bool interleaved, bool backward) {
-  if (interleaved) return backward ? norm_rope_kernel<T, LANES, true, true> : norm_rope_kernel<T, LANES, true, false>;
-  return backward ? norm_rope_kernel<T, LANES, false, true> : norm_rope_kernel<T, LANES, false, false>;
+cudaError_t run_lanes(const NormParams& A, const NormPlan& P, int rest, cudaStream_t st) {
+  if (A.interleaved)
+    return A.backward ? run_vector<T, LANES, true, true>(A, P, rest, st) : run_vector<T, LANES, true, false>(A, P, rest, st);
+  return A.backward ? run_vector<T, LANES, false, true>(A, P, rest, st) : run_vector<T, LANES, false, false>(A, P, rest, st);
 }
 
 template <typename T>
@@ -504,30 +515,25 @@ cudaError_t launch(const NormParams& A, cudaStream_t st) {
   // one warp per head: the plan of a group of 32
   const NormPlan P = plan_norm(A.num_tensors, heads, A.dim, tokens, vec ? vector_lanes(A.dim, N) : 32, A.backward);
   const unsigned ctas = P.cta0[A.num_tensors];
+  cudaError_t e = cudaSuccess;
   if (ctas == 0) {
     // no heads or tokens: the sums over nothing
   } else if (vec) {
     int tok = 1;
     for (int k = 0; k < A.num_tensors; ++k) tok = std::max(tok, P.tok[k]);
-    const int ring = A.backward ? kBackDepth * 4 * kThreads * 16 : kFwdDepth * 2 * kThreads * 16;
-    int smem = ring + 8 * ((pairs + 1) & ~1) + 8 * tok * pairs;
-    if (A.backward) smem = std::max(smem, kThreads / P.lanes * A.dim * 4);
-    auto* kernel = P.lanes == 4    ? vector_kernel<T, 4>(A.interleaved, A.backward)
-                   : P.lanes == 8  ? vector_kernel<T, 8>(A.interleaved, A.backward)
-                   : P.lanes == 16 ? vector_kernel<T, 16>(A.interleaved, A.backward)
-                                   : vector_kernel<T, 32>(A.interleaved, A.backward);
-    // the most that a call may ask for: the ring, 512 fractions, 8 x 512 cosines and sines
-    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + 8 * 512 + 8 * 8 * 512);
-    if (set != cudaSuccess) return set;
-    kernel<<<ctas, kThreads, smem, st>>>(A, P);
+    const int rest = 8 * ((pairs + 1) & ~1) + 8 * tok * pairs;
+    e = P.lanes == 4    ? run_lanes<T, 4>(A, P, rest, st)
+        : P.lanes == 8  ? run_lanes<T, 8>(A, P, rest, st)
+        : P.lanes == 16 ? run_lanes<T, 16>(A, P, rest, st)
+                        : run_lanes<T, 32>(A, P, rest, st);
   } else {
     const int smem = A.backward ? kThreads / 32 * A.dim * 4 : 0;
     if (A.backward)
       norm_rope_any_kernel<T, true><<<ctas, kThreads, smem, st>>>(A, P);
     else
       norm_rope_any_kernel<T, false><<<ctas, kThreads, smem, st>>>(A, P);
+    e = cudaGetLastError();
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !sums) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((A.dim + 31) / 32, A.num_tensors);

@@ -33,6 +33,7 @@ namespace {
 constexpr int kThreads = 256, kWarpsPerCta = kThreads / 32;
 constexpr int kPiece = 4096;      // bytes a warp copies at a time, all in flight
 constexpr int kEntries = 256;     // table entries a warp takes at a time
+constexpr int kCounts = 1024;       // reference counts a warp takes at a time
 constexpr int kPagesPerCta = 2048;  // compaction: pages of a block
 
 // `bytes` (a multiple of 16) by one warp, at most kPiece.
@@ -74,15 +75,23 @@ __device__ __forceinline__ int parent_of(const ForkParams& A, int b) {
 
 __device__ __forceinline__ int whole_tiles(const ForkParams& A, int L) { return max(0, L - A.recent) / A.N; }
 
-// Whether the next token of a sequence of L tokens, or its sinks, sees tile t.
-__device__ __forceinline__ bool tile_kept(const ForkParams& A, int L, int t) {
-  const int64_t at = static_cast<int64_t>(t) * A.N;
-  return A.window == 0 || at < A.sinks || at + A.N > static_cast<int64_t>(L) + 1 - A.window;
-}
+// Entries that the next token of a sequence of L tokens, or its sinks, sees:
+// those below `sinks` and those from `first` on.
+struct Seen {
+  int sinks, first;
+  __device__ __forceinline__ Seen(const ForkParams& A, int L) : sinks(0), first(0) {
+    if (A.window == 0) return;
+    const int s = min(A.sinks, A.max_seq_len);
+    sinks = (s / A.N + (s % A.N != 0)) * A.pages_per_tile;
+    // tile t holds a token after position L - window where t >= (L + 1 - window) / N
+    first = max(0, L - (A.window - 1)) / A.N * A.pages_per_tile;
+  }
+  __device__ __forceinline__ bool operator()(int e) const { return e < sinks || e >= first; }
+};
 
-// Entry e of old row a of length L: the page, -1 where there is none.
-__device__ __forceinline__ int entry_of(const ForkParams& A, int a, int L, int e) {
-  if (e >= whole_tiles(A, L) * A.pages_per_tile) return -1;
+// Entry e of old row a, which holds `held`: the page, -1 where there is none.
+__device__ __forceinline__ int entry_of(const ForkParams& A, int a, int held, int e) {
+  if (e >= held) return -1;
   const int id = A.table[static_cast<int64_t>(a) * A.bt_stride + e];
   if (id >= A.num_pages) {
     set_error(A.err, KVARN_DEVERR_PAGE_RANGE);
@@ -91,65 +100,88 @@ __device__ __forceinline__ int entry_of(const ForkParams& A, int a, int L, int e
   return id < 0 ? -1 : id;
 }
 
+// Items of a warp: pieces of the tails, pieces of the table rows (with the
+// lengths), pieces of the counts, each item one chain of loads.
 __global__ void __launch_bounds__(kThreads) fork_copy_kernel(const __grid_constant__ ForkParams A) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarpsPerCta;
-  for (int64_t i = warp; i < A.tail_pieces; i += warps) {
-    int k = 0;
-    int64_t j = i;
-    while (j >= A.rows[k].pieces) j -= A.rows[k++].pieces;
-    const ForkRows& R = A.rows[k];
-    const int64_t per = (static_cast<int64_t>(R.capacity) * R.row_bytes + kPiece - 1) / kPiece;
-    const int64_t unit = j / per;
-    const int b = static_cast<int>(unit / R.heads), h = static_cast<int>(unit % R.heads);
-    const int p = parent_of(A, b);
-    if (p < 0) continue;
-    const int L = length_of(A, p);
-    const int live = R.whole ? R.capacity : min(R.capacity, L - whole_tiles(A, L) * A.N);
-    const int64_t at = j % per * kPiece, end = live * R.row_bytes;
-    if (at >= end) continue;
-    const int64_t size = static_cast<int64_t>(R.capacity) * R.row_bytes;
-    copy_piece(static_cast<char*>(R.out) + unit * size + at,
-               static_cast<const char*>(R.in) + (static_cast<int64_t>(p) * R.heads + h) * size + at,
-               static_cast<int>(min(static_cast<int64_t>(kPiece), end - at)));
-  }
-  const int pieces = (A.entries + kEntries - 1) / kEntries;
-  for (int64_t i = warp; i < static_cast<int64_t>(A.num_out) * max(1, pieces); i += warps) {
-    const int b = static_cast<int>(i / max(1, pieces)), e0 = static_cast<int>(i % max(1, pieces)) * kEntries;
-    const int p = parent_of(A, b);
-    const int L = p < 0 ? 0 : length_of(A, p);
-    if (e0 == 0 && lane == 0) A.lens_out[b] = L;
-    int v[kEntries / 32];
+  const int pieces = max(1, (A.entries + kEntries - 1) / kEntries);
+  const int64_t table_items = static_cast<int64_t>(A.num_out) * pieces, count_items = (A.num_pages + kCounts - 1) / kCounts;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
+       i < A.tail_pieces + table_items + count_items; i += warps) {
+    if (i < A.tail_pieces) {
+      int k = 0;
+      int64_t j = i;
+      while (j >= A.rows[k].pieces) j -= A.rows[k++].pieces;
+      const ForkRows& R = A.rows[k];
+      const int64_t size = static_cast<int64_t>(R.capacity) * R.row_bytes, per = (size + kPiece - 1) / kPiece;
+      const int64_t unit = j / per;
+      const int b = static_cast<int>(unit / R.heads), h = static_cast<int>(unit % R.heads);
+      const int p = parent_of(A, b);
+      if (p < 0) continue;
+      const int L = length_of(A, p);
+      const int live = R.whole ? R.capacity : min(R.capacity, L - whole_tiles(A, L) * A.N);
+      const int64_t at = (j - unit * per) * kPiece, end = live * R.row_bytes;
+      if (at >= end) continue;
+      copy_piece(static_cast<char*>(R.out) + unit * size + at,
+                 static_cast<const char*>(R.in) + (static_cast<int64_t>(p) * R.heads + h) * size + at,
+                 static_cast<int>(min(static_cast<int64_t>(kPiece), end - at)));
+    } else if (i < A.tail_pieces + table_items) {
+      const int64_t j = i - A.tail_pieces;
+      const int b = static_cast<int>(j / pieces), e0 = static_cast<int>(j % pieces) * kEntries;
+      const int p = parent_of(A, b);
+      const int L = p < 0 ? 0 : length_of(A, p), held = p < 0 ? 0 : whole_tiles(A, L) * A.pages_per_tile;
+      const Seen seen(A, L);
+      if (e0 == 0 && lane == 0) A.lens_out[b] = L;
+      int v[kEntries / 32];
 #pragma unroll
-    for (int k = 0; k < kEntries / 32; ++k) {
-      const int e = e0 + 32 * k + lane;
-      v[k] = p >= 0 && e < A.entries && tile_kept(A, L, e / A.pages_per_tile) ? entry_of(A, p, L, e) : -1;
-    }
+      for (int k = 0; k < kEntries / 32; ++k) {
+        const int e = e0 + 32 * k + lane;
+        v[k] = seen(e) ? entry_of(A, p, held, e) : -1;
+      }
 #pragma unroll
-    for (int k = 0; k < kEntries / 32; ++k) {
-      const int e = e0 + 32 * k + lane;
-      if (e < A.entries) A.table_out[static_cast<int64_t>(b) * A.bt_stride + e] = v[k];
+      for (int k = 0; k < kEntries / 32; ++k) {
+        const int e = e0 + 32 * k + lane;
+        if (e < A.entries) A.table_out[static_cast<int64_t>(b) * A.bt_stride + e] = v[k];
+      }
+    } else {
+      // the counts, an empty bitmap, -1 behind it
+      const int words = (A.num_pages + 31) / 32, p0 = static_cast<int>(i - A.tail_pieces - table_items) * kCounts;
+      const bool copy = A.refs_out != A.refs;
+      if (A.vectors && p0 + kCounts <= A.num_pages) {
+        int4 v[kCounts / 128];
+        if (copy) {
+#pragma unroll
+          for (int k = 0; k < kCounts / 128; ++k) v[k] = reinterpret_cast<const int4*>(A.refs + p0)[32 * k + lane];
+#pragma unroll
+          for (int k = 0; k < kCounts / 128; ++k) reinterpret_cast<int4*>(A.refs_out + p0)[32 * k + lane] = v[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kCounts / 128; ++k) {
+          const int at = p0 + 4 * (32 * k + lane);
+          reinterpret_cast<int4*>(A.freed + p0)[32 * k + lane] =
+              make_int4(at < words ? 0 : -1, at + 1 < words ? 0 : -1, at + 2 < words ? 0 : -1, at + 3 < words ? 0 : -1);
+        }
+      } else {
+        for (int at = p0 + lane; at < min(A.num_pages, p0 + kCounts); at += 32) {
+          if (copy) A.refs_out[at] = A.refs[at];
+          A.freed[at] = at < words ? 0 : -1;
+        }
+      }
     }
-  }
-  // the counts, an empty bitmap, -1 behind it
-  const int words = (A.num_pages + 31) / 32;
-  for (int64_t i = warp * 32 + lane; i < A.num_pages; i += warps * 32) {
-    if (A.refs_out != A.refs) A.refs_out[i] = A.refs[i];
-    A.freed[i] = i < words ? 0 : -1;
   }
 }
 
 // Children of every old row, counted by each CTA for itself, then the rows'
-// entries a warp at a time.
+// entries a warp at a time. What is read before pdl_wait_primary no kernel of
+// this call writes, and what came before the call had finished when the copy
+// kernel let this one start.
 __global__ void __launch_bounds__(kThreads) fork_count_kernel(const __grid_constant__ ForkParams A) {
   extern __shared__ int children[];
   for (int a = threadIdx.x; a < A.num_in; a += kThreads) children[a] = 0;
   __syncthreads();
-  pdl_wait_primary();
-  pdl_launch_dependents();
   for (int b = threadIdx.x; b < A.num_out; b += kThreads) {
     const int p = A.parents[b];
     if (p >= 0 && p < A.num_in) atomicAdd(&children[p], 1);
@@ -157,29 +189,36 @@ __global__ void __launch_bounds__(kThreads) fork_count_kernel(const __grid_const
   __syncthreads();
   const int lane = threadIdx.x & 31, pieces = (A.entries + kEntries - 1) / kEntries;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarpsPerCta;
+  bool waited = false;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
        i < static_cast<int64_t>(A.num_in) * pieces; i += warps) {
     const int a = static_cast<int>(i / pieces), e0 = static_cast<int>(i % pieces) * kEntries;
     const int c = children[a];
     if (c == 1 && A.window == 0) continue;
-    const int L = length_of(A, a);
-    if (e0 >= whole_tiles(A, L) * A.pages_per_tile) continue;
+    const int L = length_of(A, a), held = whole_tiles(A, L) * A.pages_per_tile;
+    if (e0 >= held) continue;
+    const Seen seen(A, L);
     int id[kEntries / 32], d[kEntries / 32];
 #pragma unroll
     for (int k = 0; k < kEntries / 32; ++k) {
       const int e = e0 + 32 * k + lane;
-      d[k] = (tile_kept(A, L, e / A.pages_per_tile) ? c : 0) - 1;
-      id[k] = d[k] && e < A.entries ? entry_of(A, a, L, e) : -1;
+      d[k] = (seen(e) ? c : 0) - 1;
+      id[k] = d[k] && e < A.entries ? entry_of(A, a, held, e) : -1;
     }
-    // a page that forks with its row is one of many: the counts of all are in
-    // flight together
+    if (!waited) pdl_wait_primary();
+    waited = true;
+    // all atomics of the piece in flight together
+    int old[kEntries / 32];
 #pragma unroll
-    for (int k = 0; k < kEntries / 32; ++k) {
-      if (id[k] < 0) continue;
-      const int old = atomicAdd(A.refs_out + id[k], d[k]);
-      if (old > 0 && old + d[k] <= 0) atomicOr(A.freed + (id[k] >> 5), static_cast<int>(1u << (id[k] & 31)));
-    }
+    for (int k = 0; k < kEntries / 32; ++k) old[k] = id[k] >= 0 ? atomicAdd(A.refs_out + id[k], d[k]) : 0;
+#pragma unroll
+    for (int k = 0; k < kEntries / 32; ++k)
+      if (id[k] >= 0 && old[k] > 0 && old[k] + d[k] <= 0)
+        atomicOr(A.freed + (id[k] >> 5), static_cast<int>(1u << (id[k] & 31)));
   }
+  // the list kernel may start once every CTA is here, and waits for the end
+  if (!waited) pdl_wait_primary();
+  pdl_launch_dependents();
 }
 
 constexpr int kListCtas = 8, kListThreads = 1024;
@@ -200,9 +239,15 @@ __global__ void __cluster_dims__(kListCtas, 1, 1) __launch_bounds__(kListThreads
     // agree with the rows: what it came to decides
     uint32_t b = static_cast<uint32_t>(A.freed[w0 + i]), keep = 0;
     while (b) {
-      const int bit = __ffs(b) - 1;
-      b &= b - 1;
-      if (A.refs_out[(w0 + i) * 32 + bit] <= 0) keep |= 1u << bit;
+      int bit[8], refs[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {  // eight counts in flight
+        bit[k] = __ffs(b) - 1;
+        b &= b - 1;
+        refs[k] = bit[k] >= 0 ? A.refs_out[(w0 + i) * 32 + bit[k]] : 1;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) keep |= refs[k] <= 0 ? 1u << bit[k] : 0u;
     }
     bits[i] = keep;
   }
@@ -397,19 +442,21 @@ cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
                ((static_cast<int64_t>(R.capacity) * R.row_bytes + kPiece - 1) / kPiece);
     A.tail_pieces += R.pieces;
   }
+  A.vectors = ((reinterpret_cast<uintptr_t>(A.refs) | reinterpret_cast<uintptr_t>(A.refs_out) |
+                reinterpret_cast<uintptr_t>(A.freed)) % 16) == 0;
   const int pieces = (A.entries + kEntries - 1) / kEntries;
-  const int64_t copies = std::max({A.tail_pieces, static_cast<int64_t>(A.num_out) * std::max(1, pieces),
-                                   static_cast<int64_t>(A.num_pages) / 32});
-  cudaError_t e = chained(fork_copy_kernel, ctas_for(copies, 6), kThreads, 0, st, A);
+  const int64_t copies = A.tail_pieces + static_cast<int64_t>(A.num_out) * std::max(1, pieces) + (A.num_pages + kCounts - 1) / kCounts;
+  // as many CTAs as are resident: five of 48 registers
+  cudaError_t e = chained(fork_copy_kernel, ctas_for(copies, 5), kThreads, 0, st, A);
   if (e != cudaSuccess) return e;
   const int smem = 4 * A.num_in;
-  e = cudaFuncSetAttribute(fork_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kForkMaxRows);
+  static SmemLimit count_limit, list_limit;
+  e = count_limit.set(fork_count_kernel, 4 * kForkMaxRows);
   if (e != cudaSuccess) return e;
   e = chained(fork_count_kernel, ctas_for(static_cast<int64_t>(A.num_in) * pieces, 4), kThreads, smem, st, A);
   if (e != cudaSuccess) return e;
   const int words = (A.num_pages + 31) / 32;
-  e = cudaFuncSetAttribute(fork_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           4 * ((kForkMaxPages / 32 + kListCtas - 1) / kListCtas));
+  e = list_limit.set(fork_list_kernel, 4 * ((kForkMaxPages / 32 + kListCtas - 1) / kListCtas));
   if (e != cudaSuccess) return e;
   return chained(fork_list_kernel, kListCtas, kListThreads, 4 * std::max(1, (words + kListCtas - 1) / kListCtas), st, A);
 }
@@ -433,7 +480,7 @@ cudaError_t launch_compact(const CompactParams& p, void* workspace, cudaStream_t
   if (e != cudaSuccess) return e;
   const int64_t per = (A.page_bytes + kPiece - 1) / kPiece;
   const int64_t items = std::max<int64_t>(A.num_pages / 2 * per, (static_cast<int64_t>(A.rows) * A.entries + 31) / 32);
-  return chained(compact_move_kernel, ctas_for(items, 6), kThreads, 0, st, A);
+  return chained(compact_move_kernel, ctas_for(items, 4), kThreads, 0, st, A);  // four CTAs of 54 registers are resident
 }
 
 }  // namespace kvarn

@@ -858,7 +858,8 @@ template <int D, int R, int CODE>
 cudaError_t run(const Q8Args& A, int ctas, cudaStream_t st) {
   using S = Shape<D, R>;
   auto* kernel = q8_decode_kernel<D, R, CODE>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  static SmemLimit limit;
+  cudaError_t e = limit.set(kernel, S::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);

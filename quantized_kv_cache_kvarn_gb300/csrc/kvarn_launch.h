@@ -395,6 +395,23 @@ cudaError_t launch_q8_decode(const Q8DecodeParams& p, cudaStream_t st);
 
 int device_sm_count();
 
+// A launch as a programmatic dependent of the kernel before it on the stream:
+// the kernel waits (pdl_wait_primary) before it touches memory.
+template <typename... P, typename... Args>
+cudaError_t chained(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A kernel's limit of dynamic shared memory, raised once per device to one
 // value whatever the call (a static object per kernel).
 class SmemLimit {

@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
   float2* cs = reinterpret_cast<float2*>(rest + 8 * ((pairs + 1) & ~1));  // [tok][pairs]
   const int tokens = A.num_seqs * A.num_tokens;  // fits 32 bits
   const int tid = threadIdx.x;
+  pdl_wait_primary();
+  pdl_launch_dependents();
 
   const int c = tid % LANES, tt = tid / LANES % tok, hs = tid / (LANES * tok), slots = kThreads / (LANES * tok);
   const bool on = c < columns, turn = c < chunks;
@@ -342,6 +344,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
   const NormTensor& t = A.t[k];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pairs = A.rope_dim / 2, rest = A.dim - A.rope_dim;
   float* mine = reinterpret_cast<float*>(smem) + warp * A.dim;  // this warp's gradient of the weights
+  pdl_wait_primary();
+  pdl_launch_dependents();
   if constexpr (BACK)
     for (int d = lane; d < A.dim; d += 32) mine[d] = 0.f;
   __syncwarp();
@@ -482,8 +486,8 @@ cudaError_t run_vector(const NormParams& A, const NormPlan& P, int rest, cudaStr
   // beside the ring at most 512 fractions, 8 x 512 cosines and sines
   const cudaError_t e = limit.set(kernel, kRing + 8 * 512 + 8 * 8 * 512);
   if (e != cudaSuccess) return e;
-  kernel<<<P.cta0[A.num_tensors], kThreads, std::max(kRing + rest, BACK ? kThreads / LANES * A.dim * 4 : 0), st>>>(A, P);
-  return cudaGetLastError();
+  return chained(kernel, dim3(static_cast<unsigned>(P.cta0[A.num_tensors])), kThreads,
+                 std::max(kRing + rest, BACK ? kThreads / LANES * A.dim * 4 : 0), st, A, P);
 }
 template <typename T, int LANES>
 cudaError_t run_lanes(const NormParams& A, const NormPlan& P, int rest, cudaStream_t st) {
@@ -528,23 +532,10 @@ cudaError_t launch(const NormParams& A, cudaStream_t st) {
                         : run_lanes<T, 32>(A, P, rest, st);
   } else {
     const int smem = A.backward ? kThreads / 32 * A.dim * 4 : 0;
-    if (A.backward)
-      norm_rope_any_kernel<T, true><<<ctas, kThreads, smem, st>>>(A, P);
-    else
-      norm_rope_any_kernel<T, false><<<ctas, kThreads, smem, st>>>(A, P);
-    e = cudaGetLastError();
+    e = chained(A.backward ? norm_rope_any_kernel<T, true> : norm_rope_any_kernel<T, false>, dim3(ctas), kThreads, smem, st, A, P);
   }
   if (e != cudaSuccess || !sums) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((A.dim + 31) / 32, A.num_tensors);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_weight_sum_kernel, A, P);
+  return chained(norm_weight_sum_kernel, dim3((A.dim + 31) / 32, A.num_tensors), 1024, 0, st, A, P);
 }
 
 }  // namespace

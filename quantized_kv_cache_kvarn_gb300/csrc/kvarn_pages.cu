@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarpsPerCta = kThreads / 32;
 constexpr int kPiece = 4096;      // bytes a warp copies at a time, all in flight
+constexpr int kCopyCtas = 4;      // resident CTAs of the kernels that copy: 126 MB of pages in 53 us, 68 with six
 constexpr int kEntries = 256;     // table entries a warp takes at a time
 constexpr int kCounts = 1024;       // reference counts a warp takes at a time
 constexpr int kPagesPerCta = 2048;  // compaction: pages of a block
@@ -42,15 +43,13 @@ __device__ __forceinline__ void copy_piece(void* dst, const void* src, int bytes
   const uint4* s = static_cast<const uint4*>(src);
   uint4* d = static_cast<uint4*>(dst);
   const int n = bytes >> 4;
-  if (n == kPiece / 16) {
-    uint4 v[8];
+  uint4 v[kPiece / 512];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = s[lane + 32 * i];
+  for (int i = 0; i < kPiece / 512; ++i)
+    if (lane + 32 * i < n) v[i] = s[lane + 32 * i];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[lane + 32 * i] = v[i];
-  } else {
-    for (int i = lane; i < n; i += 32) d[i] = s[i];
-  }
+  for (int i = 0; i < kPiece / 512; ++i)
+    if (lane + 32 * i < n) d[lane + 32 * i] = v[i];
 }
 
 // ---------------------------------------------------------------- fork
@@ -102,7 +101,7 @@ __device__ __forceinline__ int entry_of(const ForkParams& A, int a, int held, in
 
 // Items of a warp: pieces of the tails, pieces of the table rows (with the
 // lengths), pieces of the counts, each item one chain of loads.
-__global__ void __launch_bounds__(kThreads) fork_copy_kernel(const __grid_constant__ ForkParams A) {
+__global__ void __launch_bounds__(kThreads, kCopyCtas) fork_copy_kernel(const __grid_constant__ ForkParams A) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -234,22 +233,34 @@ __global__ void __cluster_dims__(kListCtas, 1, 1) __launch_bounds__(kListThreads
   const int tid = threadIdx.x, lane = tid & 31, rank = static_cast<int>(cluster.block_rank());
   const int words = (A.num_pages + 31) / 32, share = (words + kListCtas - 1) / kListCtas;
   const int w0 = min(words, rank * share), n = min(words, w0 + share) - w0;
-  for (int i = tid; i < n; i += kListThreads) {
-    // a count may have passed through 0 on its way where the counts did not
-    // agree with the rows: what it came to decides
-    uint32_t b = static_cast<uint32_t>(A.freed[w0 + i]), keep = 0;
-    while (b) {
-      int bit[8], refs[8];
+  constexpr int kWords = 8;  // of a thread, in flight together
+  for (int i0 = tid; i0 < n; i0 += kWords * kListThreads) {
+    uint32_t word[kWords];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {  // eight counts in flight
-        bit[k] = __ffs(b) - 1;
-        b &= b - 1;
-        refs[k] = bit[k] >= 0 ? A.refs_out[(w0 + i) * 32 + bit[k]] : 1;
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) keep |= refs[k] <= 0 ? 1u << bit[k] : 0u;
+    for (int j = 0; j < kWords; ++j) {
+      const int i = i0 + j * kListThreads;
+      word[j] = i < n ? static_cast<uint32_t>(A.freed[w0 + i]) : 0u;
     }
-    bits[i] = keep;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      const int i = i0 + j * kListThreads;
+      if (i >= n) break;
+      // a count may have passed through 0 on its way where the counts did not
+      // agree with the rows: what it came to decides
+      uint32_t b = word[j], keep = 0;
+      while (b) {
+        int bit[4], refs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // four counts in flight
+          bit[k] = __ffs(b) - 1;
+          b &= b - 1;
+          refs[k] = bit[k] >= 0 ? A.refs_out[(w0 + i) * 32 + bit[k]] : 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) keep |= refs[k] <= 0 ? 1u << bit[k] : 0u;
+      }
+      bits[i] = keep;
+    }
   }
   __syncthreads();
   const int per = (n + kListThreads - 1) / kListThreads, i0 = min(n, tid * per), i1 = min(n, i0 + per);
@@ -374,55 +385,45 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const __grid_con
   }
 }
 
-// Pages in pieces of kPiece bytes to a warp, then the tables.
-__global__ void __launch_bounds__(kThreads) compact_move_kernel(const __grid_constant__ CompactParams A) {
+// Items of a warp: 32 table entries (a chain of three loads, so they come
+// first), then pieces of kPiece bytes of the pages that move.
+__global__ void __launch_bounds__(kThreads, kCopyCtas) compact_move_kernel(const __grid_constant__ CompactParams A) {
   pdl_wait_primary();
   const int lane = threadIdx.x & 31, moves = *A.moves;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarpsPerCta;
   const int64_t per = (A.page_bytes + kPiece - 1) / kPiece;
-  for (int64_t i = warp; i < moves * per; i += warps) {
-    const int64_t k = i / per, at = i % per * kPiece;
-    const int2 from = A.movers[k];
-    const int to = A.holes[k];
-    copy_piece(A.cache + to * A.page_bytes + at, A.cache + from.x * A.page_bytes + at,
-               static_cast<int>(min(static_cast<int64_t>(kPiece), A.page_bytes - at)));
-    if (at == 0 && lane == 0) {
-      A.refs_out[to] = from.y;
-      A.remap[from.x] = to;
-    }
-  }
-  for (int64_t i = warp * 32 + lane; i < static_cast<int64_t>(A.rows) * A.entries; i += warps * 32) {
-    const int64_t at = i / A.entries * A.bt_stride + i % A.entries;
-    int id = A.table[at];
-    if (id >= A.num_pages) {
-      set_error(A.err, KVARN_DEVERR_PAGE_RANGE);
-      id = -1;
-    } else if (id >= 0) {
-      // a mover's new id is written while this runs: either form names it
-      id = *static_cast<volatile const int32_t*>(A.remap + id);
-      if (id == -1) set_error(A.err, KVARN_DEVERR_PAGE_RANGE);  // a free page
-      if (id <= -2) id = A.holes[-2 - id];
+  const int64_t cells = static_cast<int64_t>(A.rows) * A.entries, table_items = (cells + 31) / 32;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5); i < table_items + moves * per;
+       i += warps) {
+    if (i < table_items) {
+      const int64_t cell = i * 32 + lane;
+      if (cell >= cells) continue;
+      const int64_t at = cell / A.entries * A.bt_stride + cell % A.entries;
+      int id = A.table[at];
+      if (id >= A.num_pages) {
+        set_error(A.err, KVARN_DEVERR_PAGE_RANGE);
+        id = -1;
+      } else if (id >= 0) {
+        // a mover's new id is written while this runs: either form names it
+        id = *static_cast<volatile const int32_t*>(A.remap + id);
+        if (id == -1) set_error(A.err, KVARN_DEVERR_PAGE_RANGE);  // a free page
+        if (id <= -2) id = A.holes[-2 - id];
+      } else {
+        id = -1;
+      }
+      A.table_out[at] = id;
     } else {
-      id = -1;
+      const int64_t j = i - table_items, k = j / per, at = (j - k * per) * kPiece;
+      const int2 from = A.movers[k];
+      const int to = A.holes[k];
+      copy_piece(A.cache + to * A.page_bytes + at, A.cache + from.x * A.page_bytes + at,
+                 static_cast<int>(min(static_cast<int64_t>(kPiece), A.page_bytes - at)));
+      if (at == 0 && lane == 0) {
+        A.refs_out[to] = from.y;
+        A.remap[from.x] = to;
+      }
     }
-    A.table_out[at] = id;
   }
-}
-
-template <typename... P, typename... Args>
-cudaError_t chained(void (*kernel)(P...), int ctas, int threads, int smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // CTAs of kThreads for so many warp items, at most `per_sm` an SM.
@@ -446,8 +447,8 @@ cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
                 reinterpret_cast<uintptr_t>(A.freed)) % 16) == 0;
   const int pieces = (A.entries + kEntries - 1) / kEntries;
   const int64_t copies = A.tail_pieces + static_cast<int64_t>(A.num_out) * std::max(1, pieces) + (A.num_pages + kCounts - 1) / kCounts;
-  // as many CTAs as are resident: five of 48 registers
-  cudaError_t e = chained(fork_copy_kernel, ctas_for(copies, 5), kThreads, 0, st, A);
+  // as many CTAs as are resident
+  cudaError_t e = chained(fork_copy_kernel, ctas_for(copies, kCopyCtas), kThreads, 0, st, A);
   if (e != cudaSuccess) return e;
   const int smem = 4 * A.num_in;
   static SmemLimit count_limit, list_limit;
@@ -479,8 +480,8 @@ cudaError_t launch_compact(const CompactParams& p, void* workspace, cudaStream_t
   e = chained(compact_plan_kernel, blocks, kThreads, 0, st, A, blocks);
   if (e != cudaSuccess) return e;
   const int64_t per = (A.page_bytes + kPiece - 1) / kPiece;
-  const int64_t items = std::max<int64_t>(A.num_pages / 2 * per, (static_cast<int64_t>(A.rows) * A.entries + 31) / 32);
-  return chained(compact_move_kernel, ctas_for(items, 4), kThreads, 0, st, A);  // four CTAs of 54 registers are resident
+  const int64_t items = A.num_pages / 2 * per + (static_cast<int64_t>(A.rows) * A.entries + 31) / 32;
+  return chained(compact_move_kernel, ctas_for(items, kCopyCtas), kThreads, 0, st, A);  // as many as are resident
 }
 
 }  // namespace kvarn

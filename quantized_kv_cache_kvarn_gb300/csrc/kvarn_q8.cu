@@ -189,11 +189,12 @@ __device__ __forceinline__ void read_at(uint8_t* page, T* dst, int64_t token_str
   }
 }
 
-// Warp item: ((b blocks + u) Hkv + h) 2 + (0: K, 1: V), or b Hkv blocks ...
-// The heads are innermost, so that token-major inputs are read in whole rows.
+// Warp item ((b blocks + u) Hkv + h) 2 + (0: K, 1: V): the heads are innermost, so that token-major inputs are read in whole rows.
 template <int D, typename T, int CODE, bool READ>
 __global__ void __launch_bounds__(32 * kWarps) q8_block_kernel(const __grid_constant__ Q8BlockParams A) {
   __shared__ __align__(16) unsigned char sm[kWarps][16 * D];
+  pdl_wait_primary();
+  pdl_launch_dependents();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t n = item >> 1;
   const int h = static_cast<int>(n % A.num_kv_heads);
@@ -248,6 +249,8 @@ __device__ __forceinline__ void append_one(const Q8BlockParams& A, int b, int h,
 template <int D, typename T, int CODE>
 __global__ void __launch_bounds__(32 * kWarps) q8_append_kernel(const __grid_constant__ Q8BlockParams A) {
   __shared__ __align__(16) unsigned char sm[kWarps][16 * D];
+  pdl_wait_primary();
+  pdl_launch_dependents();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t n = item >> 1;
   const int h = static_cast<int>(n % A.num_kv_heads);
@@ -287,11 +290,9 @@ cudaError_t launch_q8_blocks(const Q8BlockParams& p, bool read, cudaStream_t st)
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
   return with_types(p, [&](auto d, auto t, auto c) {
     using T = decltype(t);
-    if (read)
-      q8_block_kernel<decltype(d)::value, T, decltype(c)::value, true><<<static_cast<unsigned>(ctas), 32 * kWarps, 0, st>>>(p);
-    else
-      q8_block_kernel<decltype(d)::value, T, decltype(c)::value, false><<<static_cast<unsigned>(ctas), 32 * kWarps, 0, st>>>(p);
-    return cudaGetLastError();
+    return chained(read ? q8_block_kernel<decltype(d)::value, T, decltype(c)::value, true>
+                        : q8_block_kernel<decltype(d)::value, T, decltype(c)::value, false>,
+                   dim3(static_cast<unsigned>(ctas)), 32 * kWarps, 0, st, p);
   });
 }
 
@@ -300,8 +301,8 @@ cudaError_t launch_q8_append(const Q8BlockParams& p, cudaStream_t st) {
   const int64_t ctas = (items + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
   return with_types(p, [&](auto d, auto t, auto c) {
-    q8_append_kernel<decltype(d)::value, decltype(t), decltype(c)::value><<<static_cast<unsigned>(ctas), 32 * kWarps, 0, st>>>(p);
-    return cudaGetLastError();
+    return chained(q8_append_kernel<decltype(d)::value, decltype(t), decltype(c)::value>, dim3(static_cast<unsigned>(ctas)),
+                   32 * kWarps, 0, st, p);
   });
 }
 

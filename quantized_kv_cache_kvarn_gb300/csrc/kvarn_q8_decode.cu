@@ -816,30 +816,39 @@ __global__ void __launch_bounds__(128) q8_merge_kernel(const __grid_constant__ Q
     const int n = static_cast<int>(w1 - w0 + 1);
     const float* part = A.part + (2 * w0 * R + rr % R) * ROW;
     auto slot = [&](int i) { return part + static_cast<int64_t>(2 * i + (i == 0 && inside ? 1 : 0)) * R * ROW; };
+    // a lane keeps the head (m, l, mt) of every 32nd part: the maxima first
     float MT = -INFINITY;
+    float4 head = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
     for (int i = lane; i < n; i += 32) {
-      const float* p = slot(i);
-      M = fmaxf(M, p[0]);
-      MT = fmaxf(MT, p[2]);
+      const float4 v = *reinterpret_cast<const float4*>(slot(i));
+      M = fmaxf(M, v.x);
+      MT = fmaxf(MT, v.z);
+      if (i < 32) head = v;
     }
     M = warp_max_xor(M, 1, 32);
     MT = warp_max_xor(MT, 1, 32);
     const float mu = M == -INFINITY ? 0.f : M, mtu = MT == -INFINITY ? 0.f : MT;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* p = slot(i);
-      const float4 head = *reinterpret_cast<const float4*>(p);
-      L = fmaf(head.y, exp2f(head.x - mu), L);
-      const float w = exp2f(head.z - mtu);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      if (i0 > 0 && i0 + lane < n) head = *reinterpret_cast<const float4*>(slot(i0 + lane));
+      const bool mine = i0 + lane < n;
+      const float w = mine ? exp2f(head.z - mtu) : 0.f;
+      L += mine ? head.y * exp2f(head.x - mu) : 0.f;
+      const int count = min(32, n - i0);
+#pragma unroll 8
+      for (int i = 0; i < count; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float* p = slot(i0 + i) + 4 + lane * E;
 #pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p + 4 + lane * E + e);
-        acc[e] = fmaf(v.x, w, acc[e]);
-        acc[e + 1] = fmaf(v.y, w, acc[e + 1]);
-        acc[e + 2] = fmaf(v.z, w, acc[e + 2]);
-        acc[e + 3] = fmaf(v.w, w, acc[e + 3]);
+        for (int e = 0; e < E; e += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(p + e);
+          acc[e] = fmaf(v.x, wi, acc[e]);
+          acc[e + 1] = fmaf(v.y, wi, acc[e + 1]);
+          acc[e + 2] = fmaf(v.z, wi, acc[e + 2]);
+          acc[e + 3] = fmaf(v.w, wi, acc[e + 3]);
+        }
       }
     }
+    L = warp_sum_xor(L, 1, 32);
     f = out_factor(mu, mtu, L);
     M = mu;
   }
@@ -861,23 +870,11 @@ cudaError_t run(const Q8Args& A, int ctas, cudaStream_t st) {
   static SmemLimit limit;
   cudaError_t e = limit.set(kernel, S::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = S::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, A);
+  e = chained(kernel, dim3(ctas), 32 * kWarps, S::SMEM, st, A);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(A.B) * A.Q * A.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, q8_merge_kernel<D, R>, A, static_cast<int64_t>(ctas) * S::TEAMS);
+  return chained(q8_merge_kernel<D, R>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, A,
+                 static_cast<int64_t>(ctas) * S::TEAMS);
 }
 
 }  // namespace

@@ -13,7 +13,7 @@
 // The counts are whole numbers, so the order of the atomics does not matter.
 //
 // Compact. n live pages move to the lowest ids: the k-th free page below n
-// (a hole) receives the k-th live page at or above n. Three kernels: live
+// (a hole) receives the k-th live page at or above n. Up to three kernels: live
 // pages per block of pages; their prefix sums and with them the list of
 // moves; the moves, beside the tables. A page's move is read and written once
 // (HBM bounds it), a hole is never a source, so moves need no order.
@@ -36,6 +36,11 @@ constexpr int kCopyCtas = 4;      // resident CTAs of the kernels that copy: 126
 constexpr int kEntries = 256;     // table entries a warp takes at a time
 constexpr int kCounts = 1024;       // reference counts a warp takes at a time
 constexpr int kPagesPerCta = 2048;  // compaction: pages of a block
+
+// Compaction: up to so many pages every CTA of the plan counts for itself what
+// is in use, without a kernel for the blocks' sums: 6.2 us against 8.2 for 1531
+// pages, 8.8 against 9.7 for 16384, 12.3 against 10.9 for 32768.
+constexpr int kDirectPages = 16384;
 
 // `bytes` (a multiple of 16) by one warp, at most kPiece.
 __device__ __forceinline__ void copy_piece(void* dst, const void* src, int bytes) {
@@ -335,21 +340,33 @@ __global__ void __launch_bounds__(kThreads) compact_count_kernel(const __grid_co
 }
 
 // Moves, new counts and new ids (a mover's: -2 - its rank, until it moves).
+// DIRECT: every CTA counts the live pages for itself, from all counts, instead
+// of from the blocks' sums.
+template <bool DIRECT>
 __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const __grid_constant__ CompactParams A, int blocks) {
   pdl_wait_primary();
   pdl_launch_dependents();
   // live pages before this block, in all, and below the `live`-th page
-  int b = 0, a = 0, live, before;
-  for (int i = threadIdx.x; i < blocks; i += kThreads) {
-    const int s = A.block_live[i];
-    a += s;
-    if (i < static_cast<int>(blockIdx.x)) b += s;
+  int b = 0, a = 0, c = 0, live, before, below;
+  if constexpr (DIRECT) {
+#pragma unroll 8
+    for (int page = threadIdx.x; page < A.num_pages; page += kThreads) {
+      const int used = A.refs[page] > 0;
+      a += used;
+      if (page < static_cast<int>(blockIdx.x) * kPagesPerCta) b += used;
+    }
+  } else {
+    for (int i = threadIdx.x; i < blocks; i += kThreads) {
+      const int s = A.block_live[i];
+      a += s;
+      if (i < static_cast<int>(blockIdx.x)) b += s;
+    }
   }
   block_prefix(b, &before);
   block_prefix(a, &live);
-  const int edge = live / kPagesPerCta;
-  int c = 0, below;
+  const int edge = DIRECT ? 0 : live / kPagesPerCta;
   for (int i = threadIdx.x; i < edge; i += kThreads) c += A.block_live[i];
+#pragma unroll 8
   for (int page = edge * kPagesPerCta + threadIdx.x; page < live; page += kThreads) c += A.refs[page] > 0;
   block_prefix(c, &below);
   constexpr int kPer = kPagesPerCta / kThreads;
@@ -475,9 +492,15 @@ cudaError_t launch_compact(const CompactParams& p, void* workspace, cudaStream_t
   A.moves = A.block_live + blocks;
   A.movers = reinterpret_cast<int2*>(static_cast<char*>(workspace) + (4LL * (blocks + 1) + 15) / 16 * 16);
   A.holes = reinterpret_cast<int32_t*>(A.movers + A.num_pages / 2 + 1);
-  cudaError_t e = chained(compact_count_kernel, blocks, kThreads, 0, st, A);
-  if (e != cudaSuccess) return e;
-  e = chained(compact_plan_kernel, blocks, kThreads, 0, st, A, blocks);
+  cudaError_t e;
+  // (in place a CTA would count pages whose counts another one has written)
+  if (A.refs_out != A.refs && A.num_pages <= kDirectPages) {
+    e = chained(compact_plan_kernel<true>, blocks, kThreads, 0, st, A, blocks);
+  } else {
+    e = chained(compact_count_kernel, blocks, kThreads, 0, st, A);
+    if (e != cudaSuccess) return e;
+    e = chained(compact_plan_kernel<false>, blocks, kThreads, 0, st, A, blocks);
+  }
   if (e != cudaSuccess) return e;
   const int64_t per = (A.page_bytes + kPiece - 1) / kPiece;
   const int64_t items = A.num_pages / 2 * per + (static_cast<int64_t>(A.rows) * A.entries + 31) / 32;

@@ -35,6 +35,8 @@
  *     with kvarn_read_error_flags. After such a fault the outputs of that
  *     call are unspecified, but no out-of-bounds access is made.
  *   - Device pointers must be 16-byte aligned; the cache 128-byte aligned.
+ *   - A workspace belongs to one call at a time: calls that may overlap on the
+ *     GPU (two streams, two captured graphs) need workspaces of their own.
  *
  * Rotated basis. Codes and scales are stored in the rotated basis y = x H,
  * H the Sylvester Hadamard matrix in natural order scaled by 1/sqrt(D)

@@ -1006,14 +1006,17 @@ static int32_t norm_rope(const kvarn_norm_rope_tensor* tensors, int32_t num_tens
                                         t.dy_head_stride != t.out_head_stride))
         return KVARN_EINVAL;
     }
-    if ((t.dweight && (t.dweight == t.weight || t.dweight == t.out)) || (t.weight && t.weight == t.out)) return KVARN_EINVAL;
+    const void* dw = t.dweight;
+    if ((dw && (dw == t.weight || dw == t.out || dw == t.x || dw == t.dy)) || (t.weight && t.weight == t.out))
+      return KVARN_EINVAL;
     // a tensor is written while the others are read and written
     for (int32_t j = 0; j < p.num_tensors; ++j) {
       const NormTensor& o = p.t[j];
       if (t.num_heads && o.heads && (t.out == o.out || t.out == o.x || t.x == o.out)) return KVARN_EINVAL;
       if (t.num_heads && o.heads && backward && (t.out == o.dy || t.dy == o.out)) return KVARN_EINVAL;
-      if (t.dweight && (t.dweight == o.dw || t.dweight == o.w)) return KVARN_EINVAL;
-      if (o.dw && o.dw == t.weight) return KVARN_EINVAL;
+      if (dw && (dw == o.dw || dw == o.w || dw == o.x || dw == o.dy || dw == o.out)) return KVARN_EINVAL;
+      if (o.dw && (o.dw == t.weight || o.dw == t.x || o.dw == t.dy || o.dw == t.out)) return KVARN_EINVAL;
+      if ((t.weight && t.weight == o.out) || (o.w && o.w == t.out)) return KVARN_EINVAL;
     }
     p.t[p.num_tensors++] = {t.x,           t.dy,            t.out,          t.weight,        t.dweight,
                             t.x_seq_stride, t.x_token_stride, t.x_head_stride, t.dy_seq_stride, t.dy_token_stride,

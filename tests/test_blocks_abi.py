@@ -166,7 +166,9 @@ def test_norm_refusals(L, code, kw, back):
     (EINVAL, dict(dy=None)), (EINVAL, dict(ws=None)), (EALIGN, dict(ws=at(22, 8))), (EWORKSPACE, dict(size=3)), (EALIGN, dict(dweight=BASE + 2)),
     (EINVAL, dict(out=BASE + (2 << 20), out_head_stride=256, num_heads=2)), (EINVAL, dict(dweight=BASE + (4 << 20))),
     (EINVAL, dict(n=2, second=dict(dweight=BASE + (5 << 20)))), (EINVAL, dict(n=2, second=dict(dy=BASE + (3 << 20)))),
-    (EINVAL, dict(n=2, second=dict(weight=BASE + (5 << 20)))),
+    (EINVAL, dict(n=2, second=dict(weight=BASE + (5 << 20)))), (EINVAL, dict(dweight=BASE + (1 << 20))), (EINVAL, dict(dweight=BASE + (2 << 20))),
+    (EINVAL, dict(n=2, second=dict(dweight=BASE + (3 << 20)))), (EINVAL, dict(n=2, second=dict(x=BASE + (5 << 20)))),
+    (EINVAL, dict(n=2, second=dict(weight=BASE + (3 << 20)))),
 ])
 def test_norm_backward_refusals(L, code, kw):
     assert norm(L, back=True, **kw) == code

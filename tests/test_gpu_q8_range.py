@@ -1,0 +1,44 @@
+"""Attention over the 8-bit block cache at the ends of what its numbers may be: queries, keys, values and scales of any
+size in coded blocks and in the raw tail, scores of any size, sinks up to the largest length, waits that run out."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_kv_cache_kvarn_gb300 as kv
+from tests import blocks8 as b8
+from tests.test_gpu_q8 import check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from quantized_kv_cache_kvarn_gb300 import build
+    build.build()
+    kv.lib()
+
+
+def scaled(lens, Hq, Hkv, D, Q, k_power, v_power, q_power, seed):
+    """A bf16 batch whose keys, values and queries are a power of two of those of another one, the softmax's scale such
+    that the scores are the other one's (but for what queries lose below the smallest bf16 number)."""
+    x = b8.Batch(lens, Hq, Hkv, D, Q=Q, bf16=True, seed=seed)
+    for n, p in ((0, k_power), (4, v_power)):
+        at = slice(32 * D + n, 32 * D + n + 4)
+        s = np.ascontiguousarray(x.cache[..., at]).view(np.float32) * np.float32(2.0 ** p)
+        x.cache[..., at] = s.view(np.uint8)
+    x.tails[0] *= np.float32(2.0 ** k_power)
+    x.tails[1] *= np.float32(2.0 ** v_power)
+    x.q = torch.from_numpy(x.q.astype(np.float64) * 2.0 ** q_power).to(torch.bfloat16).float().numpy()
+    x.k, x.v = [k * 2.0 ** k_power for k in x.k], [v * 2.0 ** v_power for v in x.v]
+    x.sm = float(np.float32(x.sm * 2.0 ** (-k_power - q_power)))
+    return x
+
+
+HEADS = [(4, 1, 128, 1), (8, 1, 128, 3), (3, 1, 256, 1), (6, 1, 256, 3)]  # Hq, Hkv, D, Q: eight rows and sixteen
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,Q", HEADS[::2])
+@pytest.mark.parametrize("k_power,q_power", [(122, 0), (122, -100), (120, -126), (-95, 110), (-90, 0), (60, -126), (0, -128), (0, 123)])
+def test_scores_of_blocks_of_any_size(k_power, q_power, Hq, Hkv, D, Q):
+    """Without a tail."""
+    check(scaled([320, 48], Hq, Hkv, D, Q, k_power, 0, q_power, 7).gpu(kv))

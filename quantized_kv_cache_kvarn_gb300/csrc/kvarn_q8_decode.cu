@@ -59,6 +59,11 @@ namespace kvarn {
 namespace {
 
 constexpr float kOff = 12.f;  // exponent of the weights' operands over mt
+// Raw rows are any bf16 numbers, up to 2^128. Products of keys beyond 2^105 may
+// add up past a float, which those with the queries at 2^-26 of their scaled size
+// do not (at most 2^(15 - 26 + 128 + 8)). Values go in with weights of at most
+// 2^-6, so that those of 22 tokens add up to a float.
+constexpr float kRawQ = 0x1p-26f, kRawUp = kOff + 6.f;
 
 struct Q8Args {
   const void* q;
@@ -474,13 +479,15 @@ struct Rows {
   }
 
   // Raw tokens of the tail in fp32, n <= 16 rows of the stage: token 8 e + 2 t +
-  // j for row r at s[8 r + 2 e + j]; four tokens at a time (rows behind the n-th
+  // j for row r at s[8 r + 2 e + j], without the row's and the softmax's scales;
+  // queries times kRawQ where SMALL. Four tokens at a time (rows behind the n-th
   // are hidden afterwards).
-  __device__ __forceinline__ void raw_scores(const Q8Args& A, const uint16_t* K, int n, float (&s)[R]) const {
+  template <bool SMALL>
+  __device__ __forceinline__ void raw_products(const Q8Args& A, const uint16_t* K, int n, float (&s)[R]) const {
     const int t = threadIdx.x & 3;
 #pragma unroll
     for (int x = 0; x < R; ++x) s[x] = 0.f;
-#pragma unroll 4
+#pragma unroll(SMALL && NR == 2 ? 1 : 4)
     for (int i = 0; i < ((n + 3) & ~3); ++i) {
       float d[NR];
 #pragma unroll
@@ -493,8 +500,12 @@ struct Rows {
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            const float2 a = __half22float2(u32_as_h2(q[4 * c + k][2 * r]));
-            const float2 b = __half22float2(u32_as_h2(q[4 * c + k][2 * r + 1]));
+            float2 a = __half22float2(u32_as_h2(q[4 * c + k][2 * r]));
+            float2 b = __half22float2(u32_as_h2(q[4 * c + k][2 * r + 1]));
+            if constexpr (SMALL) {
+              a = f2mul(a, f2(kRawQ));
+              b = f2mul(b, f2(kRawQ));
+            }
             d[r] = fmaf(a.x, f[4 * k], d[r]);
             d[r] = fmaf(a.y, f[4 * k + 1], d[r]);
             d[r] = fmaf(b.x, f[4 * k + 2], d[r]);
@@ -507,14 +518,39 @@ struct Rows {
         d[r] += __shfl_xor_sync(0xffffffffu, d[r], 2);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (i == 8 * (x >> 1) + 2 * t + (x & 1)) s[8 * r + x] = d[r] * A.scale_log2 * qi[r];
+          if (i == 8 * (x >> 1) + 2 * t + (x & 1)) s[8 * r + x] = d[r];
       }
     }
   }
 
+  __device__ __forceinline__ void raw_scores(const Q8Args& A, const uint16_t* K, int n, float (&s)[R]) const {
+    // a large scale comes before the row's power of two, a small one after it: what lies between is a float
+    const bool large = fabsf(A.scale_log2) >= 1.f;
+    float before = large ? A.scale_log2 : 1.f;
+    const float after = (large ? 1.f : A.scale_log2) * (1.f / kRawQ);
+    if constexpr (NR == 1) {
+      raw_products<true>(A, K, n, s);
+    } else {  // the factor on sixteen rows' queries costs more than a look at the products
+      raw_products<false>(A, K, n, s);
+      const int t = threadIdx.x & 3;
+      bool fine = true;
+#pragma unroll
+      for (int x = 0; x < R; ++x)
+        if ((x & 7) < 4) fine = fine && (8 * (x >> 1 & 1) + 2 * t + (x & 1) >= n || fabsf(s[x]) < INFINITY);
+      if (__builtin_expect(__any_sync(0xffffffffu, !fine), 0))
+        raw_products<true>(A, K, n, s);
+      else
+        before *= kRawQ;
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[8 * r + x] = s[8 * r + x] * before * qi[r] * after;
+  }
+
   __device__ __forceinline__ void add_raw(const Q8Args& A, const uint16_t* V, int token0, int n, const float (&s)[R]) {
     const int lane = threadIdx.x & 31, t = lane & 3;
-    float w[NR][4], ms[NR];
+    float w[NR][4], ms[NR], mts[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       ms[r] = -INFINITY;
@@ -524,8 +560,9 @@ struct Rows {
         w[r][x] = i < n && sees(A, r, token0 + i) ? s[8 * r + x] : -INFINITY;
         ms[r] = fmaxf(ms[r], w[r][x]);
       }
+      mts[r] = ms[r] + kRawUp;
     }
-    raise(ms, ms);
+    raise(ms, mts);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       float2 sum = f2(0.f);

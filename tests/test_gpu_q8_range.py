@@ -24,7 +24,8 @@ def scaled(lens, Hq, Hkv, D, Q, k_power, v_power, q_power, seed):
     x = b8.Batch(lens, Hq, Hkv, D, Q=Q, bf16=True, seed=seed)
     for n, p in ((0, k_power), (4, v_power)):
         at = slice(32 * D + n, 32 * D + n + 4)
-        s = np.ascontiguousarray(x.cache[..., at]).view(np.float32) * np.float32(2.0 ** p)
+        with np.errstate(over="ignore"):  # pages that hold no block hold any bytes
+            s = np.ascontiguousarray(x.cache[..., at]).view(np.float32) * np.float32(2.0 ** p)
         x.cache[..., at] = s.view(np.uint8)
     x.tails[0] *= np.float32(2.0 ** k_power)
     x.tails[1] *= np.float32(2.0 ** v_power)
@@ -42,3 +43,12 @@ HEADS = [(4, 1, 128, 1), (8, 1, 128, 3), (3, 1, 256, 1), (6, 1, 256, 3)]  # Hq, 
 def test_scores_of_blocks_of_any_size(k_power, q_power, Hq, Hkv, D, Q):
     """Without a tail."""
     check(scaled([320, 48], Hq, Hkv, D, Q, k_power, 0, q_power, 7).gpu(kv))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,Q", HEADS)
+@pytest.mark.parametrize("k_power,v_power,q_power", [(122, 0, 0), (122, 0, -100), (-95, 0, 110), (0, 123, 0), (0, -90, 0), (110, 120, -126),
+                                                     (122, 123, -122), (0, 0, 123), (0, 0, -128)])
+@pytest.mark.parametrize("lens", [[13, 15, 1], [333, 50, 9]])
+def test_raw_tails_of_any_size(lens, k_power, v_power, q_power, Hq, Hkv, D, Q):
+    """Tails alone, and behind coded blocks of the same sizes."""
+    check(scaled(lens, Hq, Hkv, D, Q, k_power, v_power, q_power, 9).gpu(kv))

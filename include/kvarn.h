@@ -776,7 +776,9 @@ int32_t kvarn_q8_append(const void* k, const void* v, const int32_t* seq_lens, i
  *   out, lse       as kvarn_decode_verify
  *   workspace      >= kvarn_q8_decode_workspace_bytes(...)
  * A query that sees no token gives out = 0 and lse = -inf. Values of hidden
- * tokens do not matter, whatever they are. At most 8 query heads per KV head;
+ * tokens do not matter, whatever they are. Queries, keys, values and scales may
+ * be of any size whose scores, sm_scale log2(e) q . k, stay below 2^27 in
+ * magnitude. At most 8 query heads per KV head;
  * num_seqs * Q * num_q_heads is at most 2^30. seq_lens outside [0,
  * max_seq_len] set KVARN_DEVERR_SEQ_LEN and are clamped. The sums are taken in
  * a fixed order: the same call gives the same bits.

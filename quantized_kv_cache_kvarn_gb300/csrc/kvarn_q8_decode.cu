@@ -28,7 +28,9 @@
 // m of s for the sum of the weights, and mt of s + e, 2^e the power of two in
 // the block's V scale, for the output, so that blocks of any scales add up
 // without leaving fp16's range: the operand is 2^(s + e - mt + 12) times the
-// scale's mantissa, and a weight counts down to 2^-36 of the largest share.
+// scale's mantissa, and a weight counts down to 2^-36 of the largest share. Both
+// are floats, so beyond scores of 2^24 (fp32 counts in twos there) mt is rounded
+// up, by at most the step of the score: at 2^27 that leaves the weights 20 bits.
 //
 // At head_dim 256 two warps share an item, 128 channels each (one warp's output
 // alone would take 128 registers a thread): they add each other's scores by way
@@ -164,8 +166,7 @@ __device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// x as fp16 hi + lo, saturated: fp32 rounds s + ev - mt of scores beyond 2^24,
-// and 2^(kOff + 1) may be passed by more than fp16 holds.
+// x as fp16 hi + lo (the weights stay below 2^(kOff + 1), so nothing saturates).
 __device__ __forceinline__ void split_sat(float2 x, uint32_t& hi, uint32_t& lo) {
   asm("cvt.rn.satfinite.f16x2.f32 %0, %2, %1;" : "=r"(hi) : "f"(x.x), "f"(x.y));
   const float2 r = f2fma(__half22float2(u32_as_h2(hi)), f2(-1.f), x);
@@ -302,9 +303,10 @@ struct Rows {
 
   // Two scores of a row to their weights for the sum, 2^(s - m), and for the
   // output, 2^(s + ev - mt + kOff) vm with 2^ev vm the V scale; cm = -m and ct =
-  // ev - mt + kOff of the row. The output's are below 2^(kOff + 1).
+  // (m - mt) + ev + kOff of the row: s - m comes first, so that scores of more
+  // than 24 bits lose nothing. The output's are below 2^(kOff + 1).
   static __device__ __forceinline__ float2 weigh(float2 s, float cm, float ct, float vm, float2& sum) {
-    const float2 x = f2add(s, f2(cm)), y = f2add(s, f2(ct));
+    const float2 x = f2add(s, f2(cm)), y = f2add(x, f2(ct));
     sum = f2add(sum, make_float2(ex2(x.x), ex2(x.y)));
     return f2mul(make_float2(ex2(y.x), ex2(y.y)), f2(vm));
   }
@@ -395,14 +397,14 @@ struct Rows {
       for (int p = 0; p < 2; ++p)
         top[p] = fmaxf(fmaxf(s[8 * r + 4 * p], s[8 * r + 4 * p + 1]), fmaxf(s[8 * r + 4 * p + 2], s[8 * r + 4 * p + 3]));
       ms[r] = fmaxf(top[0], top[1]);
-      mts[r] = fmaxf(top[0] + ev[0], top[1] + ev[1]);
+      mts[r] = fmaxf(__fadd_ru(top[0], ev[0]), __fadd_ru(top[1], ev[1]));  // a bound of every share
     }
     raise(ms, mts);
     float2 w[NR][2][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       float2 sum = f2(0.f);
-      const float cm = -base(m[r]), ct = kOff - base(mt[r]);
+      const float cm = -base(m[r]), ct = kOff + (base(m[r]) - base(mt[r]));
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -560,13 +562,13 @@ struct Rows {
         w[r][x] = i < n && sees(A, r, token0 + i) ? s[8 * r + x] : -INFINITY;
         ms[r] = fmaxf(ms[r], w[r][x]);
       }
-      mts[r] = ms[r] + kRawUp;
+      mts[r] = __fadd_ru(ms[r], kRawUp);
     }
     raise(ms, mts);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       float2 sum = f2(0.f);
-      const float cm = -base(m[r]), ct = kOff - base(mt[r]);
+      const float cm = -base(m[r]), ct = kOff + (base(m[r]) - base(mt[r]));
 #pragma unroll
       for (int x = 0; x < 4; x += 2) {
         const float2 v = weigh(make_float2(w[r][x], w[r][x + 1]), cm, ct, 1.f, sum);

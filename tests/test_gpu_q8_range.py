@@ -52,3 +52,31 @@ def test_scores_of_blocks_of_any_size(k_power, q_power, Hq, Hkv, D, Q):
 def test_raw_tails_of_any_size(lens, k_power, v_power, q_power, Hq, Hkv, D, Q):
     """Tails alone, and behind coded blocks of the same sizes."""
     check(scaled(lens, Hq, Hkv, D, Q, k_power, v_power, q_power, 9).gpu(kv))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,Q", HEADS)
+@pytest.mark.parametrize("power", [20, 22, 24])
+@pytest.mark.parametrize("lens", [[320, 64], [13, 7], [333, 50]])
+def test_scores_beyond_what_fp32_counts(lens, power, Hq, Hkv, D, Q):
+    """Scores of 2^24 and more, which fp32 holds in steps of two and more: where one token is ahead of the others by more
+    than what scores may be off by, the output is its value (the weight is hi + lo and the scale's mantissa a product:
+    2^-20 of it) and the lse its score."""
+    x = b8.Batch([L + Q - 1 for L in lens], Hq, Hkv, D, Q=Q, seed=3)
+    x.sm *= 2.0 ** power
+    x.gpu(kv)
+    out, lse = (t.cpu().numpy().astype(np.float64) for t in x.decode(kv))
+    assert kv.read_error_flags(x.t["err"]) == 0
+    seen = 0
+    for b, L in enumerate(x.lens):
+        for j in range(Q):
+            for h in range(Hq):
+                k, v, q = x.k[b][h // (Hq // Hkv)][:L - Q + j + 1], x.v[b][h // (Hq // Hkv)], x.q[b, j, h].astype(np.float64)
+                s = x.sm * (k @ q)
+                off = x.sm * (D / 2 + 4) * 2.0 ** -23 * (np.abs(k) @ np.abs(q))
+                i = int(s.argmax())
+                if len(s) > 1 and s[i] - off[i] - 200 <= np.delete(s + off, i).max():
+                    continue
+                seen += abs(s[i]) > 2.0 ** (power + 1)
+                assert (np.abs(out[b, j, h] - v[i]) <= 2.0 ** -20 * np.abs(v[i])).all(), (b, j, h, s[i])
+                assert abs(lse[b, j, h] - s[i]) <= off[i] + 2.0 ** -22 * abs(s[i])
+    assert seen >= Q

@@ -876,8 +876,9 @@ int32_t kvarn_norm_rope_backward(const kvarn_norm_rope_tensor* tensors, int32_t 
  *
  * page_refs_out[p] = page_refs[p] - the times that old rows name p + the times
  * that new rows do: references of others than these rows stay. freed: the
- * pages whose count fell from above 0 to 0, ascending, then -1 up to entry
- * num_pages; freed_count[0] of them.
+ * pages whose count fell from above 0 to 0 (or below, where the counts did not
+ * agree with the rows), ascending, then -1 up to entry num_pages;
+ * freed_count[0] of them.
  *
  *   parents        device int32 [num_out]; num_in, num_out at most 32768
  *   seq_lens       device int32 [num_in]; outside [0, max_seq_len]: sets

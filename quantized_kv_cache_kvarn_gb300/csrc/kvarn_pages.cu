@@ -7,10 +7,11 @@
 // dependents:
 //   copy   tails (live rows), lengths, tables; the counts to their new place
 //   count  an old row's pages by (children that keep them) - 1, nothing where
-//          that is 0; a page whose count falls to 0 sets its bit in a bitmap
-//          kept where the list of freed pages will be
+//          that is 0; a page whose count passes between above 0 and not above
+//          turns its bit in a bitmap kept where the list of freed pages will be
 //   list   one cluster turns the bitmap into the list, in order
-// The counts are whole numbers, so the order of the atomics does not matter.
+// The counts are whole numbers and a bit says how often a count has passed, odd
+// or even, so the order of the atomics does not matter, whatever the counts.
 //
 // Compact. n live pages move to the lowest ids: the k-th free page below n
 // (a hole) receives the k-th live page at or above n. Up to three kernels: live
@@ -223,8 +224,8 @@ __global__ void __launch_bounds__(kThreads) fork_count_kernel(const __grid_const
     for (int k = 0; k < kEntries / 32; ++k) old[k] = id[k] >= 0 ? atomicAdd(A.refs_out + id[k], d[k]) : 0;
 #pragma unroll
     for (int k = 0; k < kEntries / 32; ++k)
-      if (id[k] >= 0 && old[k] > 0 && old[k] + d[k] <= 0)
-        atomicOr(A.freed + (id[k] >> 5), static_cast<int>(1u << (id[k] & 31)));
+      if (id[k] >= 0 && (old[k] > 0) != (old[k] + d[k] > 0))
+        atomicXor(A.freed + (id[k] >> 5), static_cast<int>(1u << (id[k] & 31)));
   }
   // the list kernel may start once every CTA is here, and waits for the end
   if (!waited) pdl_wait_primary();
@@ -256,8 +257,8 @@ __global__ void __cluster_dims__(kListCtas, 1, 1) __launch_bounds__(kListThreads
     for (int j = 0; j < kWords; ++j) {
       const int i = i0 + j * kListThreads;
       if (i >= n) break;
-      // a count may have passed through 0 on its way where the counts did not
-      // agree with the rows: what it came to decides
+      // of the counts that ended on the other side than they began, those that
+      // are not above 0 now
       uint32_t b = word[j], keep = 0;
       while (b) {
         int bit[4], refs[4];

@@ -128,7 +128,7 @@ struct Seq {
     wp = C;
     if (A.window > 0) {
       wp = min(C, max(0, L - A.Q + 1 - A.window) / kPageTokens);
-      sp = min(C, (A.sinks + kPageTokens - 1) / kPageTokens);
+      sp = min(C, A.sinks / kPageTokens + (A.sinks % kPageTokens != 0));
       if (sp >= wp) sp = wp = C;
     }
     np = sp + C - wp;

@@ -1,5 +1,7 @@
 """Attention over the 8-bit block cache at the ends of what its numbers may be: queries, keys, values and scales of any
 size in coded blocks and in the raw tail, scores of any size, sinks up to the largest length, waits that run out."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -80,3 +82,19 @@ def test_scores_beyond_what_fp32_counts(lens, power, Hq, Hkv, D, Q):
                 assert (np.abs(out[b, j, h] - v[i]) <= 2.0 ** -20 * np.abs(v[i])).all(), (b, j, h, s[i])
                 assert abs(lse[b, j, h] - s[i]) <= off[i] + 2.0 ** -22 * abs(s[i])
     assert seen >= Q
+
+
+@pytest.mark.parametrize("sinks", [(1 << 31) - 16, (1 << 31) - 15, (1 << 31) - 1])
+def test_sinks_up_to_the_largest_length(sinks):
+    """max_seq_len of 2^31 - 1: every token is one of the sinks."""
+    x = b8.Batch([100, ], 4, 1, 128, seed=2).gpu(kv)
+    t, most = x.t, (1 << 31) - 1
+    P = ctypes.c_void_p
+    # the table's row is as long as the stride says; entries behind the sequence's blocks are not read
+    code = kv.lib().kvarn_q8_decode(P(t["q"].data_ptr()), 4, 1, x.sm, P(t["cache"].data_ptr()), ctypes.byref(x.layout), x.code,
+                                    P(t["table"].data_ptr()), most // 16, P(t["lens"].data_ptr()), most, P(t["tail_k"].data_ptr()),
+                                    P(t["tail_v"].data_ptr()), t["tail_k"].shape[2], 20, sinks, 1, P(t["out"].data_ptr()),
+                                    P(t["lse"].data_ptr()), P(t["space"].data_ptr()), t["space"].numel(), P(t["err"].data_ptr()),
+                                    P(torch.cuda.current_stream().cuda_stream))
+    assert code == 0
+    check(x, t["out"], t["lse"])

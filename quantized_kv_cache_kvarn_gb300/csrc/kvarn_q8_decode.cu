@@ -778,10 +778,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q8_decode_kernel(const __grid_
       if (half == 0 && !dead && k > 0 && issued < count) issue();
     }
     if (dead) {
-      // give up: the copies under way have to land before the CTA leaves
+      // give up: the copies under way have to land before the CTA leaves, which
+      // the warp that asked for them sees to (the other does not know how many
+      // they are, and a stage that was not asked for would hold it to the limit)
       if (!came) set_error(A.err, KVARN_DEVERR_TIMEOUT);
-      for (int j = k; j < min(count, k + kStages); ++j)
-        if (half != 0 || j < issued) mbar_wait_bounded(bar + j % kStages, (j / kStages) & 1, 100000000LL);
+      if (half == 0)
+        for (int j = k; j < issued; ++j) mbar_wait_bounded(bar + j % kStages, (j / kStages) & 1, 100000000LL);
       return;
     }
     if (paged)

@@ -98,3 +98,46 @@ def test_sinks_up_to_the_largest_length(sinks):
                                     P(torch.cuda.current_stream().cuda_stream))
     assert code == 0
     check(x, t["out"], t["lse"])
+
+
+def test_a_pair_that_gives_up_leaves_at_once():
+    """At head_dim 256 two warps share an item; where one's wait runs out both leave as soon as the copies that were asked
+    for have landed, long before the 1e8 cycles (48 ms) that a copy that never comes would be waited for."""
+    B, Hq, Hkv, D, L = 16, 8, 2, 256, 16384
+    pages = B * L // 16  # 270 MB: pages come from memory, and waits are long wherever a warp is
+    g = torch.Generator(device="cuda").manual_seed(0)
+    lay = kv.q8_layout(D, Hkv, pages)
+    cache = torch.randint(0, 100, (pages, Hkv, kv.q8_page_bytes(lay)), generator=g, device="cuda", dtype=torch.uint8)
+    cache[..., 32 * D:] = torch.tensor([0.01, 0.01] + [0.0] * 6, device="cuda").view(torch.uint8)
+    table = torch.randperm(pages, generator=g, device="cuda").int().view(B, L // 16)
+    lens, err = torch.full((B,), L, dtype=torch.int32, device="cuda"), kv.new_error_word()
+    q = torch.randn((B, 1, Hq, D), generator=g, device="cuda").half()
+    out = torch.empty((B, 1, Hq, D), device="cuda")
+    space = torch.empty(kv.q8_decode_workspace_bytes(lay, B, Hq, 1, L), dtype=torch.uint8, device="cuda")
+
+    def call():
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        kv.q8_decode(q, lay, 0, cache, table, lens, L, out, space, err, D ** -0.5)
+        b.record()
+        torch.cuda.synchronize()
+        flags = kv.read_error_flags(err)
+        err.zero_()
+        return a.elapsed_time(b), flags
+
+    for _ in range(3):
+        assert call()[1] == 0
+    first = out.clone()
+    assert first.isfinite().all()
+    gave_up, slowest = 0, 0.0
+    try:
+        for cycles in (1, 50, 200, 500, 1000, 2000, 3000, 5000, 8000):
+            kv.set_copy_wait_test(cycles)
+            for _ in range(5):
+                ms, flags = call()
+                assert flags == kv.DEVERR_TIMEOUT or (flags == 0 and torch.equal(out, first))
+                gave_up, slowest = gave_up + (flags != 0), max(slowest, ms)
+    finally:
+        kv.set_copy_wait_test(0)
+    assert gave_up > 0 and slowest < 20, (gave_up, slowest)
+    assert call()[1] == 0 and torch.equal(out, first)

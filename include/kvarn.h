@@ -809,7 +809,8 @@ int32_t kvarn_q8_decode(const void* q, int32_t num_q_heads, int32_t num_queries,
  * kvarn_norm_rope_backward takes the same x and the gradient dy of the output
  * and gives dx and, where dweight is not NULL, the gradient of the weights,
  * summed over tokens and heads (fp32, overwritten; the sums are taken in a
- * fixed order, the same call gives the same bits).
+ * fixed order, the same call gives the same bits; at most 128 terms are added up
+ * in a row in fp32, so sizes whose parts pass 2^31 - 1 are KVARN_EUNSUPPORTED).
  *
  *   tensors      host array of 1 .. KVARN_ROPE_MAX_TENSORS tensors that share
  *                positions and D (queries and keys). Element (b, n, h, d) of

@@ -980,6 +980,8 @@ static int32_t norm_rope(const kvarn_norm_rope_tensor* tensors, int32_t num_tens
   }
   const int64_t tokens = static_cast<int64_t>(num_seqs) * num_tokens;
   if (heads > (1 << 20) || tokens > (1 << 30)) return KVARN_EUNSUPPORTED;
+  const int64_t space = backward ? norm_rope_workspace_bytes(num_tensors, every, head_dim, tokens) : 0;
+  if (space < 0) return KVARN_EUNSUPPORTED;
   // the gradient of the weights over no tokens or heads is still written
   if ((tokens == 0 || heads == 0) && !sums) return KVARN_OK;
   if (rope_dim > 0 && tokens > 0 && (!positions || !inv_freq)) return KVARN_EINVAL;
@@ -1025,7 +1027,7 @@ static int32_t norm_rope(const kvarn_norm_rope_tensor* tensors, int32_t num_tens
   if (sums) {
     if (!workspace && tokens > 0 && heads > 0) return KVARN_EINVAL;
     if (!aligned(workspace, 16)) return KVARN_EALIGN;
-    if (workspace_bytes < norm_rope_workspace_bytes(num_tensors, every, head_dim, tokens)) return KVARN_EWORKSPACE;
+    if (workspace_bytes < space) return KVARN_EWORKSPACE;
   }
   p.dim = head_dim;
   p.dtype = dtype;

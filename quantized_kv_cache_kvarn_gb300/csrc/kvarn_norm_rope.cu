@@ -29,13 +29,17 @@ namespace {
 constexpr int kThreads = 256;
 
 // Work of a launch: tiles of `tok` tokens of each tensor, `per` consecutive
-// tiles to a CTA, CTAs [cta0[k], cta0[k + 1]) for tensor k.
+// tiles to a CTA, CTAs [cta0[k], cta0[k + 1]) for tensor k. Backward, heads are
+// shared out too: CTA i of a tensor takes span i % spans of `span` heads.
 struct NormPlan {
   int32_t cta0[kRopeMaxTensors + 1];
   int32_t tok[kRopeMaxTensors];
   int32_t per[kRopeMaxTensors];
+  int32_t span[kRopeMaxTensors];
+  int32_t spans[kRopeMaxTensors];
   int32_t lanes;  // of a head's group (vector path)
 };
+constexpr int kMaxRounds = 128;  // terms of the weights' gradient that are added up in a row
 
 __device__ __forceinline__ float weight_at(const void* w, int dtype, int i) {
   if (!w) return 1.f;
@@ -116,9 +120,11 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
   // A round is one head of every group's token; the rounds of all the CTA's
   // tiles are asked for in one sequence, DEPTH ahead, each lane its own
   // vectors into its own slots: no barrier, and nothing held in registers.
-  const int per = BACK ? P.per[k] : 1;  // forward: one tile
-  const int tile0 = (static_cast<int>(blockIdx.x) - P.cta0[k]) * per;
-  const int rounds = (t.heads + slots - 1) / slots;  // of a tile
+  const int per = BACK ? P.per[k] : 1;  // forward: one tile, all heads
+  const int cta = static_cast<int>(blockIdx.x) - P.cta0[k], spans = BACK ? P.spans[k] : 1;
+  const int tile0 = (BACK ? cta / spans : cta) * per;
+  const int h0 = BACK ? cta % spans * P.span[k] : 0, heads = BACK ? min(P.span[k], t.heads - h0) : t.heads;
+  const int rounds = (heads + slots - 1) / slots;  // of a tile
   int ahead_tile = tile0, ahead_left = rounds, ahead_mine = 0, slot = 0;
   const T* ahead_x = nullptr;
   const T* ahead_g = nullptr;
@@ -129,9 +135,9 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
     ahead_g = static_cast<const T*>(t.dy);
     if (tile < tile0 + per && n < tokens && on) {
       const int seq = n / A.num_tokens, pos_in = n % A.num_tokens;
-      ahead_x += seq * t.x_seq + pos_in * t.x_tok + hs * t.x_head + first;
-      if (BACK) ahead_g += seq * t.g_seq + pos_in * t.g_tok + hs * t.g_head + first;
-      ahead_mine = (t.heads - hs + slots - 1) / slots;
+      ahead_x += seq * t.x_seq + pos_in * t.x_tok + (h0 + hs) * t.x_head + first;
+      if (BACK) ahead_g += seq * t.g_seq + pos_in * t.g_tok + (h0 + hs) * t.g_head + first;
+      ahead_mine = (heads - hs + slots - 1) / slots;
     }
   };
   at_tile(tile0);
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
       cv[e] = make_float2(v.x, v.z);
       sv[e] = make_float2(v.y, v.w);
     }
-    T* dst = static_cast<T*>(t.out) + seq * t.o_seq + pos_in * t.o_tok + hs * t.o_head + first;
+    T* dst = static_cast<T*>(t.out) + seq * t.o_seq + pos_in * t.o_tok + (h0 + hs) * t.o_head + first;
     const int64_t o_step = slots * t.o_head;
     // Every lane of the CTA makes every round, so that the sums' exchanges are
     // those of whole warps.
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
         ba[e] = f2mul(wa[e], sv[e]);
         bb[e] = f2mul(wb[e], cv[e]);
       }
-      for (int h = hs; h - hs < t.heads; h += slots) {
+      for (int h = hs; h - hs < heads; h += slots) {
         uint4 v[VECS];
         take(v);
         float f[2 * N];
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
         for (int e = 0; e < M; ++e) s2 = f2fma(fa[e], fa[e], f2fma(fb[e], fb[e], s2));
         const float2 rs = f2(rsqrtf(fmaf(group_sum(s2.x + s2.y), inv_dim, A.eps)));
         refill();
-        if (live && h < t.heads) {
+        if (live && h < heads) {
           float2 ya[M], yb[M];
 #pragma unroll
           for (int e = 0; e < M; ++e) {
@@ -256,9 +262,9 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
         dst += o_step;
       }
     } else {
-      for (int h = hs; h - hs < t.heads; h += slots) {
+      for (int h = hs; h - hs < heads; h += slots) {
         uint4 v[VECS];
-        const bool here = live && h < t.heads;
+        const bool here = live && h < heads;
         take(v);
         float f[2 * N];
         float2 xa[M], xb[M], ga[M], gb[M], s2 = f2(0.f), q2 = f2(0.f);
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBackCtas : kFwdCtas)
         }
         refill();
         const float root = rsqrtf(fmaf(ss, inv_dim, A.eps));
-        const float rs1 = n0 + tt < tokens && h < t.heads ? root : 0.f;  // no row: nothing, even with eps 0
+        const float rs1 = n0 + tt < tokens && h < heads ? root : 0.f;  // no row: nothing, even with eps 0
         const float m = qs * rs1 * inv_dim;  // (u . h) / D
         const float2 rs = f2(rs1), mm = f2(-m);
 #pragma unroll
@@ -350,10 +356,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
     for (int d = lane; d < A.dim; d += 32) mine[d] = 0.f;
   __syncwarp();
   const int tokens = A.num_seqs * A.num_tokens;
-  const int64_t n0 = static_cast<int64_t>(static_cast<int>(blockIdx.x) - P.cta0[k]) * P.per[k] * tok;
+  const int cta = static_cast<int>(blockIdx.x) - P.cta0[k];
+  const int64_t n0 = static_cast<int64_t>(cta / P.spans[k]) * P.per[k] * tok;
   const int64_t n1 = min(static_cast<int64_t>(tokens), n0 + static_cast<int64_t>(P.per[k]) * tok);
-  for (int64_t i = n0 * t.heads + warp; i < n1 * t.heads; i += kThreads / 32) {
-    const int64_t n = i / t.heads, h = i % t.heads, seq = n / A.num_tokens, pos_in = n % A.num_tokens;
+  const int h0 = cta % P.spans[k] * P.span[k], heads = min(P.span[k], t.heads - h0);
+  for (int64_t i = n0 * heads + warp; i < n1 * heads; i += kThreads / 32) {
+    const int64_t n = i / heads, h = h0 + i % heads, seq = n / A.num_tokens, pos_in = n % A.num_tokens;
     const T* x = static_cast<const T*>(t.x) + seq * t.x_seq + pos_in * t.x_tok + h * t.x_head;
     const T* dy = static_cast<const T*>(t.dy) + (BACK ? seq * t.g_seq + pos_in * t.g_tok + h * t.g_head : 0);
     T* out = static_cast<T*>(t.out) + seq * t.o_seq + pos_in * t.o_tok + h * t.o_head;
@@ -439,37 +447,44 @@ __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const __grid_cons
   }
 }
 
-// Tiles and CTAs of every tensor. Forward a CTA takes one tile (several, with
-// their vectors asked for in one sequence, took 122 to 156 us where one takes
-// 106). Backward the CTAs fill the SMs once, shared out by the tensors' work (a
-// tile's rounds and about one more for its cosines and barriers), but none adds
-// up more than 128 rounds.
-NormPlan plan_norm(int num_tensors, const int32_t* heads, int dim, int64_t tokens, int lanes, bool backward) {
-  NormPlan P{};
+// Tiles and CTAs of every tensor; the number of CTAs, or -1 where a grid does not
+// hold them. Forward a CTA takes one tile (several, with their vectors asked for
+// in one sequence, took 122 to 156 us where one takes 106). Backward the CTAs
+// fill the SMs once, shared out by the tensors' work (a tile's rounds and about
+// one more for its cosines and barriers), but none adds up more than kMaxRounds
+// rounds: a tile of more heads than that is cut into spans of them.
+int64_t plan_norm(NormPlan& P, int num_tensors, const int32_t* heads, int dim, int64_t tokens, int lanes, bool backward) {
+  P = NormPlan{};
   P.lanes = lanes;
   const int groups = kThreads / lanes;
   const int64_t sms = device_sm_count();
-  int64_t tiles[kRopeMaxTensors], rounds[kRopeMaxTensors], all = 0;
+  int64_t tiles[kRopeMaxTensors], rounds[kRopeMaxTensors], all = 0, ctas = 0;
   for (int k = 0; k < num_tensors; ++k) {
     // tokens of a tile: as many as leave each group a head, halved while
     // fewer than four CTAs per SM remain
     int tok = 1;
     while (tok < 8 && tok * 2 <= groups && (tok * heads[k] < groups || (tokens + 2 * tok - 1) / (2 * tok) >= 4 * sms)) tok *= 2;
     P.tok[k] = tok;
+    const int slots = groups / tok;  // heads of a round
+    P.span[k] = backward ? std::min(heads[k], kMaxRounds * slots) : heads[k];
+    P.spans[k] = heads[k] ? (heads[k] + P.span[k] - 1) / P.span[k] : 1;
     tiles[k] = heads[k] ? (tokens + tok - 1) / tok : 0;
-    rounds[k] = (static_cast<int64_t>(heads[k]) * tok + groups - 1) / groups;
-    all += tiles[k] * (rounds[k] + 1);
+    rounds[k] = (P.span[k] + slots - 1) / slots;
+    all += tiles[k] * P.spans[k] * (rounds[k] + 1);
   }
   for (int k = 0; k < num_tensors; ++k) {
     int64_t per = 1;
     if (backward && tiles[k]) {
-      const int64_t want = std::max<int64_t>(1, 2 * sms * tiles[k] * (rounds[k] + 1) / all);
-      per = std::max<int64_t>(1, std::min<int64_t>((tiles[k] + want - 1) / want, 128 / std::max<int64_t>(1, rounds[k])));
+      const int64_t work = tiles[k] * P.spans[k];
+      const int64_t want = std::max<int64_t>(1, 2 * sms * work * (rounds[k] + 1) / all);
+      per = std::max<int64_t>(1, std::min<int64_t>((work + want - 1) / want, kMaxRounds / std::max<int64_t>(1, rounds[k])));
     }
     P.per[k] = static_cast<int32_t>(per);
-    P.cta0[k + 1] = P.cta0[k] + static_cast<int32_t>((tiles[k] + per - 1) / per);
+    ctas += (tiles[k] + per - 1) / per * P.spans[k];
+    if (ctas > 0x7fffffff) return -1;
+    P.cta0[k + 1] = static_cast<int32_t>(ctas);
   }
-  return P;
+  return ctas;
 }
 
 int vector_lanes(int dim, int n) {
@@ -517,8 +532,9 @@ cudaError_t launch(const NormParams& A, cudaStream_t st) {
     vec = vec && at % 16 == 0 && strides % N == 0;
   }
   // one warp per head: the plan of a group of 32
-  const NormPlan P = plan_norm(A.num_tensors, heads, A.dim, tokens, vec ? vector_lanes(A.dim, N) : 32, A.backward);
-  const unsigned ctas = P.cta0[A.num_tensors];
+  NormPlan P;
+  const int64_t ctas = plan_norm(P, A.num_tensors, heads, A.dim, tokens, vec ? vector_lanes(A.dim, N) : 32, A.backward);
+  if (ctas < 0) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaSuccess;
   if (ctas == 0) {
     // no heads or tokens: the sums over nothing
@@ -532,7 +548,7 @@ cudaError_t launch(const NormParams& A, cudaStream_t st) {
                         : run_lanes<T, 32>(A, P, rest, st);
   } else {
     const int smem = A.backward ? kThreads / 32 * A.dim * 4 : 0;
-    e = chained(A.backward ? norm_rope_any_kernel<T, true> : norm_rope_any_kernel<T, false>, dim3(ctas), kThreads, smem, st, A, P);
+    e = chained(A.backward ? norm_rope_any_kernel<T, true> : norm_rope_any_kernel<T, false>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, st, A, P);
   }
   if (e != cudaSuccess || !sums) return e;
   return chained(norm_weight_sum_kernel, dim3((A.dim + 31) / 32, A.num_tensors), 1024, 0, st, A, P);
@@ -540,12 +556,17 @@ cudaError_t launch(const NormParams& A, cudaStream_t st) {
 
 }  // namespace
 
-// One row of `dim` per CTA, of the plan with the most CTAs.
+// One row of `dim` per CTA, of the plan with the most CTAs; -1 where a plan has
+// more than a grid.
 int64_t norm_rope_workspace_bytes(int32_t num_tensors, const int32_t* heads, int32_t dim, int64_t tokens) {
-  int64_t ctas = 0;
-  for (int lanes = 4; lanes <= 32; lanes *= 2)
-    ctas = std::max<int64_t>(ctas, plan_norm(num_tensors, heads, dim, tokens, lanes, true).cta0[num_tensors]);
-  return ctas * dim * 4;
+  int64_t most = 0;
+  for (int lanes = 4; lanes <= 32; lanes *= 2) {
+    NormPlan P;
+    const int64_t ctas = plan_norm(P, num_tensors, heads, dim, tokens, lanes, true);
+    if (ctas < 0) return -1;
+    most = std::max(most, ctas);
+  }
+  return most * dim * 4;
 }
 
 cudaError_t launch_norm_rope(const NormParams& A, cudaStream_t st) {

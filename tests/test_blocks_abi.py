@@ -352,3 +352,12 @@ def test_binding_of_pages(calls):
                  (cache, i(10), i(2, 3), i(10), i(2, 3), i(10), i(2))):
         refused(calls, kv.compact_pages, *args, ws, err)
     assert calls == ["kvarn_fork_sequences", "kvarn_compact_pages", "kvarn_compact_pages"]
+
+
+def test_norm_gradient_of_more_heads_than_a_grid_holds(L):
+    """The weights' gradient adds up at most 128 heads of a group in a row, so that tokens times heads are limited."""
+    most = dict(B=1 << 20, S=1 << 10, D=8, R=0, num_heads=1 << 20)
+    assert norm(L, back=True, **most) == EUNSUPPORTED
+    heads = (ctypes.c_int32 * 1)(1 << 20)
+    assert L.kvarn_norm_rope_backward_workspace_bytes(heads, 1, 8, 1 << 20, 1 << 10) == -1
+    assert L.kvarn_norm_rope_backward_workspace_bytes(heads, 1, 8, 1, 64) > 0

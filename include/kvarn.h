@@ -730,6 +730,10 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
  * completes a block, which is coded into its page from the tail's 15 rows and
  * the token (the tail is then free). A length of 0 skips the sequence. The
  * decision is taken on the device.
+ * Drafted tokens under verification are raw rows that the caller writes: with n
+ * tokens appended, the next ones go to rows n % 16 .. of the tail (kvarn_q8_decode
+ * with Q queries then has lengths of n + Q - 1), and the accepted ones are
+ * appended, one call each, which puts them where they are or completes a block.
  *   k, v         device, kv_dtype [num_seqs][Hkv][D]
  *   tail_k/v     device, kv_dtype [num_seqs][Hkv][tail_capacity][D],
  *                tail_capacity >= 15

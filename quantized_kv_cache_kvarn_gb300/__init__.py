@@ -916,7 +916,10 @@ def q8_read_blocks(k, v, layout: Layout, code, block_start, block_table, cache, 
 
 def q8_append(k, v, layout: Layout, code, seq_lens, max_seq_len, tail_k, tail_v, block_table, cache, err, stream=None):
     """k, v: [B, Hkv, D] newest tokens (seq_lens counts them); tail_k/v:
-    [B, Hkv, capacity, D], capacity at least 15."""
+    [B, Hkv, capacity, D], capacity at least 15. Tokens drafted for a
+    verification: with n tokens appended, write them to rows n % 16 .. of the
+    tails, q8_decode with lengths n + Q - 1, then append the accepted ones, one
+    call each (sequences that accept fewer: length 0)."""
     what = "q8_append"
     kv_dtype = torch.bfloat16 if layout.kv_dtype == BF16 else torch.float16
     B, H, D = seq_lens.shape[0], layout.num_kv_heads, layout.head_dim

@@ -706,11 +706,12 @@ int32_t kvarn_rope(const kvarn_rope_tensor* tensors, int32_t num_tensors, int32_
  * v_bits = 8, rope_dim 0; norm_iters and scale_dtype are ignored. `code` of
  * every call on a cache is the same. Page of one KV head, 32 D + 32 bytes:
  *   [0, 16D)     K codes, one row of D bytes per token, whose 16-byte units
- *                sit at unit u XOR 4(token % 2); int8 codes plus 128
+ *                sit at unit u XOR 4(token % 2); int8 codes, of V too, plus 128
  *   [16D, 32D)   V codes: lane L = 4g + t owns one 32-bit word per 8-channel
  *                block nc, byte j + 2h of it channel 8nc + g of token 8h + 2t
  *                + j; the word sits at byte 16(32(nc/4) + L) + 4(nc%4)
- *   [32D, +4)    K scale fp32    [32D + 4, +4)  V scale    [32D + 8, +24) 0
+ *   [32D, +4)    K scale fp32    [32D + 4, +4)  V scale    [32D + 8, +24) not
+ *                used, left as they are
  *
  * kvarn_q8_encode_blocks writes, for every sequence b and u <
  * chunk_tokens / 16, tokens [16u, 16u + 16) of the chunk as logical block

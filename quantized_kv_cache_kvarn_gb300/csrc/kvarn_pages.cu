@@ -19,11 +19,11 @@
 // moves; the moves, beside the tables. A page's move is read and written once
 // (HBM bounds it), a hole is never a source, so moves need no order.
 //
-// Measured: 32 sequences of 16384 tokens that fork among four beams 12 us on
-// the GPU, 512 of an 8-bit cache of 1.3 million pages behind a window 22 us (41
-// MB), both bound by the three launches' latencies; 126 MB of pages moved (252
-// MB of traffic) 53 us, of which the moves 36 to 43, 0.9 of the measured copy
-// bandwidth and more.
+// Measured: 32 sequences of 2000 to 16384 tokens that fork among four beams 12
+// us on the GPU, 512 of an 8-bit cache of 1.3 million pages behind a window 21 us
+// (41 MB), both bound by the three launches' latencies; 126 MB of pages moved
+// (252 MB of traffic) 52 us, of which the moves 36 to 43, 0.9 of the measured
+// copy bandwidth and more.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -112,7 +112,8 @@ __device__ __forceinline__ int entry_of(const ForkParams& A, int a, int held, in
 }
 
 // Items of a warp: pieces of the tails, pieces of the table rows (with the
-// lengths), pieces of the counts, each item one chain of loads.
+// lengths), pieces of the counts, each item one chain of loads. Four CTAs an SM
+// leave it 64 registers, of which 56 bytes spill.
 __global__ void __launch_bounds__(kThreads, kCopyCtas) fork_copy_kernel(const __grid_constant__ ForkParams A) {
   pdl_wait_primary();
   pdl_launch_dependents();

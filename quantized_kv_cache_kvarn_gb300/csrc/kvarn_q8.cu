@@ -10,7 +10,9 @@
 // Bounded by HBM: 4 bytes read and 2 written per channel and token (K and V);
 // 4 x 4096 tokens of 8 bf16 heads of 128 written and read back take 32.5 us,
 // 0.92 of the measured copy bandwidth, 7 x 2032 tokens of 4 heads of 256 29 us,
-// 0.89. An append is one launch of 2.2 us, a warp per sequence, head and side.
+// 0.89. An append is one launch, a warp per sequence, head and side: replayed
+// from a graph 1.6 us for 32 sequences of 8 heads, 2.3 where all complete a
+// block, 2.6 and 6.1 for 512.
 #include "kvarn_launch.h"
 #include "kvarn_q8.cuh"
 

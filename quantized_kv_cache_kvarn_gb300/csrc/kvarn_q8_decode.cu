@@ -41,11 +41,11 @@
 // The raw tail (at most Q + 14 tokens a sequence) is done in fp32 without the
 // tensor cores: hidden tokens' values are never multiplied, whatever they are.
 //
-// Measured: 32 x 16384 tokens of 64/8 heads of 128 (1.08 GB) 174 us, 0.91 of
-// the measured copy bandwidth; 3 queries of 24/4 heads of 256 behind a window of
-// 4096 tokens, 32 sequences, 144 us: there two groups of rows read the pages and
-// dependent instructions at two warps a scheduler bound it (issue slots 40%,
-// tensor pipe 32%). What the compiler can not reorder is put in an order without
+// Measured: 32 x 16384 tokens of 64/8 heads of 128 (1.08 GB) 175 us, 0.91 of
+// the measured copy bandwidth, of 24/4 heads of 256 186; 3 queries of 24/4 heads
+// of 256 behind a window of 4096 tokens, 32 sequences of 2000 to 65536, 146 us:
+// there two groups of rows read the pages and dependent instructions at two warps
+// a scheduler bound it (issue slots 40%, tensor pipe 31%). What the compiler can not reorder is put in an order without
 // waits: the products are volatile statements, taken in turn into four
 // accumulators (one after another into the same one: 180 and 172 us).
 #include <math.h>
@@ -906,9 +906,11 @@ __global__ void __launch_bounds__(128) q8_merge_kernel(const __grid_constant__ Q
   if (A.lse && lane == 0) A.lse[row] = lse_of(M, L);
 }
 
-// Sixteen rows to a group wherever there are more than eight: 12 rows at
-// head_dim 256 behind a window take 92 us as one group of sixteen, 125 as two
-// of eight, 18 rows 143 as two and 166 as three, 16 rows at 128 143 and 205.
+// Sixteen rows to a group wherever there are more than eight. 32 sequences of
+// 24/4 heads of 256 behind a window of 4096 tokens: 2 queries (12 rows) 95 us as
+// one group of sixteen, 121 as two of eight; 3 queries (18 rows) 154 as two, 167
+// as three. 2 queries of 64/8 heads of 128 (16 rows) over 32 x 8192 tokens 139
+// and 185.
 int rows_per_group(int rows) { return rows > 8 ? 16 : 8; }
 
 template <int D, int R, int CODE>

@@ -41,13 +41,14 @@
 // The raw tail (at most Q + 14 tokens a sequence) is done in fp32 without the
 // tensor cores: hidden tokens' values are never multiplied, whatever they are.
 //
-// Measured: 32 x 16384 tokens of 64/8 heads of 128 (1.08 GB) 175 us, 0.91 of
+// Measured: 32 x 16384 tokens of 64/8 heads of 128 (1.08 GB) 174 us, 0.92 of
 // the measured copy bandwidth, of 24/4 heads of 256 186; 3 queries of 24/4 heads
-// of 256 behind a window of 4096 tokens, 32 sequences of 2000 to 65536, 146 us:
+// of 256 behind a window of 4096 tokens, 32 sequences of 2000 to 65536, 145 us:
 // there two groups of rows read the pages and dependent instructions at two warps
-// a scheduler bound it (issue slots 40%, tensor pipe 31%). What the compiler can not reorder is put in an order without
-// waits: the products are volatile statements, taken in turn into four
-// accumulators (one after another into the same one: 180 and 172 us).
+// a scheduler bound it (issue slots 40%, tensor pipe 31%). What the compiler can
+// not reorder is put in an order without waits: the products are volatile
+// statements, taken in turn into four accumulators (one after another into the
+// same one: 180 and 172 us, when the rest took 176 and 146).
 #include <math.h>
 
 #include <algorithm>
@@ -302,13 +303,18 @@ struct Rows {
   }
 
   // Two scores of a row to their weights for the sum, 2^(s - m), and for the
-  // output, 2^(s + ev - mt + kOff) vm with 2^ev vm the V scale; cm = -m and ct =
-  // (m - mt) + ev + kOff of the row: s - m comes first, so that scores of more
-  // than 24 bits lose nothing. The output's are below 2^(kOff + 1).
-  static __device__ __forceinline__ float2 weigh(float2 s, float cm, float ct, float vm, float2& sum) {
-    const float2 x = f2add(s, f2(cm)), y = f2add(x, f2(ct));
+  // output, 2^(s - mt + kOff) times the V scale, below 2^(kOff + 1); cm = -m. Next
+  // to scores of more than 24 bits fp32 has no room for kOff and the scale's
+  // exponent ev. With eight rows they come after s - m: ct = kOff + (m - mt) + ev,
+  // the factor is the scale's mantissa. With sixteen that wait shows, and they are
+  // in the factor but for what would leave 2^(s - mt) no room: ct = add - mt. (One
+  // way for both: 32 x 16384 tokens 175.0 us and window_verify 147.3, or 177.6 and
+  // 144.8; each its own 174.3 and 145.2.)
+  static constexpr bool kExponents = NR == 1;
+  static __device__ __forceinline__ float2 weigh(float2 s, float cm, float ct, float factor, float2& sum) {
+    const float2 x = f2add(s, f2(cm)), y = f2add(kExponents ? x : s, f2(ct));
     sum = f2add(sum, make_float2(ex2(x.x), ex2(x.y)));
-    return f2mul(make_float2(ex2(y.x), ex2(y.y)), f2(vm));
+    return f2mul(make_float2(ex2(y.x), ex2(y.y)), f2(factor));
   }
   // m and mt with 0 for a row that has seen nothing.
   __device__ __forceinline__ float base(float x) const { return x == -INFINITY ? 0.f : x; }
@@ -370,7 +376,7 @@ struct Rows {
   __device__ __forceinline__ void add_pages(const Q8Args& A, const unsigned char* pg0, const unsigned char* pg1, int half,
                                             const Seq& sq, int i0, int n, float (&s)[R]) {
     const int lane = threadIdx.x & 31, t = lane & 3;
-    float ev[2], vm[2];
+    float ev[2], add[2], factor[2];  // exponent of the V scale; its shares of weigh's ct and factor
     int first[2];
     bool edge = n < 2, bad[2];
 #pragma unroll
@@ -378,7 +384,15 @@ struct Rows {
       const uint32_t bits = *reinterpret_cast<const uint32_t*>((p ? pg1 : pg0) + q8_scales(D) + 4);
       ev[p] = static_cast<float>(static_cast<int>(bits >> 23) - 127);
       bad[p] = bits >= 0x7f800000u;  // not a scale: the block reads as NaN
-      vm[p] = bad[p] ? nan_f() : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+      if constexpr (kExponents) {
+        add[p] = ev[p];
+        factor[p] = bad[p] ? nan_f() : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+      } else {
+        // the largest share of a block has s - mt <= -ev: with the scales of 2^64 and more that is taken up again
+        const bool large = ev[p] >= 64.f;
+        add[p] = large ? 64.f : 0.f;
+        factor[p] = bad[p] ? nan_f() : __uint_as_float(bits) * (large ? 0x1p-52f : 0x1p12f);
+      }
       first[p] = p < n ? sq.block(i0 + p) * kPageTokens : 0;
       if (A.window > 0 && first[p] + kPageTokens > A.sinks && first[p] <= sq.L - 1 - A.window) edge = true;
     }
@@ -404,13 +418,13 @@ struct Rows {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       float2 sum = f2(0.f);
-      const float cm = -base(m[r]), ct = kOff + (base(m[r]) - base(mt[r]));
+      const float cm = -base(m[r]), ct = kExponents ? kOff + (base(m[r]) - base(mt[r])) : -base(mt[r]);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int x = 8 * r + 4 * p + 2 * e;
-          w[r][p][e] = weigh(make_float2(s[x], s[x + 1]), cm, ct + ev[p], vm[p], sum);
+          w[r][p][e] = weigh(make_float2(s[x], s[x + 1]), cm, ct + add[p], factor[p], sum);
         }
       l[r] += sum.x + sum.y;
     }
@@ -568,10 +582,10 @@ struct Rows {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       float2 sum = f2(0.f);
-      const float cm = -base(m[r]), ct = kOff + (base(m[r]) - base(mt[r]));
+      const float cm = -base(m[r]), ct = kExponents ? kOff + (base(m[r]) - base(mt[r])) : -base(mt[r]);
 #pragma unroll
       for (int x = 0; x < 4; x += 2) {
-        const float2 v = weigh(make_float2(w[r][x], w[r][x + 1]), cm, ct, 1.f, sum);
+        const float2 v = weigh(make_float2(w[r][x], w[r][x + 1]), cm, ct, kExponents ? 1.f : 0x1p12f, sum);
         w[r][x] = v.x;
         w[r][x + 1] = v.y;
       }

@@ -57,6 +57,19 @@ def test_raw_tails_of_any_size(lens, k_power, v_power, q_power, Hq, Hkv, D, Q):
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,Q", HEADS)
+@pytest.mark.parametrize("power", [-90, -40, 20, 71, 72, 73, 110])
+def test_a_block_of_other_values_than_the_rest(power, Hq, Hkv, D, Q):
+    """Values of one block a power of two of the others': the output is the sum of the shares, the larger ones' to what fp32
+    counts (a share of less than 2^-36 of the largest is within what the largest may be off by)."""
+    x = b8.Batch([160 + Q - 1, 77], Hq, Hkv, D, Q=Q, bf16=True, seed=11)
+    page = int(x.table[0, 4])
+    s = np.ascontiguousarray(x.cache[page, :, 32 * D + 4:32 * D + 8]).view(np.float32) * np.float32(2.0 ** power)
+    x.cache[page, :, 32 * D + 4:32 * D + 8] = s.view(np.uint8)
+    x.v[0][:, 64:80] *= 2.0 ** power
+    check(x.gpu(kv))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,Q", HEADS)
 @pytest.mark.parametrize("power", [20, 22, 24])
 @pytest.mark.parametrize("lens", [[320, 64], [13, 7], [333, 50]])
 def test_scores_beyond_what_fp32_counts(lens, power, Hq, Hkv, D, Q):

@@ -921,9 +921,9 @@ __global__ void __launch_bounds__(128) q8_merge_kernel(const __grid_constant__ Q
 }
 
 // Sixteen rows to a group wherever there are more than eight. 32 sequences of
-// 24/4 heads of 256 behind a window of 4096 tokens: 2 queries (12 rows) 95 us as
-// one group of sixteen, 121 as two of eight; 3 queries (18 rows) 154 as two, 167
-// as three. 2 queries of 64/8 heads of 128 (16 rows) over 32 x 8192 tokens 139
+// 24/4 heads of 256 behind a window of 4096 tokens: 2 queries (12 rows) 94 us as
+// one group of sixteen, 121 as two of eight; 3 queries (18 rows) 153 as two, 167
+// as three. 2 queries of 64/8 heads of 128 (16 rows) over 32 x 8192 tokens 138
 // and 185.
 int rows_per_group(int rows) { return rows > 8 ? 16 : 8; }
 
